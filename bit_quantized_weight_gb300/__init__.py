@@ -12,4 +12,6 @@ from .qgemv import (  # noqa: F401
     moe_qgemv_nvfp4_workspace_size, qdequant_nvfp4, qdequant_q45, qg_last_device_status,
     qg_status_string, qg_debug_set_wait, read_probe, GemvChain, qgemv_chain, QgGemvOp, qgemv_swiglu_q45,
     QG_FMT_NVFP4, QG_FMT_Q4, QG_FMT_Q5, QG_EPI_NONE, QG_EPI_RESIDUAL, QG_EPI_SWIGLU,
+    KVCache, KVBatch, kv_cache_append, kv_cache_read, kv_cache_accept, tree_attention,
+    tree_attention_workspace_size, QgKvCache, QgKvBatch, QG_KV_BF16, QG_KV_FP8, QG_KV_NVFP4,
 )

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -303,6 +304,62 @@ qg_status run_op(const qg_gemv_op& g, int M, cudaStream_t stream)
     return run_op_simple(g, M, stream);
 }
 
+// A cache and a batch of its sequences, checked and packed for the kernels.
+qg_status check_kv(const qg_kv_cache* c, const qg_kv_batch* b, KvArgs& a)
+{
+    if (!c || !b) return QG_ERR_INVALID_ARG;
+    if (c->format != QG_KV_BF16 && c->format != QG_KV_FP8 && c->format != QG_KV_NVFP4) return QG_ERR_INVALID_ARG;
+    if (c->num_pages < 1 || c->kv_heads < 1 || c->kv_heads > 1024 || c->head_dim < 1 || c->page_size < 16 ||
+        c->page_size > 1024 || c->page_size % 16)
+        return QG_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QG_ERR_UNSUPPORTED;
+    const bool scaled = c->format != QG_KV_BF16;
+    if (!c->k || !c->v || (c->k_scales != nullptr) != scaled || (c->v_scales != nullptr) != scaled)
+        return QG_ERR_INVALID_ARG;
+    if (scaled && !(std::isfinite(c->k_gscale) && c->k_gscale > 0.f && std::isfinite(c->v_gscale) &&
+                    c->v_gscale > 0.f))
+        return QG_ERR_INVALID_ARG;
+    if (b->n_seqs < 0 || b->n_seqs > kKvMaxSeqs || b->max_pages < 1 || b->n_tokens < 0 ||
+        b->n_tokens > kKvMaxTokens)
+        return QG_ERR_INVALID_ARG;
+    if (b->n_seqs && (!b->page_table || !b->seq_lens || !b->token_start)) return QG_ERR_INVALID_ARG;
+    const void* ptrs[] = {c->k, c->v, c->k_scales, c->v_scales, b->page_table, b->seq_lens, b->token_start};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return QG_ERR_MISALIGNED;
+    a.fmt = c->format;
+    a.num_pages = c->num_pages;
+    a.page_size = c->page_size;
+    a.heads = c->kv_heads;
+    a.dim = c->head_dim;
+    a.codes[0] = static_cast<uint8_t*>(c->k);
+    a.codes[1] = static_cast<uint8_t*>(c->v);
+    a.scales[0] = c->k_scales;
+    a.scales[1] = c->v_scales;
+    a.g[0] = scaled ? c->k_gscale : 1.f;
+    a.g[1] = scaled ? c->v_gscale : 1.f;
+    a.table = b->page_table;
+    a.lens = b->seq_lens;
+    a.start = b->token_start;
+    a.n_seqs = b->n_seqs;
+    a.max_pages = b->max_pages;
+    a.n_tokens = b->n_tokens;
+    a.status = nullptr;
+    return QG_OK;
+}
+
+// Nothing to do for a call without sequences or rows.
+bool empty_batch(const KvArgs& a) { return a.n_seqs == 0 || a.n_tokens == 0; }
+
+// The sizes tree_attention and its workspace query share; group = query heads
+// per key/value head.
+qg_status check_tree(int q_heads, int kv_heads, int max_tree, int& group)
+{
+    if (q_heads < 1 || q_heads % kv_heads || q_heads / kv_heads > 128 || max_tree < 1 || max_tree > 64)
+        return QG_ERR_INVALID_ARG;
+    group = q_heads / kv_heads;
+    return QG_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -491,6 +548,77 @@ qg_status qg_read_probe(const void* buf, size_t bytes, uint32_t* sink, cudaStrea
     if (bytes == 0) return QG_OK;
     if (!aligned16(buf) || (reinterpret_cast<uintptr_t>(sink) & 3u)) return QG_ERR_MISALIGNED;
     return launch_read_probe(buf, bytes, sink, stream);
+}
+
+qg_status kv_cache_append(const qg_kv_cache* cache, const qg_kv_batch* batch, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, cudaStream_t stream)
+{
+    KvArgs a;
+    qg_status s = check_kv(cache, batch, a);
+    if (s != QG_OK) return s;
+    if (empty_batch(a)) return QG_OK;
+    const int64_t row = static_cast<int64_t>(a.heads) * a.dim;
+    if (!k || !v || k_stride < row || v_stride < row) return QG_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || k_stride % 8 || v_stride % 8) return QG_ERR_MISALIGNED;
+    return launch_kv_append(a, k, k_stride, v, v_stride, stream);
+}
+
+qg_status kv_cache_read(const qg_kv_cache* cache, const qg_kv_batch* batch, void* k_out, void* v_out,
+                        qg_out out_dtype, cudaStream_t stream)
+{
+    KvArgs a;
+    qg_status s = check_kv(cache, batch, a);
+    if (s != QG_OK) return s;
+    if (out_dtype != QG_OUT_BF16 && out_dtype != QG_OUT_F32) return QG_ERR_INVALID_ARG;
+    if (empty_batch(a)) return QG_OK;
+    if (!k_out || !v_out) return QG_ERR_INVALID_ARG;
+    if (!aligned16(k_out) || !aligned16(v_out)) return QG_ERR_MISALIGNED;
+    return launch_kv_read(a, k_out, v_out, out_dtype == QG_OUT_F32, stream);
+}
+
+qg_status kv_cache_accept(const qg_kv_cache* cache, const qg_kv_batch* batch, const int32_t* path,
+                          const int32_t* n_accept, int32_t* new_lens, cudaStream_t stream)
+{
+    KvArgs a;
+    qg_status s = check_kv(cache, batch, a);
+    if (s != QG_OK) return s;
+    if (a.n_seqs == 0) return QG_OK;
+    if ((a.n_tokens && !path) || !n_accept) return QG_ERR_INVALID_ARG;
+    if (!aligned16(path) || !aligned16(n_accept) || !aligned16(new_lens)) return QG_ERR_MISALIGNED;
+    return launch_kv_accept(a, path, n_accept, new_lens, stream);
+}
+
+qg_status tree_attention_workspace_size(const qg_kv_cache* cache, int q_heads, int max_tree, size_t* bytes)
+{
+    if (!cache || !bytes || cache->kv_heads < 1 || cache->head_dim < 1) return QG_ERR_INVALID_ARG;
+    if (cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256) return QG_ERR_UNSUPPORTED;
+    int group = 0;
+    const qg_status s = check_tree(q_heads, cache->kv_heads, max_tree, group);
+    if (s != QG_OK) return s;
+    *bytes = tree_attention_workspace_bytes(cache->head_dim, group, max_tree);
+    return QG_OK;
+}
+
+qg_status tree_attention(const qg_kv_cache* cache, const qg_kv_batch* batch, const void* q, int64_t q_stride,
+                         int q_heads, int max_tree, const uint64_t* tree_mask, float scale, void* out, float* lse,
+                         void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    KvArgs a;
+    qg_status s = check_kv(cache, batch, a);
+    if (s != QG_OK) return s;
+    int group = 0;
+    s = check_tree(q_heads, a.heads, max_tree, group);
+    if (s != QG_OK) return s;
+    if (!std::isfinite(scale)) return QG_ERR_INVALID_ARG;
+    if (empty_batch(a)) return QG_OK;
+    if (!q || !out || q_stride < static_cast<int64_t>(q_heads) * a.dim) return QG_ERR_INVALID_ARG;
+    if (!aligned16(q) || q_stride % 8 || !aligned16(out) || !aligned16(lse) || !aligned16(tree_mask))
+        return QG_ERR_MISALIGNED;
+    if (!workspace || workspace_bytes < tree_attention_workspace_bytes(a.dim, group, max_tree))
+        return QG_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return QG_ERR_MISALIGNED;
+    return launch_tree_attention(a, static_cast<const uint16_t*>(q), q_stride, q_heads, max_tree, tree_mask, scale,
+                                 static_cast<uint16_t*>(out), lse, workspace, stream);
 }
 
 qg_status qg_last_device_status(cudaStream_t stream)

@@ -1,0 +1,62 @@
+// kv_common.cuh -- what the cache kernels (kv_cache.cu) and the attention over
+// the cache (tree_attention.cu) share: a call's sequences, the place of a
+// token in the pages, and the sizes of the three storage formats.
+#pragma once
+
+#include "common.cuh"
+
+namespace qg {
+
+// Bytes of one token's codes and scales of one head.
+__host__ __device__ constexpr int kv_row_bytes(int fmt, int dim)
+{
+    return fmt == QG_KV_BF16 ? 2 * dim : fmt == QG_KV_FP8 ? dim : dim / 2;
+}
+
+__host__ __device__ constexpr int kv_scale_bytes(int fmt, int dim)
+{
+    return fmt == QG_KV_BF16 ? 0 : fmt == QG_KV_FP8 ? 1 : dim / 16;
+}
+
+// Sequence b of a call: its rows [row0, row0 + rows) and the tokens the cache
+// held before. rows = 0 for a sequence whose entries do not fit (recorded).
+struct KvSeq {
+    int row0;
+    int rows;
+    int len;
+};
+
+__device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, int b, int max_rows)
+{
+    KvSeq s;
+    s.row0 = a.start[b];
+    const int end = a.start[b + 1];
+    s.len = a.lens[b];
+    s.rows = end - s.row0;
+    const bool ok = s.row0 >= 0 && end >= s.row0 && end <= a.n_tokens && s.len >= 0 && s.rows <= max_rows &&
+                    static_cast<int64_t>(s.len) + s.rows <= static_cast<int64_t>(a.max_pages) * a.page_size;
+    if (!ok) {
+        set_device_status(a.status, QG_ERR_INVALID_ARG);
+        s.rows = 0;
+    }
+    return s;
+}
+
+// The page of position p of sequence b, or -1 (recorded) if it lies outside
+// the cache.
+__device__ __forceinline__ int kv_page(const KvArgs& a, int b, int p)
+{
+    const int page = a.table[static_cast<int64_t>(b) * a.max_pages + p / a.page_size];
+    if (page >= 0 && page < a.num_pages) return page;
+    set_device_status(a.status, QG_ERR_INVALID_ARG);
+    return -1;
+}
+
+// Index of (page, head, position) among the cache's rows: rows * row bytes is
+// the offset of its codes (64 bits: a pool may pass 2^31 rows' bytes).
+__device__ __forceinline__ int64_t kv_row(const KvArgs& a, int page, int head, int p)
+{
+    return (static_cast<int64_t>(page) * a.heads + head) * a.page_size + p % a.page_size;
+}
+
+}  // namespace qg

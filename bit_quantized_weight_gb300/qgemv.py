@@ -24,6 +24,9 @@ QG_FMT_Q5 = 2
 QG_EPI_NONE = 0
 QG_EPI_RESIDUAL = 1
 QG_EPI_SWIGLU = 2
+QG_KV_BF16 = 0
+QG_KV_FP8 = 1
+QG_KV_NVFP4 = 2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_lib", "libqgemv.so")
@@ -43,6 +46,20 @@ class QgGemvOp(ctypes.Structure):
                 ("residual", ctypes.c_void_p), ("y", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p),
                 ("norm_eps", ctypes.c_float), ("up_format", ctypes.c_int), ("up_codes", ctypes.c_void_p),
                 ("up_q_hi", ctypes.c_void_p), ("up_scales", ctypes.c_void_p), ("up_mins", ctypes.c_void_p)]
+
+
+class QgKvCache(ctypes.Structure):
+    """qg_kv_cache of include/qgemv.h."""
+    _fields_ = [("format", ctypes.c_int), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("k_gscale", ctypes.c_float), ("v_gscale", ctypes.c_float)]
+
+
+class QgKvBatch(ctypes.Structure):
+    """qg_kv_batch of include/qgemv.h."""
+    _fields_ = [("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("token_start", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int), ("max_pages", ctypes.c_int), ("n_tokens", ctypes.c_int)]
 
 
 class QGemvError(RuntimeError):
@@ -78,6 +95,12 @@ def lib():
         L.qgemv_swiglu_q45.argtypes = [_P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _P, _P, _F, _P, _I, _I, _I, _P]
         L.qdequant_nvfp4.argtypes = [_P, _P, _F, _P, _I, _I, _P]
         L.qdequant_q45.argtypes = [_P, _P, _P, _P, _I, _P, _I, _I, _P]
+        pc, pb, i64 = ctypes.POINTER(QgKvCache), ctypes.POINTER(QgKvBatch), ctypes.c_int64
+        L.kv_cache_append.argtypes = [pc, pb, _P, i64, _P, i64, _P]
+        L.kv_cache_read.argtypes = [pc, pb, _P, _P, _I, _P]
+        L.kv_cache_accept.argtypes = [pc, pb, _P, _P, _P, _P]
+        L.tree_attention.argtypes = [pc, pb, _P, i64, _I, _I, _P, _F, _P, _P, _P, ctypes.c_size_t, _P]
+        L.tree_attention_workspace_size.argtypes = [pc, _I, _I, ctypes.POINTER(ctypes.c_size_t)]
         L.qg_last_device_status.argtypes = [_P]
         L.qg_read_probe.argtypes = [_P, ctypes.c_size_t, _P, _P]
         L.qg_status_string.argtypes = [_I]
@@ -86,7 +109,8 @@ def lib():
         for name in ("qgemv_nvfp4", "qgemv_q45", "qgemv_swiglu_nvfp4", "moe_route_topk",
                      "moe_qgemv_nvfp4_workspace_size", "moe_qgemv_nvfp4", "moe_qgemv_nvfp4_noalloc",
                      "qgemv_chain", "qgemv_chain_ws", "qgemv_chain_workspace_size", "qgemv_swiglu_q45",
-                     "qdequant_nvfp4",
+                     "kv_cache_append", "kv_cache_read", "kv_cache_accept", "tree_attention",
+                     "tree_attention_workspace_size", "qdequant_nvfp4",
                      "qdequant_q45", "qg_last_device_status", "qg_debug_set_wait"):
             getattr(L, name).restype = _I
         _lib = L
@@ -314,6 +338,196 @@ def qdequant_q45(q_lo, q_hi, scale, mn, bits, w, stream=None):
     _check("qdequant_q45", lib().qdequant_q45(_ptr(q_lo), _ptr(q_hi), _ptr(scale), _ptr(mn), int(bits),
                                               _ptr(w), N, K, _stream(stream, w)))
     return w
+
+
+_KV_FORMATS = {"bf16": QG_KV_BF16, "fp8": QG_KV_FP8, "nvfp4": QG_KV_NVFP4}
+
+
+def _kv_check(name, dtype, *ts):
+    for t in ts:
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}")
+
+
+class _OnDevice:
+    """The device of a call's tensors as the current one: nothing to do when
+    it is already, else it is switched for the call."""
+
+    def __init__(self, like, *others):
+        import torch
+        self.index = like.get_device()
+        for t in others:
+            if t is not None and t.get_device() != self.index:
+                raise ValueError("a call's tensors must be on one device")
+        self.guard = None if self.index == torch.cuda.current_device() else torch.cuda.device(self.index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+class KVCache:
+    """A paged key/value cache over the caller's tensors (qg_kv_cache): codes
+    k and v [pages][kv_heads][page_size][row], row = head_dim bf16 values
+    ("bf16"), head_dim bytes ("fp8") or head_dim/2 bytes ("nvfp4"), uint8;
+    scales uint8 [pages][kv_heads][page_size] ("fp8") or [...][head_dim/16]
+    ("nvfp4"), None for "bf16". The tensors must stay in place while the
+    cache is used; KVCache.empty allocates them."""
+
+    def __init__(self, fmt, k, v, k_scales=None, v_scales=None, k_gscale=1.0, v_gscale=1.0):
+        import torch
+        if fmt not in _KV_FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(_KV_FORMATS)}")
+        _cuda(k, v, k_scales, v_scales)
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must have one shape [pages][kv_heads][page_size][row]")
+        _kv_check("codes", torch.bfloat16 if fmt == "bf16" else torch.uint8, k, v)
+        pages, heads, page, row = k.shape
+        dim = row * 2 if fmt == "nvfp4" else row
+        want = {"bf16": None, "fp8": (pages, heads, page), "nvfp4": (pages, heads, page, dim // 16)}[fmt]
+        for t in (k_scales, v_scales):
+            if (None if t is None else tuple(t.shape)) != want:
+                raise ValueError(f"scales of a {fmt} cache must have shape {want}")
+        _kv_check("scales", torch.uint8, k_scales, v_scales)
+        self.fmt, self.head_dim, self.kv_heads, self.page_size = fmt, dim, heads, page
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        _OnDevice(k, v, k_scales, v_scales)
+        self.rec = QgKvCache(_KV_FORMATS[fmt], pages, page, heads, dim, _ptr(k), _ptr(v), _ptr(k_scales),
+                             _ptr(v_scales), float(k_gscale), float(v_gscale))
+        self.ref = ctypes.byref(self.rec)
+
+    @classmethod
+    def empty(cls, fmt, num_pages, page_size, kv_heads, head_dim, k_gscale=1.0, v_gscale=1.0, device="cuda"):
+        """A cache of zeros in new device memory."""
+        import torch
+        if fmt not in _KV_FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(_KV_FORMATS)}")
+        shape = (num_pages, kv_heads, page_size)
+        dt = torch.bfloat16 if fmt == "bf16" else torch.uint8
+        row = head_dim // 2 if fmt == "nvfp4" else head_dim
+        k, v = (torch.zeros(shape + (row,), dtype=dt, device=device) for _ in range(2))
+        if fmt == "bf16":
+            return cls(fmt, k, v)
+        tail = () if fmt == "fp8" else (head_dim // 16,)
+        ks, vs = (torch.full(shape + tail, 1 if fmt == "fp8" else 0, dtype=torch.uint8, device=device)
+                  for _ in range(2))
+        return cls(fmt, k, v, ks, vs, k_gscale, v_gscale)
+
+
+class KVBatch:
+    """The sequences of a call (qg_kv_batch): page_table int32 [n][max_pages],
+    seq_lens int32 [n], token_start int32 [n+1], all on the device, and the
+    rows of the call's token tensors, n_tokens. The tensors may change between
+    calls (a captured graph reads them at every replay) but not move."""
+
+    def __init__(self, page_table, seq_lens, token_start, n_tokens):
+        import torch
+        _cuda(page_table, seq_lens, token_start)
+        _kv_check("page_table, seq_lens and token_start", torch.int32, page_table, seq_lens, token_start)
+        n = seq_lens.shape[0]
+        if page_table.dim() != 2 or page_table.shape[0] != n or tuple(token_start.shape) != (n + 1,):
+            raise ValueError("page_table [n][max_pages], seq_lens [n] and token_start [n + 1] must agree")
+        _OnDevice(page_table, seq_lens, token_start)
+        self.page_table, self.seq_lens, self.token_start = page_table, seq_lens, token_start
+        self.n_seqs, self.n_tokens = n, int(n_tokens)
+        self.rec = QgKvBatch(_ptr(page_table), _ptr(seq_lens), _ptr(token_start), n, page_table.shape[1],
+                             self.n_tokens)
+        self.ref = ctypes.byref(self.rec)
+
+
+def _token_rows(name, t, batch, heads, dim):
+    """The token stride of a [n_tokens][heads][dim] bf16 tensor whose tokens
+    may lie apart (columns of a fused projection's output)."""
+    import torch
+    _kv_check(name, torch.bfloat16, t)
+    if not t.is_cuda or tuple(t.shape) != (batch.n_tokens, heads, dim):
+        raise ValueError(f"{name} must be a CUDA tensor [n_tokens][{heads}][{dim}]")
+    if batch.n_tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    return t.stride(0) if batch.n_tokens > 1 else heads * dim
+
+
+def kv_cache_append(cache, batch, k, v, stream=None):
+    """Quantise rows of k and v (bf16 [n_tokens][kv_heads][head_dim], tokens may
+    be strided) into their tokens' positions."""
+    ks = _token_rows("k", k, batch, cache.kv_heads, cache.head_dim)
+    vs = _token_rows("v", v, batch, cache.kv_heads, cache.head_dim)
+    with _OnDevice(cache.k, batch.seq_lens, k, v):
+        _check("kv_cache_append", lib().kv_cache_append(cache.ref, batch.ref, _ptr(k), ks, _ptr(v), vs,
+                                                        _stream(stream, cache.k)))
+
+
+def kv_cache_read(cache, batch, k_out, v_out, stream=None):
+    """The stored values of the batch's tokens into k_out and v_out
+    [n_tokens][kv_heads][head_dim] (both bf16 or both fp32)."""
+    import torch
+    _cuda(k_out, v_out)
+    want = (batch.n_tokens, cache.kv_heads, cache.head_dim)
+    if tuple(k_out.shape) != want or tuple(v_out.shape) != want:
+        raise ValueError(f"k_out and v_out must have shape {want}")
+    if k_out.dtype not in (torch.bfloat16, torch.float32) or v_out.dtype != k_out.dtype:
+        raise ValueError("k_out and v_out must both be bfloat16 or both float32")
+    out = QG_OUT_F32 if k_out.dtype == torch.float32 else QG_OUT_BF16
+    with _OnDevice(cache.k, batch.seq_lens, k_out, v_out):
+        _check("kv_cache_read", lib().kv_cache_read(cache.ref, batch.ref, _ptr(k_out), _ptr(v_out), out,
+                                                    _stream(stream, cache.k)))
+    return k_out, v_out
+
+
+def kv_cache_accept(cache, batch, path, n_accept, new_lens=None, stream=None):
+    """Move the accepted path of each sequence's drafts to the front of them
+    (path int32 [n_tokens], n_accept int32 [n]); new_lens int32 [n] receives
+    the sequences' new lengths and may be the batch's seq_lens."""
+    import torch
+    _cuda(path, n_accept, new_lens)
+    _kv_check("path, n_accept and new_lens", torch.int32, path, n_accept, new_lens)
+    if tuple(path.shape) != (batch.n_tokens,) or tuple(n_accept.shape) != (batch.n_seqs,) or (
+            new_lens is not None and tuple(new_lens.shape) != (batch.n_seqs,)):
+        raise ValueError("path [n_tokens], n_accept [n_seqs] and new_lens [n_seqs] must agree with the batch")
+    with _OnDevice(cache.k, batch.seq_lens, path, n_accept, new_lens):
+        _check("kv_cache_accept", lib().kv_cache_accept(cache.ref, batch.ref, _ptr(path), _ptr(n_accept),
+                                                        _ptr(new_lens), _stream(stream, cache.k)))
+    return new_lens
+
+
+def tree_attention_workspace_size(cache, q_heads, max_tree) -> int:
+    b = ctypes.c_size_t(0)
+    with _OnDevice(cache.k):
+        _check("tree_attention_workspace_size",
+               lib().tree_attention_workspace_size(cache.ref, int(q_heads), int(max_tree), ctypes.byref(b)))
+    return b.value
+
+
+def tree_attention(cache, batch, q, out, max_tree, tree_mask=None, scale=None, lse=None, workspace=None, stream=None):
+    """Attention of the batch's drafted tokens (already appended) over the
+    cache: q bf16 [n_tokens][q_heads][head_dim] (tokens may be strided), out
+    bf16 of that shape, tree_mask int64 [n_tokens] of 64 bits (None: chains),
+    lse fp32 [n_tokens][q_heads] or None; scale defaults to 1/sqrt(head_dim).
+    workspace: a uint8 tensor of tree_attention_workspace_size bytes."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError("q must be [n_tokens][q_heads][head_dim]")
+    heads, dim = q.shape[1], cache.head_dim
+    qs = _token_rows("q", q, batch, heads, dim)
+    _cuda(out, tree_mask, lse, workspace)
+    _kv_check("out", torch.bfloat16, out)
+    _kv_check("tree_mask", torch.int64, tree_mask)
+    _kv_check("lse", torch.float32, lse)
+    if tuple(out.shape) != tuple(q.shape) or (tree_mask is not None and tuple(tree_mask.shape) != (batch.n_tokens,)) \
+            or (lse is not None and tuple(lse.shape) != (batch.n_tokens, heads)):
+        raise ValueError("out, tree_mask and lse must agree with q")
+    if scale is None:
+        scale = dim ** -0.5
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _OnDevice(cache.k, batch.seq_lens, q, out, tree_mask, lse, workspace):
+        _check("tree_attention", lib().tree_attention(
+            cache.ref, batch.ref, _ptr(q), qs, heads, int(max_tree), _ptr(tree_mask), float(scale), _ptr(out),
+            _ptr(lse), _ptr(workspace), nbytes, _stream(stream, cache.k)))
+    return out
 
 
 def read_probe(buf, sink, stream=None):

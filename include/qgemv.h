@@ -343,11 +343,165 @@ QG_API qg_status qdequant_q45(const uint8_t* q_lo, const uint8_t* q_hi, const vo
  */
 QG_API qg_status qg_read_probe(const void* buf, size_t bytes, uint32_t* sink, cudaStream_t stream);
 
+/* ------------------------------------------------------------------ cache and attention of a decode step */
+
+/* How a cache holds its keys and values. */
+typedef enum { QG_KV_BF16 = 0, QG_KV_FP8 = 1, QG_KV_NVFP4 = 2 } qg_kv_format;
+
+/*
+ * A paged key/value cache in caller-owned device memory (NInfer article,
+ * section 4: a low-precision KV cache in pages of 64 tokens, BF16, FP8-E4M3
+ * or NVFP4; Decapybara README, decode_ops.cu: microscaled FP8 KV). A page
+ * holds page_size consecutive tokens of one sequence, each key/value head
+ * apart: codes [num_pages][kv_heads][page_size][row bytes].
+ *   QG_KV_BF16   row = head_dim bf16 values, no scales
+ *   QG_KV_FP8    row = head_dim E4M3 codes; scales u8
+ *                [num_pages][kv_heads][page_size], one byte s in 1..22 per
+ *                token and head; value = e4m3(code) * 2^(s-15) * g
+ *   QG_KV_NVFP4  row = head_dim/2 bytes, two E2M1 codes each, the low nibble
+ *                holding the even index; scales u8
+ *                [num_pages][kv_heads][page_size][head_dim/16] (E4M3);
+ *                value = e2m1(code) * e4m3(scale) * g
+ * with g = k_gscale or v_gscale, by value (finite and positive; ignored for
+ * QG_KV_BF16). code times scale is an f16 number in every format, so nothing
+ * that reads the cache rounds it.
+ *   page_size   a multiple of 16, 16..1024
+ *   head_dim    64, 128 or 256 (else QG_ERR_UNSUPPORTED)
+ *   kv_heads    1..1024
+ *   k, v        codes; k_scales, v_scales NULL for QG_KV_BF16
+ */
+typedef struct {
+    int format;
+    int num_pages;
+    int page_size;
+    int kv_heads;
+    int head_dim;
+    void* k;
+    void* v;
+    uint8_t* k_scales;
+    uint8_t* v_scales;
+    float k_gscale;
+    float v_gscale;
+} qg_kv_cache;
+
+/*
+ * The sequences of one call and their tokens, packed: sequence b has rows
+ * token_start[b] .. token_start[b+1] - 1 of the call's token tensors, which
+ * stand at the positions seq_lens[b], seq_lens[b] + 1, ... of that sequence;
+ * position p lies in page page_table[b][p / page_size]. The arrays are DEVICE
+ * data (a captured graph replays with new lengths); sizes are by value.
+ *   page_table   int32 [n_seqs][max_pages]; entries past a sequence's last
+ *                position are not read
+ *   seq_lens     int32 [n_seqs], tokens in the cache before this call's
+ *   token_start  int32 [n_seqs + 1], ascending, the last at most n_tokens
+ *   n_seqs       0..1024     max_pages >= 1     n_tokens 0..2^24 (rows)
+ * Rows behind the last sequence are neither read nor written. A sequence
+ * whose entries do not fit (a negative length, rows outside n_tokens,
+ * positions beyond max_pages * page_size) is left out, and so is a token
+ * whose page lies outside the cache; each records QG_ERR_INVALID_ARG in the
+ * device status word. (Where token_start does not ascend, rows that two
+ * sequences claim may be left out with the one that does not fit.) Sequences
+ * may share pages that a call only reads; a position that a call writes
+ * belongs to one sequence.
+ */
+typedef struct {
+    const int32_t* page_table;
+    const int32_t* seq_lens;
+    const int32_t* token_start;
+    int n_seqs;
+    int max_pages;
+    int n_tokens;
+} qg_kv_batch;
+
+/*
+ * Quantise keys and values as they are written: row i of k and v (all heads)
+ * goes to its token's position. With y = fp32_rne(x / g):
+ *   QG_KV_FP8    s = the smallest of 1..22 with max|y| <= 448 * 2^(s-15) over
+ *                the head's values (22 if none), code = e4m3_rne(y * 2^(15-s))
+ *   QG_KV_NVFP4  scale = e4m3_rne(fp32_rne(max|y| / 6)) over 16 values,
+ *                code = e2m1_rne(fp32_rne(y / scale)), 0 for scale 0
+ * Ties go to the even code and what is too large saturates, infinities too.
+ * A NaN is left out of an FP8 maximum and stays NaN; an NVFP4 block that
+ * holds one gets a NaN scale.
+ *   k, v      bf16, row i at k + i * k_stride: kv_heads * head_dim values, so
+ *             they may be columns of a fused projection's output
+ *   k_stride, v_stride   elements, >= kv_heads * head_dim, multiples of 8
+ *             (else QG_ERR_MISALIGNED)
+ */
+QG_API qg_status kv_cache_append(const qg_kv_cache* cache, const qg_kv_batch* batch, const void* k, int64_t k_stride,
+                                 const void* v, int64_t v_stride, cudaStream_t stream);
+
+/*
+ * Read tokens back: the inverse of kv_cache_append, row i of k_out and v_out
+ * [n_tokens][kv_heads][head_dim] = the values stored at its token's position,
+ * one fp32 rounding of (code * scale) * g, then bf16_rne for QG_OUT_BF16. A
+ * token whose page lies outside the cache reads as zeros.
+ */
+QG_API qg_status kv_cache_read(const qg_kv_cache* cache, const qg_kv_batch* batch, void* k_out, void* v_out,
+                               qg_out out_dtype, cudaStream_t stream);
+
+/*
+ * Keep the accepted path of a drafted tree: the call's tokens of sequence b
+ * stand at seq_lens[b] + j; for i < n_accept[b] position seq_lens[b] + i
+ * receives what stood at position seq_lens[b] + path[token_start[b] + i],
+ * codes and scales unchanged, and new_lens[b] = seq_lens[b] + n_accept[b].
+ *   path      int32 [n_tokens], rows as the tokens'; per sequence ascending,
+ *             i <= path[i] < the sequence's tokens
+ *   n_accept  int32 [n_seqs], 0 .. the sequence's tokens
+ *   new_lens  int32 [n_seqs] or NULL; may be seq_lens itself
+ * A sequence that breaks these, or a page outside the cache in what it moves,
+ * leaves that sequence unmoved with new_lens[b] = seq_lens[b] and records
+ * QG_ERR_INVALID_ARG in the device status word.
+ */
+QG_API qg_status kv_cache_accept(const qg_kv_cache* cache, const qg_kv_batch* batch, const int32_t* path,
+                                 const int32_t* n_accept, int32_t* new_lens, cudaStream_t stream);
+
+/*
+ * Attention of drafted tokens over the cache (NInfer article, section 3: one
+ * step verifies a lane's drafts; a plain decode step is a tree of one). The
+ * call's tokens are already in the cache (kv_cache_append with the same
+ * batch). Token j of sequence b sees every position below seq_lens[b] and,
+ * of the sequence's own tokens, those whose bits are set in its mask:
+ *   out[i][h] = bf16_rne( sum_p softmax_p(scale * q[i][h] . K[p][h/G]) V[p][h/G] )
+ *   lse[i][h] = ln sum_p exp(scale * q[i][h] . K[p][h/G]),   G = q_heads / kv_heads
+ * over the positions p it sees; a token that sees nothing gets zeros and
+ * -infinity. What stands in places that a token does not see never reaches
+ * it, infinities and NaN included.
+ *   q          bf16, row i at q + i * q_stride: q_heads * head_dim values;
+ *              q_stride in elements, a multiple of 8
+ *   q_heads    a multiple of kv_heads, at most 128 * kv_heads
+ *   max_tree   1..64, the largest number of tokens of a sequence of this
+ *              call; a sequence that has more is left out, with
+ *              QG_ERR_INVALID_ARG in the device status word
+ *   tree_mask  uint64 [n_tokens], bit j: sees its sequence's token j (its own
+ *              bit included: nothing is implied); NULL: token j sees the
+ *              tokens 0..j, a chain
+ *   scale      finite
+ *   out        bf16 [n_tokens][q_heads][head_dim]
+ *   lse        fp32 [n_tokens][q_heads] or NULL
+ *   workspace  device memory of at least tree_attention_workspace_size()
+ *              bytes, 256-byte aligned; needs no initialisation, is scratch
+ *              after the call, and may be shared by calls that do not overlap
+ *              on the GPU
+ * Products of q and K and of the softmax weights and V accumulate in fp32;
+ * the weights enter the second product as f16 (bf16 for QG_KV_BF16). Keys in a
+ * page outside the cache are not seen. The result does not depend on the
+ * stream's other work (fixed order, no atomics).
+ */
+QG_API qg_status tree_attention(const qg_kv_cache* cache, const qg_kv_batch* batch, const void* q, int64_t q_stride,
+                                int q_heads, int max_tree, const uint64_t* tree_mask, float scale, void* out,
+                                float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of tree_attention's workspace on the current device for any batch of
+ * this cache, these heads and max_tree. */
+QG_API qg_status tree_attention_workspace_size(const qg_kv_cache* cache, int q_heads, int max_tree, size_t* bytes);
+
 /*
  * Synchronise `stream`, then return and clear the device status word:
  * QG_OK, QG_ERR_DEVICE_TIMEOUT when a bounded device-side wait gave up (the
  * kernel stopped early; its outputs are undefined), or QG_ERR_INVALID_ARG for
- * out-of-range device data (MoE expert ids).
+ * out-of-range device data (MoE expert ids, a cache batch's lengths, pages and
+ * paths).
  */
 QG_API qg_status qg_last_device_status(cudaStream_t stream);
 
