@@ -1,94 +1,843 @@
-// tree_attention.cu -- attention of drafted tokens over the paged cache.
-#include "kv_common.cuh"
+// tree_attention.cu -- attention of drafted tokens over the paged cache on
+// warp-level MMA, and the kernel that joins a unit's parts.
+//
+// out = softmax(scale q K^T) V over a cache that is read once: what bounds it
+// is the cache's bytes. Each warp walks its own blocks of keys with its own
+// running maximum and sum (no barrier between warps until a unit ends), its
+// keys and values arriving through a ring of cp.async copies in which every
+// lane fetches exactly the bytes that it will feed to its MMA fragments:
+//   * m16n8k16 wants, for the keys (B operand of q K^T), two pairs of values
+//     along head_dim per lane and key, and sums do not care in which order
+//     head_dim is walked: lane (g, c) takes 16 bytes at 16 c (+ 64 u) of key g
+//     and uses them in order, q being laid out to match;
+//   * for the values (B operand of P V), pairs of keys per lane and column:
+//     lane (g, c) takes 16 bytes at 16 g (+ 128 p) of the keys 2c, 2c + 1,
+//     2c + 8, 2c + 9, so that its columns are bytes of its own registers, and
+//     pairs up two keys' bytes with byte permutes before the conversion.
+// Nothing is transposed through shared memory and no lane reads another's copy
+// (block scales apart).
+#include <type_traits>
+
+#include "tree_common.cuh"
 
 namespace qg {
 namespace {
 
-// One warp per (row, query head): the running maximum and sum of a softmax,
-// one key at a time.
-__global__ void __launch_bounds__(256) tree_simple_kernel(KvArgs a, const uint16_t* q, int64_t q_stride, int q_heads,
-                                                          int max_tree, const uint64_t* mask, float scale,
-                                                          uint16_t* out, float* lse)
+constexpr int kMmaWarps = 4;
+constexpr int kMmaThreads = 32 * kMmaWarps;
+constexpr float kOffset = 7.f;   // weights are 2^(s - m + 7): f16 keeps 11 bits down to 2^-21 of the largest
+constexpr float kLazy = 8.f;     // ... and a maximum is replaced only once it is passed by 2^8 (2^15 < 65504)
+
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+// Sizes of a format's rows as the lanes fetch them.
+template <int FMT, int D>
+struct Lay {
+    static constexpr int kRow = kv_row_bytes(FMT, D);
+    static constexpr int kScale = kv_scale_bytes(FMT, D);
+    static constexpr int kPerByteX2 = FMT == QG_KV_BF16 ? 1 : FMT == QG_KV_FP8 ? 2 : 4;  // values per 2 bytes
+    static constexpr int kKB = kRow / 4 < 16 ? kRow / 4 : 16;    // bytes of a key piece
+    static constexpr int kKP = kRow / 4 / kKB;                   // pieces per lane and key
+    static constexpr int kKE = kKB * kPerByteX2 / 2;             // values of a key piece
+    static constexpr int kVB = kRow / 8 < 16 ? kRow / 8 : 16;    // the same for values
+    static constexpr int kVP = kRow / 8 / kVB;
+    static constexpr int kVE = kVB * kPerByteX2 / 2;
+    // keys per block (16 or 32): a block's bytes stay within 8 KB
+    static constexpr int kGroups = kRow <= 128 ? 2 : 1;
+    static constexpr int kKeys = 16 * kGroups;
+    static constexpr int kKBytes = kKeys * kRow;
+    static constexpr int kSBytes = kKeys * kScale;
+    static constexpr int kStage = 2 * (kKBytes + kSBytes);
+};
+
+template <int FMT, int D, int RT>
+struct MmaPlan {
+    using L = Lay<FMT, D>;
+    static constexpr int kRows = 16 * RT;
+    static constexpr int kStep = kMmaWarps * L::kKeys;
+    static constexpr int kQ = RT * D * 32;                       // bytes of q fragments
+    static constexpr int kHead = kQ + kRows * 16;                // + masks, exponents
+    // two CTAs per SM, one where three blocks per warp do not fit beside each other
+    static constexpr int kCtas = kHead + 3 * kMmaWarps * L::kStage <= 112 * 1024 ? 2 : 1;
+    static constexpr int kBudget = (kCtas == 2 ? 112 : 224) * 1024 - kHead;
+    static constexpr int kFit = kBudget / (kMmaWarps * L::kStage);
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
+    static constexpr int kRing = kMmaWarps * kStages * L::kStage;
+    static constexpr int kJoin = kMmaWarps * kRows * (D + 4) * 4 + kMmaWarps * kRows * 8;
+    static constexpr int kPrefix = (kKvMaxSeqs + 1) * 8;
+    static constexpr int kBoth = kRing > kJoin ? kRing : kJoin;
+    static constexpr int kBody = kBoth > kPrefix ? kBoth : kPrefix;
+    static constexpr int kSmem = kHead + kBody;
+    static_assert(kStages >= 3, "ring too short");
+};
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool on)
 {
-    pdl_enter();
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int row = static_cast<int>(unit / q_heads), h = static_cast<int>(unit % q_heads);
-    if (row >= a.n_tokens) return;
-    int b = 0;
-    KvSeq s{};
-    for (; b < a.n_seqs; ++b) {
-        s = kv_seq(a, b, max_tree);
-        if (row >= s.row0 && row - s.row0 < s.rows) break;
+    const int n = on ? BYTES : 0;                                // 0: zeros, nothing is read
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n)
+                     : "memory");
+}
+
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// `BYTES` of this lane's copy as words.
+template <int BYTES>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[BYTES / 4])
+{
+    if constexpr (BYTES == 16) {
+        const uint4 v = lds128(addr);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    } else if constexpr (BYTES == 8) {
+        const uint2 v = lds64(addr);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        w[0] = lds32(addr);
     }
-    if (b == a.n_seqs) return;
-    const int n = a.dim / 32;
-    float qf[8], acc[8];
-    for (int i = 0; i < n; ++i) {
-        qf[i] = bf16_bits_to_f32(q[row * q_stride + h * a.dim + lane * n + i]);
-        acc[i] = 0.f;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1)
+{
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Zeroes each 16-bit half that is infinite or NaN.
+template <bool BF16>
+__device__ __forceinline__ uint32_t finite_halves(uint32_t x)
+{
+    const uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
+    if ((x & e) == e) x &= 0xFFFF0000u;
+    if (((x >> 16) & e) == e) x &= 0x0000FFFFu;
+    return x;
+}
+
+// Values of a key piece: the pairs that k-step w of the piece feeds to the MMA.
+template <int FMT, int WORDS>
+__device__ __forceinline__ void key_pair(const uint32_t (&r)[WORDS], int w, const uint32_t (&sc)[2], uint32_t& b0,
+                                         uint32_t& b1)
+{
+    if constexpr (FMT == QG_KV_BF16) {
+        b0 = r[2 * w];
+        b1 = r[2 * w + 1];
+    } else if constexpr (FMT == QG_KV_FP8) {
+        b0 = e4m3x2_to_f16x2(r[w] & 0xFFFFu);
+        b1 = e4m3x2_to_f16x2(r[w] >> 16);
+    } else {
+        const uint32_t x = r[w / 2] >> (16 * (w & 1));
+        b0 = hmul2(e2m1x2_to_f16x2(x & 0xFFu), sc[w / 4]);
+        b1 = hmul2(e2m1x2_to_f16x2((x >> 8) & 0xFFu), sc[w / 4]);
     }
-    const int j = row - s.row0, head = h / (q_heads / a.heads);
-    const uint64_t bits = mask ? mask[row] : (2ull << j) - 1;
-    float m = -INFINITY, l = 0.f;
-    const int rb = kv_row_bytes(a.fmt, a.dim), sb = kv_scale_bytes(a.fmt, a.dim);
-    for (int p = 0; p < s.len + s.rows; ++p) {
-        if (p >= s.len && !((bits >> (p - s.len)) & 1)) continue;
-        const int page = kv_page(a, b, p);
-        if (page < 0) continue;
-        const int64_t r = kv_row(a, page, head, p);
-        float kf[2][8];
-        for (int kv = 0; kv < 2; ++kv)
-            for (int i = 0; i < n; ++i) {
-                const int d = lane * n + i;
-                const uint8_t* c = a.codes[kv] + r * rb;
-                float v;
-                if (a.fmt == QG_KV_BF16) {
-                    v = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(c)[d]);
-                } else if (a.fmt == QG_KV_FP8) {
-                    v = half_bits_to_f32(e4m3x2_to_f16x2(c[d]) & 0xFFFFu) *
-                        half_bits_to_f32(static_cast<uint32_t>(a.scales[kv][r]) << 10) * a.g[kv];
-                } else {
-                    v = half_bits_to_f32(e2m1x2_to_f16x2(c[d / 2] >> (4 * (d & 1)) & 15) & 0xFFFFu) *
-                        half_bits_to_f32(e4m3x2_to_f16x2(a.scales[kv][r * sb + d / 16]) & 0xFFFFu) * a.g[kv];
-                }
-                kf[kv][i] = v;
+}
+
+// Values of two keys' pieces side by side: word i holds elements of both; out
+// gets one f16x2 / bf16x2 (key 0 low, key 1 high) per element, in order.
+template <int FMT>
+__device__ __forceinline__ void value_pairs(uint32_t w0, uint32_t w1, uint32_t sc,
+                                            uint32_t (&out)[FMT == QG_KV_BF16 ? 2 : FMT == QG_KV_FP8 ? 4 : 8])
+{
+    if constexpr (FMT == QG_KV_BF16) {
+        out[0] = __byte_perm(w0, w1, 0x5410);
+        out[1] = __byte_perm(w0, w1, 0x7632);
+    } else if constexpr (FMT == QG_KV_FP8) {
+        const uint32_t x = __byte_perm(w0, w1, 0x5140), y = __byte_perm(w0, w1, 0x7362);
+        out[0] = hmul2(e4m3x2_to_f16x2(x & 0xFFFFu), sc);
+        out[1] = hmul2(e4m3x2_to_f16x2(x >> 16), sc);
+        out[2] = hmul2(e4m3x2_to_f16x2(y & 0xFFFFu), sc);
+        out[3] = hmul2(e4m3x2_to_f16x2(y >> 16), sc);
+    } else {
+        const uint32_t even = (w0 & 0x0F0F0F0Fu) | ((w1 & 0x0F0F0F0Fu) << 4);
+        const uint32_t odd = ((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u);
+        uint32_t e[4], o[4];
+        e2m1x8_to_f16x2x4(even, e);
+        e2m1x8_to_f16x2x4(odd, o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            out[2 * i] = hmul2(e[i], sc);
+            out[2 * i + 1] = hmul2(o[i], sc);
+        }
+    }
+}
+
+// One warp's side of a unit: where its keys stand and what its ring holds.
+struct Walk {
+    int b, head;
+    int first, end;              // the segment's keys
+    int len, keys;               // context and all keys of the sequence
+    int n;                       // this warp's blocks
+};
+
+template <int FMT, int D, int RT>
+__global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_mma_kernel(const __grid_constant__ TreeArgs t)
+{
+    using L = Lay<FMT, D>;
+    using P = MmaPlan<FMT, D, RT>;
+    constexpr bool kBf16 = FMT == QG_KV_BF16;
+    constexpr int kNT = 2 * L::kGroups;              // key tiles of 8 per block
+    constexpr int kOT = D / 8;                       // output tiles of 8 columns
+    constexpr int kSteps = L::kKE / 4;               // k-steps per key piece
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint4* q_frag = reinterpret_cast<uint4*>(smem);
+    uint64_t* row_mask = reinterpret_cast<uint64_t*>(smem + P::kQ);
+    int* row_exp = reinterpret_cast<int*>(smem + P::kQ + P::kRows * 8);
+    uint8_t* body = smem + P::kHead;
+    const KvArgs& a = t.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, c = lane & 3;
+
+    // Predecessors are complete after the wait, so the joining kernel, which
+    // starts early, may read the batch as soon as it is launched.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int64_t* prefix = reinterpret_cast<int64_t*>(body);
+    tree_prefix(t, prefix);
+    __syncthreads();
+    const int64_t total = prefix[a.n_seqs];
+    const int64_t chunk = tree_chunk(total, t.grid);
+    const int64_t cta_first = blockIdx.x * chunk;
+    const int64_t cta_end = min(total, cta_first + chunk);
+    if (cta_first >= cta_end) return;
+    int b = tree_find(prefix, a.n_seqs, cta_first);
+    int64_t base = prefix[b];                        // first step of sequence b
+    __syncthreads();                                 // the ring takes the prefix sums' place
+
+    const uint32_t ring = smem_u32(body) + warp * (P::kStages * L::kStage);
+    int64_t at = cta_first;
+    while (at < cta_end) {
+        TreeSeq u = tree_seq(t, b);
+        int64_t w = static_cast<int64_t>(u.steps) * u.tiles * a.heads;
+        while (at >= base + w) {
+            base += w;
+            ++b;
+            u = tree_seq(t, b);
+            w = static_cast<int64_t>(u.steps) * u.tiles * a.heads;
+        }
+        const int unit = static_cast<int>((at - base) / u.steps);
+        const int s0 = static_cast<int>((at - base) % u.steps);
+        const int s1 = static_cast<int>(min(static_cast<int64_t>(u.steps), s0 + (cta_end - at)));
+        const int head = unit / u.tiles, tile = unit % u.tiles;
+        Walk k;
+        k.b = b;
+        k.head = head;
+        k.first = s0 * P::kStep;
+        k.end = min(u.keys, s1 * P::kStep);
+        k.len = u.s.len;
+        k.keys = u.keys;
+        const int blocks = (k.end - k.first + L::kKeys - 1) / L::kKeys;
+        k.n = blocks > warp ? (blocks - warp - 1) / kMmaWarps + 1 : 0;
+        const int row0 = tile * P::kRows;
+        const int n_rows = min(P::kRows, u.s.rows * t.group - row0);
+
+        // ---- the ring
+        uint32_t bad = 0;                            // per ring place: groups whose page lies outside the cache
+        int page_next[L::kGroups];
+        auto look_up = [&](int i) {
+#pragma unroll
+            for (int s = 0; s < L::kGroups; ++s) {
+                const int p = k.first + (warp + i * kMmaWarps) * L::kKeys + 16 * s;
+                page_next[s] = i < k.n && p < k.end ? kv_page(a, b, p) : -2;
             }
-        float dot = 0.f;
-        for (int i = 0; i < n; ++i) dot += qf[i] * kf[0][i];
-        for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        dot *= scale;
-        const float mn = fmaxf(m, dot), f = expf(m - mn), w = expf(dot - mn);
-        l = l * f + w;
-        for (int i = 0; i < n; ++i) acc[i] = acc[i] * f + w * kf[1][i];
-        m = mn;
+        };
+        auto issue = [&](int i) {
+            const int place = i % P::kStages;
+            const uint32_t dst = ring + place * L::kStage;
+            bad &= ~(3u << (2 * place));
+            if (i < k.n) {
+#pragma unroll
+                for (int s = 0; s < L::kGroups; ++s) {
+                    const int p = k.first + (warp + i * kMmaWarps) * L::kKeys + 16 * s;
+                    const int page = page_next[s];
+                    if (page == -1) bad |= 1u << (2 * place + s);
+                    const int64_t row = kv_row(a, max(page, 0), head, p);
+                    const uint8_t* kp = a.codes[0] + row * L::kRow;
+                    const uint8_t* vp = a.codes[1] + row * L::kRow;
+                    const int left = page >= 0 ? k.end - p : 0;    // keys of this group
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int x = 0; x < L::kKP; ++x)
+                            cp_async<L::kKB>(dst + (((2 * s + j) * L::kKP + x) * 32 + lane) * L::kKB,
+                                             kp + (8 * j + g) * L::kRow + x * 4 * L::kKB + c * L::kKB,
+                                             8 * j + g < left);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int key = 2 * c + (y & 1) + 8 * (y >> 1);
+#pragma unroll
+                        for (int x = 0; x < L::kVP; ++x)
+                            cp_async<L::kVB>(dst + L::kKBytes + (((4 * s + y) * L::kVP + x) * 32 + lane) * L::kVB,
+                                             vp + key * L::kRow + x * 8 * L::kVB + g * L::kVB, key < left);
+                    }
+                    if constexpr (L::kScale > 0) {
+                        // 16 keys' scales are kScale pieces of 16 bytes
+                        const uint32_t sd = dst + 2 * L::kKBytes + 16 * s * L::kScale;
+                        if (lane < 2 * L::kScale) {
+                            const int kv = lane >= L::kScale, x = lane - kv * L::kScale;
+                            cp_async<16>(sd + kv * L::kSBytes + x * 16, a.scales[kv] + row * L::kScale + x * 16,
+                                         left > 0);
+                        }
+                    }
+                }
+            }
+            cp_commit();
+        };
+        look_up(0);
+#pragma unroll
+        for (int i = 0; i < P::kStages - 1; ++i) {
+            issue(i);
+            look_up(i + 1);
+        }
+
+        // ---- q as MMA fragments, scaled to f16's range by a power of two per row
+        for (int r = warp; r < P::kRows; r += kMmaWarps) {
+            const int tok = (row0 + r) / t.group, qh = head * t.group + (row0 + r) % t.group;
+            constexpr int kPer = D / 32 < 4 ? 4 : D / 32;      // values per lane
+            uint32_t w2[kPer / 2] = {};
+            const bool on = r < n_rows && lane * kPer < D;
+            if (on) {
+                const uint16_t* src = t.q + (u.s.row0 + tok) * t.q_stride + qh * D + lane * kPer;
+#pragma unroll
+                for (int i = 0; i < kPer / 2; ++i) w2[i] = reinterpret_cast<const uint32_t*>(src)[i];
+            }
+            int pe = 0;
+            if constexpr (!kBf16) {
+                uint32_t mag = 0;
+#pragma unroll
+                for (int i = 0; i < kPer / 2; ++i) {
+                    const uint32_t m = w2[i] & 0x7FFF7FFFu;
+                    mag = max(mag, max(m & 0xFFFFu, m >> 16));
+                }
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, off));
+                pe = mag < 0x7F80u ? prescale_exponent(mag) : 0;
+#pragma unroll
+                for (int i = 0; i < kPer / 2; ++i)
+                    w2[i] = pack_f16x2(ldexp_exact(__uint_as_float(w2[i] << 16), pe),
+                                       ldexp_exact(__uint_as_float(w2[i] & 0xFFFF0000u), pe));
+            }
+            if (lane == 0) {
+                row_exp[r] = pe;
+                row_mask[r] = r >= n_rows ? 0 : t.mask ? t.mask[u.s.row0 + tok] : (2ull << tok) - 1;
+            }
+            if (lane * kPer < D) {
+#pragma unroll
+                for (int i = 0; i < kPer / 4; ++i) {
+                    const int d = lane * kPer + 4 * i;         // four values: one lane's share of one k-step
+                    const int piece = d / (4 * L::kKE), in = d % (4 * L::kKE);
+                    const int kk = piece * kSteps + in % L::kKE / 4;
+                    const int to = (r % 8) * 4 + in / L::kKE;
+                    uint32_t* f = reinterpret_cast<uint32_t*>(q_frag + (r / 16 * (D / 16) + kk) * 32 + to);
+                    f[(r % 16) / 8] = w2[2 * i];
+                    f[(r % 16) / 8 + 2] = w2[2 * i + 1];
+                }
+            }
+        }
+        __syncthreads();
+
+        float o[RT][kOT][4], m[RT][2], l[RT][2], rowf[RT][2];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+            for (int j = 0; j < kOT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[rt][j][e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[rt][e] = -INFINITY;
+                l[rt][e] = 0.f;
+                rowf[rt][e] = ldexp_exact(t.scale * kLog2e * a.g[0], -row_exp[16 * rt + 8 * e + g]);
+            }
+        }
+
+#pragma unroll 1
+        for (int i = 0; i < k.n; ++i) {
+            cp_wait<P::kStages - 2>();
+            __syncwarp();
+            issue(i + P::kStages - 1);
+            look_up(i + P::kStages);
+            const int place = i % P::kStages;
+            const uint32_t src = ring + place * L::kStage;
+            const uint32_t k_sc = src + 2 * L::kKBytes, v_sc = k_sc + L::kSBytes;
+            const int p0 = k.first + (warp + i * kMmaWarps) * L::kKeys;
+            const uint32_t gone = (bad >> (2 * place)) & 3u;
+            const bool special = p0 + L::kKeys > k.len || gone;
+
+            // ---- scores
+            float s[RT][kNT][4];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int j = 0; j < kNT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[rt][j][e] = 0.f;
+#pragma unroll
+            for (int x = 0; x < L::kKP; ++x) {
+                uint32_t raw[kNT][L::kKB / 4], sc[kNT][2];
+#pragma unroll
+                for (int j = 0; j < kNT; ++j) {
+                    lds_words<L::kKB>(src + ((j * L::kKP + x) * 32 + lane) * L::kKB, raw[j]);
+                    if constexpr (FMT == QG_KV_NVFP4) {
+                        // the piece's one or two blocks of 16
+                        const uint32_t at8 = k_sc + (8 * j + g) * L::kScale + (x * 4 + c) * L::kKE / 16;
+                        const uint32_t two = L::kKE == 32 ? lds16(at8) : lds8(at8);
+                        const uint32_t f = e4m3x2_to_f16x2(two);
+                        sc[j][0] = __byte_perm(f, f, 0x1010);
+                        sc[j][1] = __byte_perm(f, f, 0x3232);
+                    }
+                }
+#pragma unroll
+                for (int w4 = 0; w4 < kSteps; ++w4) {
+                    uint4 af[RT];
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        af[rt] = q_frag[(rt * (D / 16) + x * kSteps + w4) * 32 + lane];
+#pragma unroll
+                    for (int j = 0; j < kNT; ++j) {
+                        uint32_t b0, b1;
+                        key_pair<FMT>(raw[j], w4, sc[j], b0, b1);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) mma_16816<kBf16>(s[rt][j], af[rt], b0, b1);
+                    }
+                }
+            }
+
+            // ---- base-2 scores, masks, running maxima
+#pragma unroll
+            for (int j = 0; j < kNT; ++j) {
+                float cf[2] = {1.f, 1.f};
+                if constexpr (FMT == QG_KV_FP8) {
+                    const uint32_t two = lds16(k_sc + 8 * j + 2 * c);
+                    cf[0] = __uint_as_float(((two & 0xFFu) + 112u) << 23);
+                    cf[1] = __uint_as_float(((two >> 8) + 112u) << 23);
+                }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[rt][j][e] *= rowf[rt][e >> 1];
+                        if constexpr (FMT == QG_KV_FP8) s[rt][j][e] *= cf[e & 1];
+                    }
+            }
+            if (special) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const uint64_t mk[2] = {row_mask[16 * rt + g], row_mask[16 * rt + 8 + g]};
+#pragma unroll
+                    for (int j = 0; j < kNT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int p = p0 + 8 * j + 2 * c + (e & 1);
+                            const bool seen = p < k.end && !((gone >> (j >> 1)) & 1u) &&
+                                              (p < k.len || ((mk[e >> 1] >> (p - k.len)) & 1ull));
+                            if (!seen) s[rt][j][e] = -INFINITY;
+                        }
+                }
+            }
+            bool raise = false;
+            float top[RT][2];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < kNT; ++j) x = fmaxf(x, fmaxf(s[rt][j][2 * e], s[rt][j][2 * e + 1]));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                    top[rt][e] = x;
+                    raise = raise || x > m[rt][e] + kLazy;
+                }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float mn = fmaxf(m[rt][e], top[rt][e]);
+                        const float f = mn == -INFINITY ? 1.f : ex2(m[rt][e] - mn);
+                        m[rt][e] = mn;
+                        l[rt][e] *= f;
+#pragma unroll
+                        for (int j = 0; j < kOT; ++j) {
+                            o[rt][j][2 * e] *= f;
+                            o[rt][j][2 * e + 1] *= f;
+                        }
+                    }
+            }
+            // ---- weights
+            uint4 pf[RT][L::kGroups];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const float z0 = (m[rt][0] == -INFINITY ? 0.f : m[rt][0]) - kOffset;
+                const float z1 = (m[rt][1] == -INFINITY ? 0.f : m[rt][1]) - kOffset;
+#pragma unroll
+                for (int j = 0; j < kNT; ++j) {
+                    s[rt][j][0] = ex2(s[rt][j][0] - z0);
+                    s[rt][j][1] = ex2(s[rt][j][1] - z0);
+                    s[rt][j][2] = ex2(s[rt][j][2] - z1);
+                    s[rt][j][3] = ex2(s[rt][j][3] - z1);
+                    l[rt][0] += s[rt][j][0] + s[rt][j][1];
+                    l[rt][1] += s[rt][j][2] + s[rt][j][3];
+                }
+#pragma unroll
+                for (int x = 0; x < L::kGroups; ++x) {
+                    pf[rt][x].x = pack16<kBf16>(s[rt][2 * x][0], s[rt][2 * x][1]);
+                    pf[rt][x].y = pack16<kBf16>(s[rt][2 * x][2], s[rt][2 * x][3]);
+                    pf[rt][x].z = pack16<kBf16>(s[rt][2 * x + 1][0], s[rt][2 * x + 1][1]);
+                    pf[rt][x].w = pack16<kBf16>(s[rt][2 * x + 1][2], s[rt][2 * x + 1][3]);
+                }
+            }
+
+            // ---- values
+            uint32_t odd_values = 0;                 // a value of this lane's is not finite
+#pragma unroll
+            for (int x = 0; x < L::kGroups; ++x) {
+#pragma unroll
+                for (int y = 0; y < L::kVP; ++y) {
+                    uint32_t raw[4][L::kVB / 4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        lds_words<L::kVB>(src + L::kKBytes + (((4 * x + z) * L::kVP + y) * 32 + lane) * L::kVB,
+                                          raw[z]);
+                    constexpr int kPer = kBf16 ? 2 : FMT == QG_KV_FP8 ? 4 : 8;   // values of a word
+#pragma unroll
+                    for (int i4 = 0; i4 < L::kVB / 4; ++i4) {
+                        uint32_t sc[2] = {0, 0};     // scales of keys (2c, 2c + 1) and (2c + 8, 2c + 9)
+                        if constexpr (FMT == QG_KV_FP8) {
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                const uint32_t two = lds16(v_sc + 16 * x + 8 * z + 2 * c);
+                                sc[z] = (two & 0xFFu) << 10 | (two >> 8) << 26;
+                            }
+                        } else if constexpr (FMT == QG_KV_NVFP4) {
+                            const int blk = (y * 8 * L::kVE + g * L::kVE + i4 * 8) / 16;
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                const uint32_t at8 = v_sc + (16 * x + 8 * z + 2 * c) * L::kScale + blk;
+                                sc[z] = e4m3x2_to_f16x2(lds8(at8) | lds8(at8 + L::kScale) << 8);
+                            }
+                        }
+                        if (special && !kBf16) {
+                            // scales that stand behind the last key are not zeros like its codes
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                const int p = p0 + 16 * x + 8 * z + 2 * c;
+                                if (p >= k.end || ((gone >> x) & 1u)) sc[z] &= 0xFFFF0000u;
+                                if (p + 1 >= k.end || ((gone >> x) & 1u)) sc[z] &= 0x0000FFFFu;
+                            }
+                        }
+                        uint32_t b0[kPer], b1[kPer];
+                        value_pairs<FMT>(raw[0][i4], raw[1][i4], sc[0], b0);
+                        value_pairs<FMT>(raw[2][i4], raw[3][i4], sc[1], b1);
+                        if (special) {
+                            // 0 * infinity must not reach rows that do not see the key
+#pragma unroll
+                            for (int e = 0; e < kPer; ++e) {
+                                const uint32_t f0 = finite_halves<kBf16>(b0[e]), f1 = finite_halves<kBf16>(b1[e]);
+                                odd_values |= (f0 ^ b0[e]) | (f1 ^ b1[e]);
+                                b0[e] = f0;
+                                b1[e] = f1;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < kPer; ++e)
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt)
+                                mma_16816<kBf16>(o[rt][y * L::kVE + i4 * kPer + e], pf[rt][x], b0[e], b1[e]);
+                    }
+                }
+            }
+            if (special && __any_sync(0xffffffffu, odd_values != 0)) {
+                // the values left out above, one key at a time, to the rows that see them
+#pragma unroll
+                for (int j = 0; j < kNT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll 1
+                        for (int cc = 0; cc < 4; ++cc) {
+                            const int p = p0 + 8 * j + 2 * cc + e;
+                            float wt[RT][2];
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) {
+                                wt[rt][0] = __shfl_sync(0xffffffffu, s[rt][j][e], (lane & ~3) | cc);
+                                wt[rt][1] = __shfl_sync(0xffffffffu, s[rt][j][2 + e], (lane & ~3) | cc);
+                            }
+                            if (p >= k.end || ((gone >> (j >> 1)) & 1u)) continue;
+                            const int64_t row = kv_row(a, kv_page(a, b, p), head, p);
+#pragma unroll
+                            for (int x = 0; x < kOT; ++x)
+#pragma unroll
+                                for (int n = 0; n < 2; ++n) {
+                                    const int d = x / L::kVE * (8 * L::kVE) + (2 * c + n) * L::kVE + x % L::kVE;
+                                    const float v = kv_value(a, 1, row, d);
+                                    if (fabsf(v) < INFINITY) continue;
+#pragma unroll
+                                    for (int rt = 0; rt < RT; ++rt) {
+                                        if (wt[rt][0] > 0.f) o[rt][x][n] += wt[rt][0] * v;
+                                        if (wt[rt][1] > 0.f) o[rt][x][2 + n] += wt[rt][1] * v;
+                                    }
+                                }
+                        }
+            }
+        }
+
+        // ---- join the warps and write
+        cp_wait<0>();
+        __syncthreads();
+        float* jo = reinterpret_cast<float*>(body);
+        float2* jm = reinterpret_cast<float2*>(body + kMmaWarps * P::kRows * (D + 4) * 4);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = l[rt][e];
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                const int r = 16 * rt + 8 * e + g;
+                if (c == 0) jm[warp * P::kRows + r] = make_float2(m[rt][e] - kOffset, x);
+                float* dst = jo + (warp * P::kRows + r) * (D + 4);
+#pragma unroll
+                for (int j = 0; j < kOT; j += 4)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const int d = j / L::kVE * (8 * L::kVE) + (2 * c + n) * L::kVE + j % L::kVE;
+                        *reinterpret_cast<float4*>(dst + d) =
+                            make_float4(o[rt][j][2 * e + n], o[rt][j + 1][2 * e + n], o[rt][j + 2][2 * e + n],
+                                        o[rt][j + 3][2 * e + n]);
+                    }
+            }
+        __syncthreads();
+        const bool whole = s0 == 0 && s1 == u.steps;
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (s0 == 0);
+        for (int x = threadIdx.x; x < n_rows * (D / 4); x += kMmaThreads) {
+            const int r = x / (D / 4), d = x % (D / 4) * 4;
+            float mt = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < kMmaWarps; ++y) mt = fmaxf(mt, jm[y * P::kRows + r].x);
+            float lt = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int y = 0; y < kMmaWarps; ++y) {
+                const float2 ml = jm[y * P::kRows + r];
+                const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mt);
+                const float4 z = *reinterpret_cast<const float4*>(jo + (y * P::kRows + r) * (D + 4) + d);
+                lt += f * ml.y;
+                v.x += f * z.x;
+                v.y += f * z.y;
+                v.z += f * z.z;
+                v.w += f * z.w;
+            }
+            if (whole) {
+                const int tok = u.s.row0 + (row0 + r) / t.group;
+                const int64_t h = static_cast<int64_t>(tok) * t.q_heads + head * t.group + (row0 + r) % t.group;
+                const float f = tree_inverse(lt) * a.g[1];
+                uint2 y;
+                y.x = pack16<true>(v.x * f, v.y * f);
+                y.y = pack16<true>(v.z * f, v.w * f);
+                *reinterpret_cast<uint2*>(t.out + h * D + d) = y;
+                if (t.lse && d == 0) t.lse[h] = tree_lse(mt, lt);
+            } else {
+                *reinterpret_cast<float4*>(t.part_o + (slot * P::kRows + r) * D + d) = v;
+                if (d == 0) t.part_ml[slot * P::kRows + r] = make_float2(mt, lt);
+            }
+        }
+        __syncthreads();
+        at += s1 - s0;
     }
-    for (int i = 0; i < n; ++i)
-        out[(static_cast<int64_t>(row) * q_heads + h) * a.dim + lane * n + i] =
-            f32_to_bf16_bits_rn(l > 0.f ? acc[i] / l : 0.f);
-    if (lse && lane == 0) lse[static_cast<int64_t>(row) * q_heads + h] = l > 0.f ? m + logf(l) : -INFINITY;
+}
+
+// ------------------------------------------------------------------ join
+// One warp per (token, query head): the parts of its unit, if there are
+// several, in the CTAs' order. Bound by one chain of loads (batch, then the
+// parts' maxima and sums, then the parts).
+constexpr int kJoinWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid_constant__ TreeArgs t)
+{
+    __shared__ int64_t prefix[kKvMaxSeqs + 1];
+    const KvArgs& a = t.a;
+    const int lane = threadIdx.x & 31;
+    tree_prefix(t, prefix);
+    __syncthreads();
+    const int64_t total = prefix[a.n_seqs];
+    const int64_t chunk = tree_chunk(total, t.grid);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+    const int i = static_cast<int>(x / t.q_heads), h = static_cast<int>(x % t.q_heads);
+    if (i >= a.n_tokens || total == 0) return;
+    // the sequence of row i: the number of sequences that end at or before it
+    int b = 0;
+    for (int j = 0; j < a.n_seqs; j += 32) {
+        const bool before = j + lane < a.n_seqs && a.start[j + lane + 1] <= i;
+        const int n = __popc(__ballot_sync(0xffffffffu, before));
+        b += n;
+        if (n < 32) break;
+    }
+    if (b >= a.n_seqs) return;
+    const TreeSeq u = tree_seq(t, b);
+    if (i < u.s.row0 || i - u.s.row0 >= u.s.rows) return;
+    const int row = (i - u.s.row0) * t.group + h % t.group;
+    const int64_t first = prefix[b] + static_cast<int64_t>(h / t.group * u.tiles + row / t.rows) * u.steps;
+    const int64_t c0 = first / chunk, c1 = (first + u.steps - 1) / chunk;
+    if (c0 == c1) return;                            // written whole
+    const int r = row % t.rows;
+    float m = -INFINITY;
+    for (int64_t y = c0 + lane; y <= c1; y += 32) m = fmaxf(m, t.part_ml[(2 * y + (y == c0)) * t.rows + r].x);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    constexpr int kPer = D / 32;
+    float acc[kPer] = {}, l = 0.f;
+    // as many CTAs as there may be: a CTA's slot is 2c but for the unit's first
+#pragma unroll 4
+    for (int64_t y = c0; y <= c1; ++y) {
+        const int64_t at = (2 * y + (y == c0)) * t.rows + r;
+        const float2 ml = t.part_ml[at];
+        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+        l += f * ml.y;
+        float v[kPer];
+        if constexpr (kPer == 2) {
+            *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(t.part_o + at * D + lane * kPer);
+        } else {
+#pragma unroll
+            for (int z = 0; z < kPer; z += 4)
+                *reinterpret_cast<float4*>(v + z) = *reinterpret_cast<const float4*>(t.part_o + at * D + lane * kPer + z);
+        }
+#pragma unroll
+        for (int z = 0; z < kPer; ++z) acc[z] += f * v[z];
+    }
+    const float f = tree_inverse(l) * a.g[1];
+    const int64_t to = static_cast<int64_t>(i) * t.q_heads + h;
+    uint32_t* out = reinterpret_cast<uint32_t*>(t.out + to * D) + lane * (kPer / 2);
+#pragma unroll
+    for (int z = 0; z < kPer / 2; ++z) out[z] = pack16<true>(acc[2 * z] * f, acc[2 * z + 1] * f);
+    if (t.lse && lane == 0) t.lse[to] = tree_lse(m, l);
+}
+
+// ------------------------------------------------------------------ plans
+// Two row tiles of 16 per warp where more than one is filled and the
+// accumulators fit the registers.
+int mma_row_tiles(int dim, int rows) { return rows > 16 && dim <= 128 ? 2 : 1; }
+
+template <int FMT, int D, int RT>
+cudaError_t run_mma(TreeArgs t, cudaStream_t stream)
+{
+    using P = MmaPlan<FMT, D, RT>;
+    t.step = P::kStep;
+    t.grid = P::kCtas * sm_count(-1);
+    auto kern = tree_mma_kernel<FMT, D, RT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3(static_cast<unsigned>(t.grid)), dim3(kMmaThreads), P::kSmem, stream, t);
+    if (e != cudaSuccess) return e;
+    return launch_tree_join(t, stream);
+}
+
+template <int FMT, int D>
+cudaError_t run_dim(const TreeArgs& t, cudaStream_t stream)
+{
+    if constexpr (D <= 128)
+        if (t.rows == 32) return run_mma<FMT, D, 2>(t, stream);
+    return run_mma<FMT, D, 1>(t, stream);
+}
+
+template <int FMT>
+cudaError_t run_format(const TreeArgs& t, cudaStream_t stream)
+{
+    if (t.a.dim == 64) return run_dim<FMT, 64>(t, stream);
+    if (t.a.dim == 128) return run_dim<FMT, 128>(t, stream);
+    return run_dim<FMT, 256>(t, stream);
+}
+
+// R and the workspace's two parts, for the most CTAs that a format's kernel takes.
+struct TreePlan {
+    int rows;
+    size_t o_bytes, ml_bytes;
+};
+
+TreePlan plan_tree(int head_dim, int group, int max_tree)
+{
+    TreePlan p;
+    p.rows = 16 * mma_row_tiles(head_dim, group * max_tree);
+    const size_t slots = 2 * 2 * static_cast<size_t>(sm_count(-1));
+    p.o_bytes = slots * p.rows * head_dim * sizeof(float);
+    p.ml_bytes = slots * p.rows * sizeof(float2);
+    return p;
 }
 
 }  // namespace
 
+cudaError_t launch_tree_join(const TreeArgs& t, cudaStream_t stream)
+{
+    const int64_t units = static_cast<int64_t>(t.a.n_tokens) * t.q_heads;
+    const dim3 grid(static_cast<unsigned>((units + kJoinWarps - 1) / kJoinWarps)), block(32 * kJoinWarps);
+    if (t.a.dim == 64) return launch_pdl(tree_join_kernel<64>, grid, block, 0, stream, t);
+    if (t.a.dim == 128) return launch_pdl(tree_join_kernel<128>, grid, block, 0, stream, t);
+    return launch_pdl(tree_join_kernel<256>, grid, block, 0, stream, t);
+}
+
 size_t tree_attention_workspace_bytes(int head_dim, int group, int max_tree)
 {
-    (void)head_dim;
-    (void)group;
-    (void)max_tree;
-    return 256;
+    const TreePlan p = plan_tree(head_dim, group, max_tree);
+    return p.o_bytes + p.ml_bytes;
 }
 
 qg_status launch_tree_attention(const KvArgs& in, const uint16_t* q, int64_t q_stride, int q_heads, int max_tree,
-                                const uint64_t* mask, float scale, uint16_t* out, float* lse, void*,
+                                const uint64_t* mask, float scale, uint16_t* out, float* lse, void* workspace,
                                 cudaStream_t stream)
 {
-    KvArgs a = in;
-    a.status = device_status_ptr();
-    if (!a.status) return QG_ERR_CUDA;
-    const int64_t units = static_cast<int64_t>(a.n_tokens) * q_heads;
-    const cudaError_t e = launch_pdl(tree_simple_kernel, dim3(static_cast<unsigned>((units + 7) / 8)), dim3(256), 0,
-                                     stream, a, q, q_stride, q_heads, max_tree, mask, scale, out, lse);
+    TreeArgs t{};
+    t.a = in;
+    t.a.status = device_status_ptr();
+    if (!t.a.status) return QG_ERR_CUDA;
+    t.q = q;
+    t.q_stride = q_stride;
+    t.q_heads = q_heads;
+    t.group = q_heads / in.heads;
+    t.max_tree = max_tree;
+    t.mask = mask;
+    t.scale = scale;
+    t.out = out;
+    t.lse = lse;
+    const TreePlan p = plan_tree(in.dim, t.group, max_tree);
+    t.rows = p.rows;
+    t.part_o = static_cast<float*>(workspace);
+    t.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.o_bytes);
+    const cudaError_t e = in.fmt == QG_KV_BF16  ? run_format<QG_KV_BF16>(t, stream)
+                          : in.fmt == QG_KV_FP8 ? run_format<QG_KV_FP8>(t, stream)
+                                                : run_format<QG_KV_NVFP4>(t, stream);
     return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 

@@ -70,12 +70,12 @@ def values(codes, scales, fmt, g):
 
 def attention(q, k, v, seen, scale):
     """(out, lse, a, ds) of one sequence: q [T][Hq][D], k, v [L][Hkv][D],
-    seen [T][L]; a = sum p |v| per output, ds = sum |q k| scale, the largest
-    over the keys a row sees, for the error bound."""
+    seen [T][L]; for the error bounds a = (sum p |v|, sum |v|) per output and
+    ds = sum |q k| scale, the largest over the keys a row sees."""
     T, Hq, D = q.shape
     H = k.shape[1]
     G = Hq // H
-    out, a = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
+    out, a = np.zeros((T, Hq, D)), np.zeros((2, T, Hq, D))
     lse, ds = np.full((T, Hq), -np.inf), np.zeros((T, Hq))
     for t in range(T):
         keys = np.nonzero(seen[t])[0]
@@ -89,7 +89,8 @@ def attention(q, k, v, seen, scale):
             total = w.sum()
             lse[t, h] = m + np.log(total)
             out[t, h] = (w @ vv) / total
-            a[t, h] = (w @ np.abs(vv)) / total
+            a[0, t, h] = (w @ np.abs(vv)) / total
+            a[1, t, h] = np.abs(vv).sum(0)
             ds[t, h] = (np.abs(kk) @ np.abs(q[t, h])).max() * abs(scale)
     return out, lse, a, ds
 
@@ -104,13 +105,18 @@ def attention_bounds(a, ds, lse, n_keys, D, fmt):
     within e^(+-e_s), and by half a step of its 16-bit type when it enters the
     second product (f16 2^-11; bf16 2^-8), plus 2^-21 for the exponential
     itself. Sums of n weights: n 2^-22 relative. The same relative error is in
-    the sum that divides, but for the 16-bit rounding.
+    the sum that divides, but for the 16-bit rounding. Below f16's normal
+    range half a step is 2^-25, whatever the weight: weights are held times
+    2^7 or more of the row's largest (its maximum is kept within 2^8 above),
+    so the sum of weights is at least 2^7 and a weight is off by up to 2^-32 of
+    it there: 2^-32 sum |v| in all. bf16 has the range of 32-bit numbers.
     """
     e_s = ds * (D + 10) * 2.0 ** -22
     rel = 2 * (e_s + 2.0 ** -21 + n_keys * 2.0 ** -22) + 2.0 ** (-8 if fmt == "bf16" else -11)
     with np.errstate(invalid="ignore"):
         b_lse = e_s + 2.0 ** -20 + n_keys * 2.0 ** -22 + 2.0 ** -22 * np.where(np.isfinite(lse), np.abs(lse), 0.0)
-    return a * rel[..., None] + 1e-30, b_lse
+    low = 0.0 if fmt == "bf16" else 2.0 ** -32
+    return a[0] * rel[..., None] + a[1] * low + 1e-30, b_lse
 
 
 def ancestor_masks(r, counts):
