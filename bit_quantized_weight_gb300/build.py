@@ -24,7 +24,7 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hid
          "--expt-relaxed-constexpr", "-I", CSRC, "-I", INCLUDE]
 
 SOURCES = ["api.cu", "qgemv_dense.cu", "qgemv_tc.cu", "qgemv_cc.cu", "qgemv_simple.cu", "moe.cu", "moe_noalloc.cu", "qgemv_chain.cu", "moe_cc.cu", "qgemv_mt.cu",
-           "qgemv_chain_ws.cu", "kv_cache.cu", "tree_attention.cu"]
+           "qgemv_chain_ws.cu", "kv_cache.cu", "tree_attention.cu", "tree_tc.cu"]
 
 
 def _sources():

@@ -343,6 +343,8 @@ qg_status check_kv(const qg_kv_cache* c, const qg_kv_batch* b, KvArgs& a)
     a.n_seqs = b->n_seqs;
     a.max_pages = b->max_pages;
     a.n_tokens = b->n_tokens;
+    const uint64_t groups = static_cast<uint64_t>(c->page_size / 16);
+    a.page_magic = ((1ull << 36) + groups - 1) / groups;
     a.status = nullptr;
     return QG_OK;
 }

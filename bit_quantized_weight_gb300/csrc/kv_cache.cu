@@ -293,14 +293,14 @@ __device__ __forceinline__ void move_column(const KvArgs& a, const KvSeq& s, int
         for (int u = 0; u < kBatch; ++u)
             if (i0 + u < n) {
                 const int p = s.len + path[s.row0 + i0 + u];
-                const int page = a.table[static_cast<int64_t>(b) * a.max_pages + p / a.page_size];
+                const int page = a.table[static_cast<int64_t>(b) * a.max_pages + kv_page_index(a, p)];
                 v[u] = *reinterpret_cast<const T*>(base + kv_row(a, page, head, p) * row_bytes + col);
             }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
             if (i0 + u < n) {
                 const int p = s.len + i0 + u;
-                const int page = a.table[static_cast<int64_t>(b) * a.max_pages + p / a.page_size];
+                const int page = a.table[static_cast<int64_t>(b) * a.max_pages + kv_page_index(a, p)];
                 *reinterpret_cast<T*>(base + kv_row(a, page, head, p) * row_bytes + col) = v[u];
             }
     }

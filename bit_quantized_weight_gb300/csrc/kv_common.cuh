@@ -42,21 +42,36 @@ __device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, int b, int max_rows)
     return s;
 }
 
-// The page of position p of sequence b, or -1 (recorded) if it lies outside
-// the cache.
-__device__ __forceinline__ int kv_page(const KvArgs& a, int b, int p)
+// p / page_size without a division: with k = page_size / 16 <= 64 groups of 16
+// positions per page and x = p / 16 < 2^27, x * ceil(2^36 / k) exceeds
+// x * 2^36 / k by less than x < 2^36 / k, so the high part is x / k exactly.
+__device__ __forceinline__ int kv_page_index(const KvArgs& a, int p)
 {
-    const int page = a.table[static_cast<int64_t>(b) * a.max_pages + p / a.page_size];
-    if (page >= 0 && page < a.num_pages) return page;
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(p) >> 4) * a.page_magic) >> 36);
+}
+
+// The table's entry for position p of sequence b, which kv_valid then checks:
+// apart, so that several entries can be on their way at a time.
+__device__ __forceinline__ int kv_entry(const KvArgs& a, int b, int p)
+{
+    return a.table[static_cast<int64_t>(b) * a.max_pages + kv_page_index(a, p)];
+}
+
+// The page that an entry names, or -1 (recorded) if it lies outside the cache.
+__device__ __forceinline__ int kv_valid(const KvArgs& a, int entry)
+{
+    if (static_cast<unsigned>(entry) < static_cast<unsigned>(a.num_pages)) return entry;
     set_device_status(a.status, QG_ERR_INVALID_ARG);
     return -1;
 }
+
+__device__ __forceinline__ int kv_page(const KvArgs& a, int b, int p) { return kv_valid(a, kv_entry(a, b, p)); }
 
 // Index of (page, head, position) among the cache's rows: rows * row bytes is
 // the offset of its codes (64 bits: a pool may pass 2^31 rows' bytes).
 __device__ __forceinline__ int64_t kv_row(const KvArgs& a, int page, int head, int p)
 {
-    return (static_cast<int64_t>(page) * a.heads + head) * a.page_size + p % a.page_size;
+    return (static_cast<int64_t>(page) * a.heads + head) * a.page_size + (p - kv_page_index(a, p) * a.page_size);
 }
 
 }  // namespace qg

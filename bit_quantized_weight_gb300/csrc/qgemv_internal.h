@@ -229,6 +229,7 @@ struct KvArgs {
     int n_seqs;
     int max_pages;
     int n_tokens;
+    uint64_t page_magic;        // ceil(2^36 / (page_size / 16)), see kv_page_index
     int* status;
 };
 

@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
 #pragma unroll
             for (int s = 0; s < L::kGroups; ++s) {
                 const int p = k.first + (warp + i * kMmaWarps) * L::kKeys + 16 * s;
-                page_next[s] = i < k.n && p < k.end ? kv_page(a, b, p) : -2;
+                page_next[s] = i < k.n && p < k.end ? kv_entry(a, b, p) : 0;
             }
         };
         auto issue = [&](int i) {
@@ -279,8 +279,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
 #pragma unroll
                 for (int s = 0; s < L::kGroups; ++s) {
                     const int p = k.first + (warp + i * kMmaWarps) * L::kKeys + 16 * s;
-                    const int page = page_next[s];
-                    if (page == -1) bad |= 1u << (2 * place + s);
+                    const int page = p < k.end ? kv_valid(a, page_next[s]) : 0;
+                    if (page < 0) bad |= 1u << (2 * place + s);
                     const int64_t row = kv_row(a, max(page, 0), head, p);
                     const uint8_t* kp = a.codes[0] + row * L::kRow;
                     const uint8_t* vp = a.codes[1] + row * L::kRow;
@@ -725,8 +725,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
     for (int64_t y = c0; y <= c1; ++y) {
         const int64_t at = (2 * y + (y == c0)) * t.rows + r;
         const float2 ml = t.part_ml[at];
-        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-        l += f * ml.y;
+        const bool some = ml.x != -INFINITY;         // else the part's row saw nothing
+        const float f = some ? ex2(ml.x - m) : 0.f;
+        l += some ? f * ml.y : 0.f;
         float v[kPer];
         if constexpr (kPer == 2) {
             *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(t.part_o + at * D + lane * kPer);
@@ -736,7 +737,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
                 *reinterpret_cast<float4*>(v + z) = *reinterpret_cast<const float4*>(t.part_o + at * D + lane * kPer + z);
         }
 #pragma unroll
-        for (int z = 0; z < kPer; ++z) acc[z] += f * v[z];
+        for (int z = 0; z < kPer; ++z) acc[z] += some ? f * v[z] : 0.f;
     }
     const float f = tree_inverse(l) * a.g[1];
     const int64_t to = static_cast<int64_t>(i) * t.q_heads + h;
@@ -747,10 +748,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
 }
 
 // ------------------------------------------------------------------ plans
-// Two row tiles of 16 per warp where more than one is filled and the
-// accumulators fit the registers.
-int mma_row_tiles(int dim, int rows) { return rows > 16 && dim <= 128 ? 2 : 1; }
-
 template <int FMT, int D, int RT>
 cudaError_t run_mma(TreeArgs t, cudaStream_t stream)
 {
@@ -781,7 +778,11 @@ cudaError_t run_format(const TreeArgs& t, cudaStream_t stream)
     return run_dim<FMT, 256>(t, stream);
 }
 
-// R and the workspace's two parts, for the most CTAs that a format's kernel takes.
+// Rows per unit R, which also says which kernel runs, and the workspace's two
+// parts, for the most CTAs (slots: two per CTA) that a format's kernel takes.
+// Up to 16 rows one row tile of the warp-MMA kernel, up to 32 two; more go to
+// the tensor-core kernel, in one or two tiles of 128, but for head_dim 256,
+// whose accumulators do not fit it.
 struct TreePlan {
     int rows;
     size_t o_bytes, ml_bytes;
@@ -789,11 +790,13 @@ struct TreePlan {
 
 TreePlan plan_tree(int head_dim, int group, int max_tree)
 {
+    const int rows = group * max_tree;
     TreePlan p;
-    p.rows = 16 * mma_row_tiles(head_dim, group * max_tree);
-    const size_t slots = 2 * 2 * static_cast<size_t>(sm_count(-1));
-    p.o_bytes = slots * p.rows * head_dim * sizeof(float);
-    p.ml_bytes = slots * p.rows * sizeof(float2);
+    p.rows = rows <= 16 || head_dim == 256 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+    const size_t ctas = (p.rows == 256 ? 1 : 2) * static_cast<size_t>(sm_count(-1));
+    const size_t rows_held = 2 * ctas * p.rows;
+    p.o_bytes = rows_held * head_dim * sizeof(float);
+    p.ml_bytes = rows_held * sizeof(float2);
     return p;
 }
 
@@ -835,7 +838,11 @@ qg_status launch_tree_attention(const KvArgs& in, const uint16_t* q, int64_t q_s
     t.rows = p.rows;
     t.part_o = static_cast<float*>(workspace);
     t.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.o_bytes);
-    const cudaError_t e = in.fmt == QG_KV_BF16  ? run_format<QG_KV_BF16>(t, stream)
+    const DebugState dbg = debug_state();
+    t.wait_ns = dbg.wait_ns;
+    t.starve = dbg.starve;
+    const cudaError_t e = t.rows >= 128           ? launch_tree_tc(t, stream)
+                          : in.fmt == QG_KV_BF16  ? run_format<QG_KV_BF16>(t, stream)
                           : in.fmt == QG_KV_FP8 ? run_format<QG_KV_FP8>(t, stream)
                                                 : run_format<QG_KV_NVFP4>(t, stream);
     return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;

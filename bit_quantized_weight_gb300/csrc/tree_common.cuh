@@ -34,7 +34,9 @@ struct TreeArgs {
     int rows;                 // R
     int step;                 // keys per step
     int grid;                 // CTAs of the reading kernel
-    uint64_t wait_ns;
+    int run;                  // keys of a page that the tensor-core kernel copies at a time
+    uint64_t wait_ns;         // limit of the tensor-core kernel's waits
+    int starve;               // fault injection: its key tiles are never announced
 };
 
 struct TreeSeq {
@@ -127,6 +129,7 @@ __device__ __forceinline__ float kv_value(const KvArgs& a, int kv, int64_t row, 
     return half_bits_to_f32(hmul2(h, s & 0xFFFFu) & 0xFFFFu);
 }
 
+cudaError_t launch_tree_tc(const TreeArgs& t, cudaStream_t stream);
 cudaError_t launch_tree_join(const TreeArgs& t, cudaStream_t stream);
 
 }  // namespace qg

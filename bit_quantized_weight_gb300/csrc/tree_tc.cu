@@ -1,0 +1,1029 @@
+// tree_tc.cu -- attention of drafted tokens over the paged cache on the
+// 5th-generation tensor cores, for units of many query rows.
+//
+// With R query rows per key/value head, a cached value of b bytes takes
+// 2 R / b multiplications: at 6.8 TB/s a tree of 8 tokens with 12 query heads
+// per head already asks for 650 (bf16) to 2,300 TFLOP/s (NVFP4). So the keys
+// and values are brought into shared memory once per CTA as exact f16 (bf16)
+// tiles and multiplied by tcgen05.mma:
+//   S = Q K^T   both operands in shared memory, 128 rows x 128 keys -> TMEM
+//   O += P V    P in TMEM (written over S by the softmax warps), V in shared
+//               memory as it is stored (head_dim contiguous: N-major)
+// A CTA runs two streams of row tiles, so that one's softmax overlaps the
+// other's products: either the two halves of a unit of 256 rows over the same
+// tiles of keys, or two units' worth of work of up to 128 rows each
+// (two "virtual CTAs" with their own ranges of steps).
+// Warps: 0-3 and 4-7 softmax of streams 0 and 1 (a thread per row), 8-9 bring
+// keys, 10-11 values, 12 and 13 issue the two streams' MMAs.
+#include <type_traits>
+
+#include "tcgen05.cuh"
+#include "tree_common.cuh"
+
+namespace qg {
+namespace {
+
+constexpr int kTcKeys = 128;                 // keys per tile
+constexpr int kTcRows = 128;                 // rows per stream
+constexpr int kConvertWarps = 4;
+constexpr int kTcThreads = 512;               // four warpgroups, 128 registers per thread at launch ...
+constexpr int kMmaWarp = 12;                  // of stream 0; the next warp is stream 1's
+constexpr int kIssueWarp = 14;                // starts the copies of coded keys and values
+constexpr int kLaunchRegs = 128;
+constexpr int kSoftmaxRegs = 144;            // ... dealt out anew: 2 * 144 + 104 + 120 = 4 * 128
+constexpr int kLoadRegs = 104;
+constexpr int kIssueRegs = 120;
+static_assert(2 * kSoftmaxRegs + kLoadRegs + kIssueRegs <= 4 * kLaunchRegs, "more registers than the block has");
+constexpr int kStages = 2;                   // tiles of keys and of values
+constexpr int kMaxRaw = 4;                   // tiles as they are stored, before their conversion
+// Weights are 2^(s - m + 8) with m a whole number from the row's largest score
+// (rounded up), replaced only once a score passes it by 7: a weight is at most
+// 2^15, within f16, the largest at least 2^7, and a change of m scales what was
+// summed by a power of two, without rounding.
+constexpr float kTcOffset = 8.f;
+constexpr float kTcLazy = 7.f;
+
+enum Bar : int {
+    kKFull = 0,                              // [stage]
+    kKEmpty = kKFull + kStages,
+    kVFull = kKEmpty + kStages,
+    kVEmpty = kVFull + kStages,
+    kQFull = kVEmpty + kStages,              // [stream]
+    kSFull = kQFull + 2,
+    kPFull = kSFull + 2,
+    kODone = kPFull + 2,
+    kRawFull = kODone + 2,                   // [raw stage]
+    kRawEmpty = kRawFull + kMaxRaw,
+    kVLand = kRawEmpty + kMaxRaw,
+    kBars = kVLand + 1
+};
+
+template <int FMT, int D>
+struct TcPlan {
+    static constexpr int kTile = kTcKeys * D * 2;        // bytes of a tile of Q, K or V
+    static constexpr int kHead = 1024;                   // barriers and what the warps tell each other
+    static constexpr int kQ = kHead;
+    static constexpr int kK = kQ + 2 * kTile;
+    static constexpr int kV = kK + kStages * kTile;
+    static constexpr int kRaw = kV + kStages * kTile;
+    static constexpr int kCodes = kTcKeys * kv_row_bytes(FMT, D);
+    static constexpr int kRawStage = FMT == QG_KV_BF16 ? 0 : kCodes + kTcKeys * kv_scale_bytes(FMT, D);
+    static constexpr int kRoom = 227 * 1024 - 1024 - kRaw;               // 1024 for alignment
+    static constexpr int kFit = kRawStage ? kRoom / (kRawStage ? kRawStage : 1) : 0;
+    static constexpr int kNRaw = kFit > kMaxRaw ? kMaxRaw : kFit;
+    static constexpr int kSmem = kRaw + kNRaw * kRawStage + 1024;
+    static_assert(FMT == QG_KV_BF16 || kNRaw >= 2, "too little shared memory");
+    static_assert(6 * kTile >= (kKvMaxSeqs + 1) * 8, "prefix sums lie where the tiles go");
+};
+
+// Operand tiles lie as blocks of 64 columns (128 bytes) by 128 rows, the
+// 16-byte pieces of a row permuted by the row's low three bits (the 128-byte
+// swizzle). Byte offset of piece `ch` (of 8 values) of `row`.
+__device__ __forceinline__ uint32_t tile_at(int row, int ch)
+{
+    return (ch >> 3) * (kTcRows * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+}
+
+// Descriptors of such a tile. K-major (Q, K): eight rows are 1024 bytes apart.
+// N-major (V): 64-column blocks are 16 KB apart, eight keys 1024 bytes.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, uint32_t lbo)
+{
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+           static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A bounded wait of a whole warp: all of its lanes go on, or none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const TreeArgs& t)
+{
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, t.wait_ns, t.a.status));
+}
+
+// A piece of a unit: what one stream does between two epilogues.
+struct Segment {
+    int b, head;
+    int row0, n_rows;            // query rows of the unit
+    int first, end;              // keys
+    int len, tok0, n_tok;        // context, the sequence's rows
+    int tiles;
+    int slot;                    // -1: the whole unit
+};
+
+// The segments of one virtual CTA's range of steps, in order.
+struct Cursor {
+    int64_t at, end, base;
+    int b, vc;
+
+    __device__ __forceinline__ void locate(const TreeArgs& t, const int64_t* prefix, int vcta)
+    {
+        const int64_t total = prefix[t.a.n_seqs];
+        const int64_t chunk = tree_chunk(total, t.grid);
+        vc = vcta;
+        at = min(total, vcta * chunk);
+        end = min(total, at + chunk);
+        b = at < end ? tree_find(prefix, t.a.n_seqs, at) : 0;
+        base = prefix[b];
+    }
+
+    __device__ __forceinline__ bool next(const TreeArgs& t, Segment& g)
+    {
+        if (at >= end) return false;
+        TreeSeq u = tree_seq(t, b);
+        int64_t w = static_cast<int64_t>(u.steps) * u.tiles * t.a.heads;
+        while (at >= base + w) {
+            base += w;
+            ++b;
+            u = tree_seq(t, b);
+            w = static_cast<int64_t>(u.steps) * u.tiles * t.a.heads;
+        }
+        const int unit = static_cast<int>((at - base) / u.steps);
+        const int s0 = static_cast<int>((at - base) % u.steps);
+        const int s1 = static_cast<int>(min(static_cast<int64_t>(u.steps), s0 + (end - at)));
+        g.b = b;
+        g.head = unit / u.tiles;
+        g.row0 = unit % u.tiles * t.rows;
+        g.n_rows = min(t.rows, u.s.rows * t.group - g.row0);
+        g.first = s0 * kTcKeys;
+        g.end = min(u.keys, s1 * kTcKeys);
+        g.len = u.s.len;
+        g.tok0 = u.s.row0;
+        g.n_tok = u.s.rows;
+        g.tiles = s1 - s0;
+        g.slot = s0 == 0 && s1 == u.steps ? -1 : 2 * vc + (s0 == 0);
+        at += g.tiles;
+        return true;
+    }
+};
+
+// The tiles of a CTA in the order in which they are brought and multiplied:
+// SHARED, one cursor and every tile for both streams; else the two streams'
+// tiles in turn while both have some.
+struct Side {
+    Cursor cur;
+    Segment seg;
+    int tile;
+    bool live;
+
+    __device__ __forceinline__ void start(const TreeArgs& t, const Cursor& from)
+    {
+        cur = from;
+        live = cur.next(t, seg);
+        tile = 0;
+    }
+
+    __device__ __forceinline__ void take(const TreeArgs& t, Segment& g, int& j)
+    {
+        g = seg;
+        j = tile;
+        if (++tile == g.tiles) {
+            live = cur.next(t, seg);
+            tile = 0;
+        }
+    }
+};
+
+template <bool SHARED>
+struct Items {
+    Side x, y;
+    int turn;
+
+    __device__ __forceinline__ void start(const TreeArgs& t, const Cursor* from)
+    {
+        turn = 0;
+        x.start(t, from[0]);
+        if (!SHARED) y.start(t, from[1]);
+    }
+
+    // The next tile: its stream (0 when SHARED), or -1 after the last.
+    __device__ __forceinline__ int next(const TreeArgs& t, Segment& g, int& j)
+    {
+        if (SHARED) {
+            if (!x.live) return -1;
+            x.take(t, g, j);
+            return 0;
+        }
+        if (!x.live && !y.live) return -1;
+        if (y.live && (turn == 1 || !x.live)) {
+            y.take(t, g, j);
+            turn = 0;
+            return 1;
+        }
+        x.take(t, g, j);
+        turn = 1;
+        return 0;
+    }
+};
+
+// ------------------------------------------------------------------ loads
+// What the warp that starts a tile's copies tells those that convert it.
+struct RawInfo {
+    int left;                    // keys of the tile, -1: there are no more tiles
+    int drafts;                  // its keys from here on are drafts
+    uint32_t groups;             // groups of 16 keys whose page lies in the cache
+    int pad;
+};
+
+// The runs of a tile: consecutive keys of one page, t.run of them (the largest
+// of 16, 32, 64 and 128 that divides the page size), one lane each. The page
+// table is read a tile ahead.
+template <bool SHARED>
+struct Runs {
+    Items<SHARED> items;
+    int64_t row;                 // first row of this lane's run in the cache
+    int keys;                    // its keys in the tile, up to a multiple of 16
+    bool on;                     // it is copied
+    RawInfo info;
+    bool more;
+    Segment g;
+    int j, entry;
+    bool ahead;
+
+    __device__ __forceinline__ int key() const { return (threadIdx.x & 31); }
+
+    __device__ __forceinline__ void look_up(const TreeArgs& t)
+    {
+        const int p = g.first + j * kTcKeys + key() * t.run;
+        entry = ahead && key() * t.run < kTcKeys && p < g.end ? kv_entry(t.a, g.b, p) : 0;
+    }
+
+    __device__ __forceinline__ void start(const TreeArgs& t, const Cursor* from)
+    {
+        items.start(t, from);
+        ahead = items.next(t, g, j) >= 0;
+        look_up(t);
+        step(t);
+    }
+
+    __device__ __forceinline__ void step(const TreeArgs& t)
+    {
+        more = ahead;
+        if (!more) return;
+        const int p0 = g.first + j * kTcKeys, k0 = key() * t.run;
+        info.left = min(kTcKeys, g.end - p0);
+        info.drafts = g.len - p0;
+        const bool mine = k0 < info.left;
+        const int page = mine ? kv_valid(t.a, entry) : -1;
+        on = page >= 0;
+        row = on ? kv_row(t.a, page, g.head, p0 + k0) : 0;
+        keys = on ? min(t.run, (info.left - k0 + 15) & ~15) : 0;
+        info.groups = __reduce_or_sync(0xffffffffu, on ? ((1u << (keys >> 4)) - 1u) << (k0 >> 4) : 0u);
+        ahead = items.next(t, g, j) >= 0;
+        look_up(t);
+    }
+
+    // Some of the tile's places get no key of the context.
+    __device__ __forceinline__ static bool special(const RawInfo& i)
+    {
+        return i.left < kTcKeys || i.drafts < kTcKeys || i.groups != 0xFFu;
+    }
+};
+
+// One 16-byte piece of a stored row as f16 values, eight to an element of `out`.
+template <int FMT>
+__device__ __forceinline__ void piece_values(const uint4 raw, uint32_t sc, uint4* out)
+{
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    if constexpr (FMT == QG_KV_FP8) {
+        const uint32_t s2 = sc * 0x04000400u;                // 2^(s-15) as f16, twice
+        uint32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[2 * i] = hmul2(e4m3x2_to_f16x2(w[i] & 0xFFFFu), s2);
+            h[2 * i + 1] = hmul2(e4m3x2_to_f16x2(w[i] >> 16), s2);
+        }
+        out[0] = make_uint4(h[0], h[1], h[2], h[3]);
+        out[1] = make_uint4(h[4], h[5], h[6], h[7]);
+    } else {
+        const uint32_t f = e4m3x2_to_f16x2(sc);              // the scales of the piece's two blocks
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t s2 = __byte_perm(f, f, i < 2 ? 0x1010 : 0x3232);
+            uint32_t h[4];
+            e2m1x8_to_f16x2x4(w[i], h);
+            out[i] = make_uint4(hmul2(h[0], s2), hmul2(h[1], s2), hmul2(h[2], s2), hmul2(h[3], s2));
+        }
+    }
+}
+
+// Zeroes each 16-bit value that is infinite or NaN.
+template <bool BF16>
+__device__ __forceinline__ void drop_odd(uint4& v, bool& odd)
+{
+    constexpr uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & e) == e) {
+            w[i] &= 0xFFFF0000u;
+            odd = true;
+        }
+        if (((w[i] >> 16) & e) == e) {
+            w[i] &= 0x0000FFFFu;
+            odd = true;
+        }
+    }
+}
+
+// A warp's part of a tile is in place: visible to the tensor core, then counted.
+__device__ __forceinline__ void announce(uint64_t* bar, int starve)
+{
+    fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0 && !starve) mbar_arrive(bar);
+}
+
+// Coded keys and values: one warp starts the copies of the tiles as they are
+// stored, keys and values in turn.
+template <int FMT, int D, bool SHARED>
+__device__ __forceinline__ void copy_coded(const TreeArgs& t, const Cursor* from, uint8_t* smem, uint64_t* bar,
+                                           RawInfo* infos)
+{
+    using P = TcPlan<FMT, D>;
+    constexpr int kRow = kv_row_bytes(FMT, D), kScale = kv_scale_bytes(FMT, D);
+    const KvArgs& a = t.a;
+    const int lane = threadIdx.x & 31;
+    Runs<SHARED> runs;
+    runs.start(t, from);
+    uint32_t r = 0, ph = 1;                                  // raw stage, parity of its being empty
+    auto turn = [&]() {
+        if (++r == P::kNRaw) {
+            r = 0;
+            ph ^= 1u;
+        }
+    };
+    while (runs.more) {
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+            if (!warp_wait(&bar[kRawEmpty + r], ph, t)) return;
+            const uint32_t bytes = __popc(runs.info.groups) * 16 * (kRow + kScale);
+            uint8_t* dst = smem + P::kRaw + r * P::kRawStage;
+            if (lane == 0) {
+                infos[r] = runs.info;
+                if (!t.starve) mbar_arrive_expect_tx(&bar[kRawFull + r], bytes);
+            }
+            __syncwarp();
+            if (runs.on && !t.starve) {
+                const int k0 = lane * t.run;
+                bulk_load(dst + k0 * kRow, a.codes[kv] + runs.row * kRow, runs.keys * kRow, &bar[kRawFull + r]);
+                bulk_load(dst + P::kCodes + k0 * kScale, a.scales[kv] + runs.row * kScale, runs.keys * kScale,
+                          &bar[kRawFull + r]);
+            }
+            turn();
+        }
+        runs.step(t);
+    }
+    if (!warp_wait(&bar[kRawEmpty + r], ph, t)) return;
+    if (lane == 0) {
+        infos[r].left = -1;
+        mbar_arrive(&bar[kRawFull + r]);
+    }
+}
+
+// ... and four warps convert them to f16 tiles. Drafts' values that are not
+// finite are left out (0 times them would reach rows that do not see the
+// draft) and flagged for the epilogue; what no key fills is zero.
+template <int FMT, int D>
+__device__ __forceinline__ void convert(const TreeArgs& t, uint8_t* smem, uint64_t* bar, const RawInfo* infos,
+                                        volatile int* odd_flag, int tid)
+{
+    using P = TcPlan<FMT, D>;
+    constexpr int kRow = kv_row_bytes(FMT, D), kScale = kv_scale_bytes(FMT, D);
+    constexpr int kPerKey = kRow / 16;                       // pieces of a row
+    constexpr int kKeys = 32 * kConvertWarps / kPerKey;      // keys that the threads convert at a time
+    constexpr int kChunks = FMT == QG_KV_FP8 ? 2 : 4;        // pieces of eight f16 from one of codes
+    const int c = tid % kPerKey;
+    uint32_t r = 0, ph = 0;
+    for (uint32_t it = 0;; ++it) {
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+            if (!warp_wait(&bar[kRawFull + r], ph, t)) return;
+            const RawInfo info = infos[r];
+            if (info.left < 0) return;
+            const uint32_t st = it & 1u;
+            if (!warp_wait(&bar[(kv ? kVEmpty : kKEmpty) + st], ((it >> 1) & 1u) ^ 1u, t)) return;
+            const uint32_t src = smem_u32(smem + P::kRaw + r * P::kRawStage);
+            uint8_t* tile = smem + (kv ? P::kV : P::kK) + st * P::kTile;
+            auto piece = [&](int n, uint4* out) {
+                const int key = n * kKeys + tid / kPerKey;
+                const uint32_t at = src + P::kCodes + key * kScale;
+                piece_values<FMT>(lds128(src + (n * 32 * kConvertWarps + tid) * 16),
+                                  FMT == QG_KV_FP8 ? lds8(at) : lds16(at + 2 * c), out);
+                return key;
+            };
+            if (kv == 0 || !Runs<false>::special(info)) {
+#pragma unroll 4
+                for (int n = 0; n < kPerKey; ++n) {
+                    uint4 out[kChunks];
+                    const int key = piece(n, out);
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i)
+                        *reinterpret_cast<uint4*>(tile + tile_at(key, c * kChunks + i)) = out[i];
+                }
+            } else {
+                bool odd = false;
+#pragma unroll 1
+                for (int n = 0; n < kPerKey; ++n) {
+                    uint4 out[kChunks];
+                    const int key = piece(n, out);
+                    const bool on = key < info.left && ((info.groups >> (key >> 4)) & 1u);
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i) {
+                        if (!on) out[i] = make_uint4(0, 0, 0, 0);
+                        if (key >= info.drafts) drop_odd<false>(out[i], odd);
+                        *reinterpret_cast<uint4*>(tile + tile_at(key, c * kChunks + i)) = out[i];
+                    }
+                }
+                if (odd) *odd_flag = 1;
+            }
+            announce(&bar[(kv ? kVFull : kKFull) + st], 0);
+            if ((tid & 31) == 0) mbar_arrive(&bar[kRawEmpty + r]);
+            if (++r == P::kNRaw) {
+                r = 0;
+                ph ^= 1u;
+            }
+        }
+    }
+}
+
+// bf16 keys (kv = 0) or values (1): copied straight into the tiles, swizzled on
+// the way, by one warp each. A tile of values with places to clear is announced
+// by this warp once it has done so.
+template <int D, bool SHARED>
+__device__ __forceinline__ void copy_plain(const TreeArgs& t, const CUtensorMap* map, const Cursor* from,
+                                           uint8_t* tiles, uint64_t* full, uint64_t* empty, uint64_t* land,
+                                           volatile int* odd_flag, int kv)
+{
+    constexpr int kTile = TcPlan<QG_KV_BF16, D>::kTile;
+    const int lane = threadIdx.x & 31;
+    Runs<SHARED> runs;
+    runs.start(t, from);
+    uint32_t landed = 0;
+    for (uint32_t it = 0; runs.more; ++it) {
+        const uint32_t st = it & 1u;
+        if (!warp_wait(&empty[st], ((it >> 1) & 1u) ^ 1u, t)) return;
+        const bool clear = kv == 1 && Runs<SHARED>::special(runs.info);
+        uint64_t* done = clear ? land : &full[st];
+        // boxes are whole runs: what lies behind the last key is cleared or masked
+        const uint32_t n_runs = __popc(__ballot_sync(0xffffffffu, runs.on));
+        const bool go = kv == 1 || !t.starve;
+        if (lane == 0 && go) mbar_arrive_expect_tx(done, n_runs * t.run * D * 2);
+        __syncwarp();
+        if (runs.on && go)
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+                tma_load_2d(tiles + st * kTile + x * (kTcRows * 128) + lane * t.run * 128, map, 64 * x,
+                            static_cast<int32_t>(runs.row), done);
+        if (clear) {
+            if (!warp_wait(land, landed++ & 1u, t)) return;
+            bool odd = false;
+            for (int x = lane; x < kTcKeys * D / 8; x += 32) {
+                const int key = x / (D / 8);
+                const bool on = key < runs.info.left && ((runs.info.groups >> (key >> 4)) & 1u);
+                if (on && key < runs.info.drafts) continue;
+                uint4* at = reinterpret_cast<uint4*>(tiles + st * kTile + tile_at(key, x % (D / 8)));
+                uint4 y = on ? *at : make_uint4(0, 0, 0, 0);
+                drop_odd<true>(y, odd);
+                *at = y;
+            }
+            if (odd) *odd_flag = 1;
+            announce(&full[st], 0);
+        }
+        runs.step(t);
+    }
+}
+
+// ------------------------------------------------------------------ softmax
+using f2 = unsigned long long;               // two floats, low half first
+__device__ __forceinline__ f2 f2_pack(float lo, float hi)
+{
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_unpack(f2 v, float& lo, float& hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c)
+{
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b)
+{
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t mul16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if constexpr (BF16)
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A row's scores became too large for its m: m is raised, and what was summed
+// with the old one is scaled: l, the row of O, and the weights of this tile
+// that are already written (`pieces` of 32 keys). Rare, so small rather than
+// fast.
+template <bool BF16, int D>
+__device__ __forceinline__ void raise_max(uint32_t ts, uint32_t to, bool has_o, int pieces, float top, float& m,
+                                          float& l)
+{
+    const float mn = fmaxf(m, ceilf(top));
+    const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+    m = mn;
+    l *= f;
+    uint32_t v[16];
+    if (has_o) {                             // the products of the tiles before are complete: S came after them
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+            tc_ld<16>(to + 16 * c, v);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(tc_after_wait(v[i])) * f);
+            tc_st_x16(to + 16 * c, v);
+        }
+    }
+    const uint32_t f16 = pack16<BF16>(f, f);
+#pragma unroll 1
+    for (int c = 0; c < pieces; ++c) {
+        tc_ld<16>(ts + 16 * c, v);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = mul16x2<BF16>(tc_after_wait(v[i]), f16);
+        tc_st_x16(ts + 16 * c, v);
+    }
+    tc_wait_st();
+}
+
+// One tile's scores of this thread's row to weights, in place: the weights of
+// 32 keys take the columns of 16 scores that were read before.
+template <bool BF16, bool SPECIAL, int D>
+__device__ __forceinline__ void weights(uint32_t ts, uint32_t to, bool has_o, float rowf, const uint32_t (&seen)[4],
+                                        float& m, float& l)
+{
+    f2 sum[2] = {0, 0};
+    const f2 rowf2 = f2_pack(rowf, rowf);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        uint32_t x[64];
+        tc_ld<32>(ts + 64 * c, x);
+        tc_ld<32>(ts + 64 * c + 32, x + 32);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 64; ++i) x[i] = tc_after_wait(x[i]);
+        if constexpr (SPECIAL) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                if (!((seen[2 * c + i / 32] >> (i & 31)) & 1u)) x[i] = 0xFF800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
+#pragma unroll
+        for (int i = 8; i < 64; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(x[i + e])), __uint_as_float(x[i + e + 4]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rowf;
+        if (__any_sync(0xffffffffu, top > m + kTcLazy)) {
+            float a, b, a1, b1;
+            f2_unpack(sum[0], a, a1);
+            f2_unpack(sum[1], b, b1);
+            l += (a + a1) + (b + b1);
+            sum[0] = sum[1] = 0;
+            raise_max<BF16, D>(ts, to, has_o, 2 * c, top, m, l);
+        }
+        const float z = kTcOffset - (m == -INFINITY ? 0.f : m);
+        const f2 z2 = f2_pack(z, z);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            uint32_t h[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(x[32 * y + i]), __uint_as_float(x[32 * y + i + 1])), rowf2,
+                                 z2),
+                          x0, x1);
+                x0 = ex2(x0);
+                x1 = ex2(x1);
+                if constexpr (SPECIAL) {     // also where m is still -infinity, or the scale is 0
+                    x0 = (seen[2 * c + y] >> i) & 1u ? x0 : 0.f;
+                    x1 = (seen[2 * c + y] >> (i + 1)) & 1u ? x1 : 0.f;
+                }
+                sum[(i >> 1) & 1] = f2_add(sum[(i >> 1) & 1], f2_pack(x0, x1));
+                h[i / 2] = pack16<BF16>(x0, x1);
+            }
+            tc_st_x16(ts + 32 * c + 16 * y, h);
+        }
+    }
+    float a, b, a1, b1;
+    f2_unpack(sum[0], a, a1);
+    f2_unpack(sum[1], b, b1);
+    l += (a + a1) + (b + b1);
+}
+
+// ------------------------------------------------------------------ products
+template <bool ACCUMULATE>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(ACCUMULATE ? 1 : 0)
+        : "memory");
+}
+
+// One thread per stream issues its products: S of a tile, and once its weights
+// are there O += P V, then S of the next tile over them. (The tensor core
+// takes one thread's products in order.)
+template <int FMT, int D, bool SHARED>
+__device__ __forceinline__ void multiply(const TreeArgs& t, const Cursor* from, uint8_t* smem, uint64_t* bar, uint32_t tmem,
+                                         int s)
+{
+    using P = TcPlan<FMT, D>;
+    constexpr bool kBf16 = FMT == QG_KV_BF16;
+    constexpr uint32_t id_s = tc_idesc_f16(128, kTcKeys, kBf16);
+    constexpr uint32_t id_o = tc_idesc_f16(128, D, kBf16) | 1u << 16;   // B is N-major
+    const uint64_t dq = tile_desc(smem_u32(smem + P::kQ) + s * P::kTile, 16);
+    const uint64_t dk = tile_desc(smem_u32(smem + P::kK), 16);
+    const uint64_t dv = tile_desc(smem_u32(smem + P::kV), kTcRows * 128);
+    const uint32_t ts = tmem + 128 * s, to = tmem + 256 + 128 * s;
+    auto wait = [&](int b, uint32_t parity) { return mbar_wait_bounded(&bar[b], parity, t.wait_ns, t.a.status); };
+    auto product_v = [&](uint32_t it, uint32_t np, bool first, bool last) {
+        const uint32_t st = it & 1u;
+        if (!wait(kVFull + st, (it >> 1) & 1u) || !wait(kPFull + s, np & 1u)) return false;
+        tc_fence_after();
+        const uint64_t d = dv + st * (P::kTile >> 4);
+        tc_mma_f16_ts(to, ts, d, id_o, !first);
+#pragma unroll
+        for (int x = 1; x < kTcKeys / 16; ++x) tc_mma_f16_ts(to, ts + 8 * x, d + x * (2048 >> 4), id_o, true);
+        tc_commit(&bar[kVEmpty + st]);
+        if (last) tc_commit(&bar[kODone + s]);
+        return true;
+    };
+    Items<SHARED> items;
+    items.start(t, from);
+    Segment g;
+    int j, owner;
+    uint32_t np = 0, nq = 0, before = 0;
+    bool waits = false, first = false, last = false;     // a product P V of tile `before`
+    for (uint32_t it = 0; (owner = items.next(t, g, j)) >= 0; ++it) {
+        const uint32_t st = it & 1u;
+        if (SHARED && s == 1 && g.n_rows <= kTcRows) {   // the other stream's alone: only counted
+            if (waits && !product_v(before, np++, first, last)) return;
+            waits = false;
+            if (!wait(kKFull + st, (it >> 1) & 1u)) return;
+            mbar_arrive(&bar[kKEmpty + st]);
+            if (!wait(kVFull + st, (it >> 1) & 1u)) return;
+            mbar_arrive(&bar[kVEmpty + st]);
+            continue;
+        }
+        if (!SHARED && owner != s) continue;
+        if (waits && !product_v(before, np++, first, last)) return;
+        if (!wait(kKFull + st, (it >> 1) & 1u)) return;
+        if (j == 0 && !wait(kQFull + s, nq++ & 1u)) return;
+        tc_fence_after();
+        const uint64_t d = dk + st * (P::kTile >> 4);
+        mma_ss<false>(ts, dq, d, id_s);
+#pragma unroll
+        for (int y = 1; y < D / 16; ++y) {
+            const uint32_t off = ((y >> 2) * (kTcRows * 128) + (y & 3) * 32) >> 4;
+            mma_ss<true>(ts, dq + off, d + off, id_s);
+        }
+        tc_commit(&bar[kSFull + s]);
+        tc_commit(&bar[kKEmpty + st]);
+        waits = true;
+        before = it;
+        first = j == 0;
+        last = j == g.tiles - 1;
+    }
+    if (waits) product_v(before, np, first, last);
+}
+
+template <int FMT, int D, bool SHARED>
+__global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_constant__ TreeArgs t,
+                                                                const __grid_constant__ CUtensorMap k_map,
+                                                                const __grid_constant__ CUtensorMap v_map)
+{
+    using P = TcPlan<FMT, D>;
+    constexpr bool kBf16 = FMT == QG_KV_BF16;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 512);
+    volatile int* odd_flag = reinterpret_cast<volatile int*>(smem + 520);   // a draft's value was not finite
+    const KvArgs& a = t.a;
+    const int lane = threadIdx.x & 31, warp = warp_index_uniform();
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // what earlier kernels wrote is read by bulk copies too
+    asm volatile("fence.proxy.async;" ::: "memory");
+    Cursor* from = reinterpret_cast<Cursor*>(smem + 576);    // where the CTA's one or two ranges begin
+    RawInfo* infos = reinterpret_cast<RawInfo*>(smem + 704);
+    int64_t* prefix = reinterpret_cast<int64_t*>(smem + P::kQ);
+    tree_prefix(t, prefix);
+    if (threadIdx.x == 32) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bar[kKFull + s], kBf16 ? 1 : kConvertWarps);
+            mbar_init(&bar[kKEmpty + s], SHARED ? 2 : 1);
+            mbar_init(&bar[kVFull + s], kBf16 ? 1 : kConvertWarps);
+            mbar_init(&bar[kVEmpty + s], SHARED ? 2 : 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar[kQFull + s], 4);
+            mbar_init(&bar[kSFull + s], 1);
+            mbar_init(&bar[kPFull + s], 4);
+            mbar_init(&bar[kODone + s], 1);
+        }
+        for (int s = 0; s < kMaxRaw; ++s) {
+            mbar_init(&bar[kRawFull + s], 1);
+            mbar_init(&bar[kRawEmpty + s], kConvertWarps);
+        }
+        mbar_init(&bar[kVLand], 1);
+        *odd_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tc_alloc(tmem_slot, 512);
+        tc_relinquish();
+    }
+    __syncthreads();
+    if (threadIdx.x < 2) from[threadIdx.x].locate(t, prefix, threadIdx.x * gridDim.x + blockIdx.x);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;                // S and P of stream s at 128 s, O at 256 + 128 s
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax
+        regs_up<kSoftmaxRegs>();
+        const int s = warp >> 2;
+        const int r = threadIdx.x & 127;             // row of the stream's tile = TMEM lane
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + 128 * s, to = tmem + lanes + 256 + 128 * s;
+        uint32_t n_s = 0, n_seg = 0;
+        bool ok = true;
+        Cursor mine = from[SHARED ? 0 : s];
+        Segment g;
+        while (ok && mine.next(t, g)) {
+            const int base = SHARED ? 128 * s : 0;
+            const int n_rows = g.n_rows - base;      // of this stream
+            if (n_rows <= 0) continue;
+            const bool on = r < n_rows;
+            const bool busy = 32 * (warp & 3) < n_rows;
+            const int row = g.row0 + base + (on ? r : 0);
+            const int tok = row / t.group, qh = g.head * t.group + row % t.group;
+            // ---- this row of Q, times a power of two that brings its largest value to f16's upper range
+            float rowf = 0.f;
+            {
+                uint32_t w[D / 2];
+                const uint4* src = reinterpret_cast<const uint4*>(t.q + (g.tok0 + tok) * t.q_stride + qh * D);
+                uint32_t mag = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 v = on ? src[i] : make_uint4(0, 0, 0, 0);
+                    w[4 * i] = v.x;
+                    w[4 * i + 1] = v.y;
+                    w[4 * i + 2] = v.z;
+                    w[4 * i + 3] = v.w;
+                }
+                int pe = 0;
+                if constexpr (!kBf16) {
+#pragma unroll
+                    for (int i = 0; i < D / 2; ++i) {
+                        const uint32_t m = w[i] & 0x7FFF7FFFu;
+                        mag = max(mag, max(m & 0xFFFFu, m >> 16));
+                    }
+                    pe = mag < 0x7F80u ? prescale_exponent(mag) : 0;
+                }
+                // a negative scale turns q round, so that larger products are always larger scores
+                const uint32_t flip = t.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t x = w[4 * i + e];
+                        if constexpr (kBf16)
+                            h[e] = x ^ flip;
+                        else
+                            h[e] = pack_f16x2(ldexp_exact(__uint_as_float(x << 16), pe),
+                                              ldexp_exact(__uint_as_float(x & 0xFFFF0000u), pe)) ^
+                                   flip;
+                    }
+                    *reinterpret_cast<uint4*>(smem + P::kQ + s * P::kTile + tile_at(r, i)) =
+                        make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                rowf = ldexp_exact(fabsf(t.scale) * kLog2e * a.g[0], -pe);
+            }
+            const uint64_t own = g.n_tok < 64 ? (1ull << g.n_tok) - 1 : ~0ull;
+            const uint64_t mask = (t.mask ? t.mask[g.tok0 + tok] : (2ull << tok) - 1) & own;
+            bool bad = false;                        // a page of these keys lies outside the cache
+            for (int p = g.first - g.first % a.page_size + lane * a.page_size; p < g.end; p += 32 * a.page_size)
+                bad = kv_page(a, g.b, p) < 0 || bad;
+            bad = __any_sync(0xffffffffu, bad);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[kQFull + s]);
+
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < g.tiles; ++j) {
+                ok = warp_wait(&bar[kSFull + s], n_s++ & 1u, t);
+                if (!ok) break;
+                tc_fence_after();
+                if (busy) {
+                    const int p0 = g.first + j * kTcKeys;
+                    const bool special = p0 + kTcKeys > g.len || bad;
+                    uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+                    if (special) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int off = p0 + 32 * c - g.len;
+                            seen[c] = off <= -32 ? ~0u
+                                      : off < 0  ? ((1u << -off) - 1u) | static_cast<uint32_t>(mask << -off)
+                                      : off < 64 ? static_cast<uint32_t>(mask >> off)
+                                                 : 0u;
+                            if (bad)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    const int p = p0 + 32 * c + 16 * x;
+                                    if (p < g.end && kv_page(a, g.b, p) < 0) seen[c] &= ~(0xFFFFu << (16 * x));
+                                }
+                        }
+                    }
+                    if (special)
+                        weights<kBf16, true, D>(ts, to, j > 0, rowf, seen, m, l);
+                    else
+                        weights<kBf16, false, D>(ts, to, j > 0, rowf, seen, m, l);
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kPFull + s]);
+            }
+            if (!ok) break;
+            ok = warp_wait(&bar[kODone + s], n_seg++ & 1u, t);
+            if (!ok) break;
+            tc_fence_after();
+            if (!busy) continue;
+            const int64_t h = static_cast<int64_t>(g.tok0 + tok) * t.q_heads + qh;
+            const float scale = g.slot < 0 ? tree_inverse(l) * a.g[1] : 1.f;
+            const int64_t at = static_cast<int64_t>(g.slot) * t.rows + base + r;
+            const bool fix = g.end > g.len && *odd_flag;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                __syncwarp();
+                tc_ld<32>(to + 32 * c, v);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = tc_after_wait(v[i]);
+                if (!on) continue;
+                if (fix) {
+                    // drafts' values that are not finite, left out of the tiles, to the rows that see them
+                    for (int p = max(g.first, g.len); p < g.end; ++p) {
+                        if (!((mask >> (p - g.len)) & 1ull)) continue;
+                        const int page = kv_page(a, g.b, p);
+                        if (page < 0) continue;
+                        const int64_t from = kv_row(a, page, g.head, p);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float x = kv_value(a, 1, from, 32 * c + i);
+                            if (!(fabsf(x) < INFINITY)) v[i] = __float_as_uint(__uint_as_float(v[i]) + x);
+                        }
+                    }
+                }
+                if (g.slot < 0) {
+                    uint4* dst = reinterpret_cast<uint4*>(t.out + h * D + 32 * c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            y[e] = l > 0.f || l != l
+                                       ? pack16<true>(__uint_as_float(v[8 * i + 2 * e]) * scale,
+                                                      __uint_as_float(v[8 * i + 2 * e + 1]) * scale)
+                                       : 0u;
+                        dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(t.part_o + at * D + 32 * c);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        dst[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                             __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                }
+            }
+            if (on) {
+                if (g.slot >= 0)
+                    t.part_ml[at] = make_float2(m - kTcOffset, l);
+                else if (t.lse)
+                    t.lse[h] = tree_lse(m - kTcOffset, l);
+            }
+        }
+    } else if (warp < kMmaWarp) {
+        regs_down<kLoadRegs>();
+        if constexpr (kBf16) {
+            const int kv = warp - 8;
+            if (kv < 2)
+                copy_plain<D, SHARED>(t, kv ? &v_map : &k_map, from, smem + (kv ? P::kV : P::kK),
+                                      &bar[kv ? kVFull : kKFull], &bar[kv ? kVEmpty : kKEmpty], &bar[kVLand], odd_flag,
+                                      kv);
+        } else {
+            convert<FMT, D>(t, smem, bar, infos, odd_flag, threadIdx.x - 256);
+        }
+    } else {
+        regs_down<kIssueRegs>();
+        if (warp < kMmaWarp + 2) {
+            if (lane == 0) multiply<FMT, D, SHARED>(t, from, smem, bar, tmem, warp - kMmaWarp);
+        } else if (!kBf16 && warp == kIssueWarp) {
+            if constexpr (!kBf16) copy_coded<FMT, D, SHARED>(t, from, smem, bar, infos);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+template <int FMT, int D, bool SHARED>
+cudaError_t run_tc(TreeArgs t, cudaStream_t stream)
+{
+    using P = TcPlan<FMT, D>;
+    auto kern = tree_tc_kernel<FMT, D, SHARED>;
+    // The warpgroups' registers are dealt out anew inside the kernel, which
+    // would wait for ever for more than the block was launched with.
+    static const bool fits = [&] {
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, kern) == cudaSuccess && f.numRegs >= kLaunchRegs;
+    }();
+    if (!fits) return cudaErrorInvalidConfiguration;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+    if (e != cudaSuccess) return e;
+    const int sms = sm_count(-1);
+    t.step = kTcKeys;
+    t.grid = SHARED ? sms : 2 * sms;
+    t.run = 16;
+    while (t.run < kTcKeys && t.a.page_size % (2 * t.run) == 0) t.run *= 2;
+    CUtensorMap maps[2] = {};
+    if (FMT == QG_KV_BF16)
+        for (int kv = 0; kv < 2; ++kv)
+            if (!encode_tmap_2d(&maps[kv], t.a.codes[kv], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D,
+                                static_cast<uint64_t>(t.a.num_pages) * t.a.heads * t.a.page_size, 64, t.run, true))
+                return cudaErrorInvalidValue;
+    e = launch_pdl(kern, dim3(static_cast<unsigned>(sms)), dim3(kTcThreads), P::kSmem, stream, t, maps[0], maps[1]);
+    if (e != cudaSuccess) return e;
+    return launch_tree_join(t, stream);
+}
+
+template <int FMT>
+cudaError_t run_tc_format(const TreeArgs& t, cudaStream_t stream)
+{
+    if (t.a.dim == 64)
+        return t.rows == 256 ? run_tc<FMT, 64, true>(t, stream) : run_tc<FMT, 64, false>(t, stream);
+    return t.rows == 256 ? run_tc<FMT, 128, true>(t, stream) : run_tc<FMT, 128, false>(t, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_tc(const TreeArgs& t, cudaStream_t stream)
+{
+    return t.a.fmt == QG_KV_BF16  ? run_tc_format<QG_KV_BF16>(t, stream)
+           : t.a.fmt == QG_KV_FP8 ? run_tc_format<QG_KV_FP8>(t, stream)
+                                  : run_tc_format<QG_KV_NVFP4>(t, stream);
+}
+
+}  // namespace qg
