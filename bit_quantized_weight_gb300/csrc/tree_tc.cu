@@ -23,9 +23,8 @@
 namespace qg {
 namespace {
 
-constexpr int kTcKeys = 128;                 // keys per tile
+constexpr int kTcKeys = 64;                  // keys per tile
 constexpr int kTcRows = 128;                 // rows per stream
-constexpr int kConvertWarps = 4;
 constexpr int kTcThreads = 512;               // four warpgroups, 128 registers per thread at launch ...
 constexpr int kMmaWarp = 12;                  // of stream 0; the next warp is stream 1's
 constexpr int kIssueWarp = 14;                // starts the copies of coded keys and values
@@ -34,8 +33,8 @@ constexpr int kSoftmaxRegs = 144;            // ... dealt out anew: 2 * 144 + 10
 constexpr int kLoadRegs = 104;
 constexpr int kIssueRegs = 120;
 static_assert(2 * kSoftmaxRegs + kLoadRegs + kIssueRegs <= 4 * kLaunchRegs, "more registers than the block has");
-constexpr int kStages = 2;                   // tiles of keys and of values
-constexpr int kMaxRaw = 4;                   // tiles as they are stored, before their conversion
+constexpr int kStages = 4;                   // tiles of keys and of values (SHARED; else two per stream)
+constexpr int kRawStages = 4;                // tiles as they are stored, one per converting warp
 // Weights are 2^(s - m + 8) with m a whole number from the row's largest score
 // (rounded up), replaced only once a score passes it by 7: a weight is at most
 // 2^15, within f16, the largest at least 2^7, and a change of m scales what was
@@ -49,48 +48,60 @@ enum Bar : int {
     kVFull = kKEmpty + kStages,
     kVEmpty = kVFull + kStages,
     kQFull = kVEmpty + kStages,              // [stream]
-    kSFull = kQFull + 2,
-    kPFull = kSFull + 2,
-    kODone = kPFull + 2,
-    kRawFull = kODone + 2,                   // [raw stage]
-    kRawEmpty = kRawFull + kMaxRaw,
-    kVLand = kRawEmpty + kMaxRaw,
-    kBars = kVLand + 1
+    kSFull = kQFull + 2,                     // [2 * stream + buffer]
+    kPFull = kSFull + 4,
+    kPvDone = kPFull + 4,
+    kRawFull = kPvDone + 4,                  // [raw stage]
+    kRawEmpty = kRawFull + kRawStages,
+    kVLand = kRawEmpty + kRawStages,
+    kDrain = kVLand + 1,                     // [stream]
+    kBars = kDrain + 2
 };
 
 template <int FMT, int D>
 struct TcPlan {
-    static constexpr int kTile = kTcKeys * D * 2;        // bytes of a tile of Q, K or V
+    static constexpr int kQTile = kTcRows * D * 2;
+    static constexpr int kTile = kTcKeys * D * 2;        // of keys or values, as f16 or bf16
     static constexpr int kHead = 1024;                   // barriers and what the warps tell each other
     static constexpr int kQ = kHead;
-    static constexpr int kK = kQ + 2 * kTile;
+    static constexpr int kK = kQ + 2 * kQTile;
     static constexpr int kV = kK + kStages * kTile;
     static constexpr int kRaw = kV + kStages * kTile;
     static constexpr int kCodes = kTcKeys * kv_row_bytes(FMT, D);
     static constexpr int kRawStage = FMT == QG_KV_BF16 ? 0 : kCodes + kTcKeys * kv_scale_bytes(FMT, D);
-    static constexpr int kRoom = 227 * 1024 - 1024 - kRaw;               // 1024 for alignment
-    static constexpr int kFit = kRawStage ? kRoom / (kRawStage ? kRawStage : 1) : 0;
-    static constexpr int kNRaw = kFit > kMaxRaw ? kMaxRaw : kFit;
-    static constexpr int kSmem = kRaw + kNRaw * kRawStage + 1024;
-    static_assert(FMT == QG_KV_BF16 || kNRaw >= 2, "too little shared memory");
-    static_assert(6 * kTile >= (kKvMaxSeqs + 1) * 8, "prefix sums lie where the tiles go");
+    static constexpr int kSmem = kRaw + kRawStages * kRawStage + 1024;   // + alignment
+    static_assert(kSmem <= 227 * 1024, "too much shared memory");
+    static_assert(2 * kQTile >= (kKvMaxSeqs + 1) * 8, "prefix sums lie where Q goes");
+    static_assert(kBars * 8 <= 512, "barriers");
 };
 
-// Operand tiles lie as blocks of 64 columns (128 bytes) by 128 rows, the
+// Operand tiles lie as blocks of 64 columns (128 bytes) by ROWS rows, the
 // 16-byte pieces of a row permuted by the row's low three bits (the 128-byte
 // swizzle). Byte offset of piece `ch` (of 8 values) of `row`.
+template <int ROWS>
 __device__ __forceinline__ uint32_t tile_at(int row, int ch)
 {
-    return (ch >> 3) * (kTcRows * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+    return (ch >> 3) * (ROWS * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
 }
 
 // Descriptors of such a tile. K-major (Q, K): eight rows are 1024 bytes apart.
-// N-major (V): 64-column blocks are 16 KB apart, eight keys 1024 bytes.
+// N-major (V): 64-column blocks are `lbo` apart, eight keys 1024 bytes.
 __device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, uint32_t lbo)
 {
     return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
            static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
 }
+
+// The n-th tile of a ring: its stage, and the parity of the phase in which it
+// is filled. SHARED, one ring for both streams; else each stream has half.
+template <bool SHARED>
+struct Stage {
+    uint32_t at, parity;
+    __device__ __forceinline__ Stage(int stream, uint32_t n)
+        : at(SHARED ? n % kStages : 2 * stream + n % 2), parity(SHARED ? n / kStages & 1u : n / 2 & 1u)
+    {
+    }
+};
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi)
@@ -241,11 +252,13 @@ struct RawInfo {
     int left;                    // keys of the tile, -1: there are no more tiles
     int drafts;                  // its keys from here on are drafts
     uint32_t groups;             // groups of 16 keys whose page lies in the cache
-    int pad;
+    uint32_t stage;              // where it goes, and the parity of its phase there
+    uint32_t parity;
+    int pad[3];
 };
 
 // The runs of a tile: consecutive keys of one page, t.run of them (the largest
-// of 16, 32, 64 and 128 that divides the page size), one lane each. The page
+// of 16, 32 and 64 that divides the page size), one lane each. The page
 // table is read a tile ahead.
 template <bool SHARED>
 struct Runs {
@@ -256,29 +269,33 @@ struct Runs {
     RawInfo info;
     bool more;
     Segment g;
-    int j, entry;
-    bool ahead;
+    int j, entry, owner;
+    uint32_t n[2];               // tiles of each ring so far
 
     __device__ __forceinline__ int key() const { return (threadIdx.x & 31); }
 
     __device__ __forceinline__ void look_up(const TreeArgs& t)
     {
         const int p = g.first + j * kTcKeys + key() * t.run;
-        entry = ahead && key() * t.run < kTcKeys && p < g.end ? kv_entry(t.a, g.b, p) : 0;
+        entry = owner >= 0 && key() * t.run < kTcKeys && p < g.end ? kv_entry(t.a, g.b, p) : 0;
     }
 
     __device__ __forceinline__ void start(const TreeArgs& t, const Cursor* from)
     {
         items.start(t, from);
-        ahead = items.next(t, g, j) >= 0;
+        n[0] = n[1] = 0;
+        owner = items.next(t, g, j);
         look_up(t);
         step(t);
     }
 
     __device__ __forceinline__ void step(const TreeArgs& t)
     {
-        more = ahead;
+        more = owner >= 0;
         if (!more) return;
+        const Stage<SHARED> st(owner, owner ? n[1]++ : n[0]++);
+        info.stage = st.at;
+        info.parity = st.parity;
         const int p0 = g.first + j * kTcKeys, k0 = key() * t.run;
         info.left = min(kTcKeys, g.end - p0);
         info.drafts = g.len - p0;
@@ -288,14 +305,14 @@ struct Runs {
         row = on ? kv_row(t.a, page, g.head, p0 + k0) : 0;
         keys = on ? min(t.run, (info.left - k0 + 15) & ~15) : 0;
         info.groups = __reduce_or_sync(0xffffffffu, on ? ((1u << (keys >> 4)) - 1u) << (k0 >> 4) : 0u);
-        ahead = items.next(t, g, j) >= 0;
+        owner = items.next(t, g, j);
         look_up(t);
     }
 
     // Some of the tile's places get no key of the context.
     __device__ __forceinline__ static bool special(const RawInfo& i)
     {
-        return i.left < kTcKeys || i.drafts < kTcKeys || i.groups != 0xFFu;
+        return i.left < kTcKeys || i.drafts < kTcKeys || i.groups != (1u << (kTcKeys / 16)) - 1u;
     }
 };
 
@@ -345,16 +362,17 @@ __device__ __forceinline__ void drop_odd(uint4& v, bool& odd)
     }
 }
 
-// A warp's part of a tile is in place: visible to the tensor core, then counted.
-__device__ __forceinline__ void announce(uint64_t* bar, int starve)
+// What a warp wrote of a tile is in place: visible to the tensor core, then counted.
+__device__ __forceinline__ void announce(uint64_t* bar)
 {
     fence_proxy_async_smem();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0 && !starve) mbar_arrive(bar);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // Coded keys and values: one warp starts the copies of the tiles as they are
-// stored, keys and values in turn.
+// stored, keys and values in turn, into four raw stages. On a timeout it waits
+// for the copies that are on their way.
 template <int FMT, int D, bool SHARED>
 __device__ __forceinline__ void copy_coded(const TreeArgs& t, const Cursor* from, uint8_t* smem, uint64_t* bar,
                                            RawInfo* infos)
@@ -365,17 +383,14 @@ __device__ __forceinline__ void copy_coded(const TreeArgs& t, const Cursor* from
     const int lane = threadIdx.x & 31;
     Runs<SHARED> runs;
     runs.start(t, from);
-    uint32_t r = 0, ph = 1;                                  // raw stage, parity of its being empty
-    auto turn = [&]() {
-        if (++r == P::kNRaw) {
-            r = 0;
-            ph ^= 1u;
-        }
-    };
-    while (runs.more) {
+    uint32_t job = 0;
+    bool ok = true;
+    while (ok && runs.more) {
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-            if (!warp_wait(&bar[kRawEmpty + r], ph, t)) return;
+        for (int kv = 0; kv < 2; ++kv, ++job) {
+            const uint32_t r = job % kRawStages;
+            ok = warp_wait(&bar[kRawEmpty + r], (job / kRawStages & 1u) ^ 1u, t);
+            if (!ok) break;
             const uint32_t bytes = __popc(runs.info.groups) * 16 * (kRow + kScale);
             uint8_t* dst = smem + P::kRaw + r * P::kRawStage;
             if (lane == 0) {
@@ -389,86 +404,86 @@ __device__ __forceinline__ void copy_coded(const TreeArgs& t, const Cursor* from
                 bulk_load(dst + P::kCodes + k0 * kScale, a.scales[kv] + runs.row * kScale, runs.keys * kScale,
                           &bar[kRawFull + r]);
             }
-            turn();
         }
-        runs.step(t);
+        if (ok) runs.step(t);
     }
-    if (!warp_wait(&bar[kRawEmpty + r], ph, t)) return;
-    if (lane == 0) {
-        infos[r].left = -1;
-        mbar_arrive(&bar[kRawFull + r]);
+    if (!ok) {
+        if (!t.starve)
+            for (uint32_t x = job > kRawStages ? job - kRawStages : 0; x < job; ++x)
+                warp_wait(&bar[kRawFull + x % kRawStages], x / kRawStages & 1u, t);
+        return;
+    }
+    for (int x = 0; x < kRawStages; ++x, ++job) {                // no more: to every converting warp
+        const uint32_t r = job % kRawStages;
+        if (!warp_wait(&bar[kRawEmpty + r], (job / kRawStages & 1u) ^ 1u, t)) return;
+        if (lane == 0) {
+            infos[r].left = -1;
+            mbar_arrive(&bar[kRawFull + r]);
+        }
     }
 }
 
-// ... and four warps convert them to f16 tiles. Drafts' values that are not
-// finite are left out (0 times them would reach rows that do not see the
-// draft) and flagged for the epilogue; what no key fills is zero.
+// ... and four warps, each a raw stage and every fourth tile of its own,
+// convert them to f16 tiles. Drafts' values that are not finite are left out
+// (0 times them would reach rows that do not see the draft) and flagged for the
+// epilogue; what no key fills is zero.
 template <int FMT, int D>
 __device__ __forceinline__ void convert(const TreeArgs& t, uint8_t* smem, uint64_t* bar, const RawInfo* infos,
-                                        volatile int* odd_flag, int tid)
+                                        volatile int* odd_flag, int r)
 {
     using P = TcPlan<FMT, D>;
     constexpr int kRow = kv_row_bytes(FMT, D), kScale = kv_scale_bytes(FMT, D);
     constexpr int kPerKey = kRow / 16;                       // pieces of a row
-    constexpr int kKeys = 32 * kConvertWarps / kPerKey;      // keys that the threads convert at a time
+    constexpr int kN = kTcKeys * kPerKey / 32;               // pieces per lane
     constexpr int kChunks = FMT == QG_KV_FP8 ? 2 : 4;        // pieces of eight f16 from one of codes
-    const int c = tid % kPerKey;
-    uint32_t r = 0, ph = 0;
-    for (uint32_t it = 0;; ++it) {
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-            if (!warp_wait(&bar[kRawFull + r], ph, t)) return;
-            const RawInfo info = infos[r];
-            if (info.left < 0) return;
-            const uint32_t st = it & 1u;
-            if (!warp_wait(&bar[(kv ? kVEmpty : kKEmpty) + st], ((it >> 1) & 1u) ^ 1u, t)) return;
-            const uint32_t src = smem_u32(smem + P::kRaw + r * P::kRawStage);
-            uint8_t* tile = smem + (kv ? P::kV : P::kK) + st * P::kTile;
-            auto piece = [&](int n, uint4* out) {
-                const int key = n * kKeys + tid / kPerKey;
-                const uint32_t at = src + P::kCodes + key * kScale;
-                piece_values<FMT>(lds128(src + (n * 32 * kConvertWarps + tid) * 16),
-                                  FMT == QG_KV_FP8 ? lds8(at) : lds16(at + 2 * c), out);
-                return key;
-            };
-            if (kv == 0 || !Runs<false>::special(info)) {
+    const int lane = threadIdx.x & 31, c = lane % kPerKey, kv = r & 1;
+    const uint32_t src = smem_u32(smem + P::kRaw + r * P::kRawStage);
+    for (uint32_t n = 0;; ++n) {
+        if (!warp_wait(&bar[kRawFull + r], n & 1u, t)) return;
+        const RawInfo info = infos[r];
+        if (info.left < 0) return;
+        if (!warp_wait(&bar[(kv ? kVEmpty : kKEmpty) + info.stage], info.parity ^ 1u, t)) return;
+        uint8_t* tile = smem + (kv ? P::kV : P::kK) + info.stage * P::kTile;
+        auto piece = [&](int x, uint4* out) {
+            const int key = (x * 32 + lane) / kPerKey;
+            const uint32_t at = src + P::kCodes + key * kScale;
+            piece_values<FMT>(lds128(src + (x * 32 + lane) * 16), FMT == QG_KV_FP8 ? lds8(at) : lds16(at + 2 * c), out);
+            return key;
+        };
+        if (kv == 0 || !Runs<false>::special(info)) {
 #pragma unroll 4
-                for (int n = 0; n < kPerKey; ++n) {
-                    uint4 out[kChunks];
-                    const int key = piece(n, out);
+            for (int x = 0; x < kN; ++x) {
+                uint4 out[kChunks];
+                const int key = piece(x, out);
 #pragma unroll
-                    for (int i = 0; i < kChunks; ++i)
-                        *reinterpret_cast<uint4*>(tile + tile_at(key, c * kChunks + i)) = out[i];
-                }
-            } else {
-                bool odd = false;
+                for (int i = 0; i < kChunks; ++i)
+                    *reinterpret_cast<uint4*>(tile + tile_at<kTcKeys>(key, c * kChunks + i)) = out[i];
+            }
+        } else {
+            bool odd = false;
 #pragma unroll 1
-                for (int n = 0; n < kPerKey; ++n) {
-                    uint4 out[kChunks];
-                    const int key = piece(n, out);
-                    const bool on = key < info.left && ((info.groups >> (key >> 4)) & 1u);
+            for (int x = 0; x < kN; ++x) {
+                uint4 out[kChunks];
+                const int key = piece(x, out);
+                const bool on = key < info.left && ((info.groups >> (key >> 4)) & 1u);
 #pragma unroll
-                    for (int i = 0; i < kChunks; ++i) {
-                        if (!on) out[i] = make_uint4(0, 0, 0, 0);
-                        if (key >= info.drafts) drop_odd<false>(out[i], odd);
-                        *reinterpret_cast<uint4*>(tile + tile_at(key, c * kChunks + i)) = out[i];
-                    }
+                for (int i = 0; i < kChunks; ++i) {
+                    if (!on) out[i] = make_uint4(0, 0, 0, 0);
+                    if (key >= info.drafts) drop_odd<false>(out[i], odd);
+                    *reinterpret_cast<uint4*>(tile + tile_at<kTcKeys>(key, c * kChunks + i)) = out[i];
                 }
-                if (odd) *odd_flag = 1;
             }
-            announce(&bar[(kv ? kVFull : kKFull) + st], 0);
-            if ((tid & 31) == 0) mbar_arrive(&bar[kRawEmpty + r]);
-            if (++r == P::kNRaw) {
-                r = 0;
-                ph ^= 1u;
-            }
+            if (odd) *odd_flag = 1;
         }
+        announce(&bar[(kv ? kVFull : kKFull) + info.stage]);
+        if (lane == 0) mbar_arrive(&bar[kRawEmpty + r]);
     }
 }
 
 // bf16 keys (kv = 0) or values (1): copied straight into the tiles, swizzled on
 // the way, by one warp each. A tile of values with places to clear is announced
-// by this warp once it has done so.
+// by this warp once it has done so. On a timeout it waits for the copies that
+// are on their way.
 template <int D, bool SHARED>
 __device__ __forceinline__ void copy_plain(const TreeArgs& t, const CUtensorMap* map, const Cursor* from,
                                            uint8_t* tiles, uint64_t* full, uint64_t* empty, uint64_t* land,
@@ -478,21 +493,28 @@ __device__ __forceinline__ void copy_plain(const TreeArgs& t, const CUtensorMap*
     const int lane = threadIdx.x & 31;
     Runs<SHARED> runs;
     runs.start(t, from);
-    uint32_t landed = 0;
-    for (uint32_t it = 0; runs.more; ++it) {
-        const uint32_t st = it & 1u;
-        if (!warp_wait(&empty[st], ((it >> 1) & 1u) ^ 1u, t)) return;
+    uint32_t landed = 0, filled = 0, parities = 0;               // stages ever filled, the parity of their last phase
+    const bool go = kv == 1 || !t.starve;
+    for (; runs.more; runs.step(t)) {
+        const uint32_t st = runs.info.stage;
+        if (!warp_wait(&empty[st], runs.info.parity ^ 1u, t)) {
+            if (go)
+                for (uint32_t x = 0; x < kStages; ++x)
+                    if (filled >> x & 1u) warp_wait(&full[x], parities >> x & 1u, t);
+            return;
+        }
+        filled |= 1u << st;
+        parities = (parities & ~(1u << st)) | runs.info.parity << st;
         const bool clear = kv == 1 && Runs<SHARED>::special(runs.info);
         uint64_t* done = clear ? land : &full[st];
         // boxes are whole runs: what lies behind the last key is cleared or masked
         const uint32_t n_runs = __popc(__ballot_sync(0xffffffffu, runs.on));
-        const bool go = kv == 1 || !t.starve;
         if (lane == 0 && go) mbar_arrive_expect_tx(done, n_runs * t.run * D * 2);
         __syncwarp();
         if (runs.on && go)
 #pragma unroll
             for (int x = 0; x < D / 64; ++x)
-                tma_load_2d(tiles + st * kTile + x * (kTcRows * 128) + lane * t.run * 128, map, 64 * x,
+                tma_load_2d(tiles + st * kTile + x * (kTcKeys * 128) + lane * t.run * 128, map, 64 * x,
                             static_cast<int32_t>(runs.row), done);
         if (clear) {
             if (!warp_wait(land, landed++ & 1u, t)) return;
@@ -501,15 +523,14 @@ __device__ __forceinline__ void copy_plain(const TreeArgs& t, const CUtensorMap*
                 const int key = x / (D / 8);
                 const bool on = key < runs.info.left && ((runs.info.groups >> (key >> 4)) & 1u);
                 if (on && key < runs.info.drafts) continue;
-                uint4* at = reinterpret_cast<uint4*>(tiles + st * kTile + tile_at(key, x % (D / 8)));
+                uint4* at = reinterpret_cast<uint4*>(tiles + st * kTile + tile_at<kTcKeys>(key, x % (D / 8)));
                 uint4 y = on ? *at : make_uint4(0, 0, 0, 0);
                 drop_odd<true>(y, odd);
                 *at = y;
             }
             if (odd) *odd_flag = 1;
-            announce(&full[st], 0);
+            announce(&full[st]);
         }
-        runs.step(t);
     }
 }
 
@@ -538,120 +559,88 @@ __device__ __forceinline__ f2 f2_add(f2 a, f2 b)
     return r;
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t mul16x2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    if constexpr (BF16)
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    else
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// A row's scores became too large for its m: m is raised, and what was summed
-// with the old one is scaled: l, the row of O, and the weights of this tile
-// that are already written (`pieces` of 32 keys). Rare, so small rather than
-// fast.
-template <bool BF16, int D>
-__device__ __forceinline__ void raise_max(uint32_t ts, uint32_t to, bool has_o, int pieces, float top, float& m,
-                                          float& l)
-{
-    const float mn = fmaxf(m, ceilf(top));
-    const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
-    m = mn;
-    l *= f;
-    uint32_t v[16];
-    if (has_o) {                             // the products of the tiles before are complete: S came after them
-#pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-            tc_ld<16>(to + 16 * c, v);
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(tc_after_wait(v[i])) * f);
-            tc_st_x16(to + 16 * c, v);
-        }
-    }
-    const uint32_t f16 = pack16<BF16>(f, f);
-#pragma unroll 1
-    for (int c = 0; c < pieces; ++c) {
-        tc_ld<16>(ts + 16 * c, v);
-        tc_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = mul16x2<BF16>(tc_after_wait(v[i]), f16);
-        tc_st_x16(ts + 16 * c, v);
-    }
-    tc_wait_st();
-}
-
-// One tile's scores of this thread's row to weights, in place: the weights of
-// 32 keys take the columns of 16 scores that were read before.
+// One tile's 64 scores of this thread's row to weights, in place: the weights
+// of 32 keys take the columns of 16 scores that were read before. A row whose
+// scores became too large for its m has m raised, and what was summed with the
+// old one is scaled: l and the row of O, once the products of the tile before
+// are complete (those before it are: they came ahead of these scores). That is
+// rare, so small rather than fast.
 template <bool BF16, bool SPECIAL, int D>
-__device__ __forceinline__ void weights(uint32_t ts, uint32_t to, bool has_o, float rowf, const uint32_t (&seen)[4],
-                                        float& m, float& l)
+__device__ __forceinline__ bool weights(const TreeArgs& t, uint32_t ts, uint32_t to, uint64_t* before, uint32_t parity,
+                                        float rowf, const uint32_t (&seen)[2], float& m, float& l)
 {
-    f2 sum[2] = {0, 0};
     const f2 rowf2 = f2_pack(rowf, rowf);
+    uint32_t x[64];
+    tc_ld<32>(ts, x);
+    tc_ld<32>(ts + 32, x + 32);
+    tc_wait_ld();
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        uint32_t x[64];
-        tc_ld<32>(ts + 64 * c, x);
-        tc_ld<32>(ts + 64 * c + 32, x + 32);
-        tc_wait_ld();
+    for (int i = 0; i < 64; ++i) x[i] = tc_after_wait(x[i]);
+    if constexpr (SPECIAL) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) x[i] = tc_after_wait(x[i]);
-        if constexpr (SPECIAL) {
+        for (int i = 0; i < 64; ++i)
+            if (!((seen[i / 32] >> (i & 31)) & 1u)) x[i] = 0xFF800000u;
+    }
+    float mx[4];
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (!((seen[2 * c + i / 32] >> (i & 31)) & 1u)) x[i] = 0xFF800000u;
-        }
-        float mx[4];
+    for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
+    for (int i = 8; i < 64; i += 8)
 #pragma unroll
-        for (int i = 8; i < 64; i += 8)
+        for (int e = 0; e < 4; ++e)
+            mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(x[i + e])), __uint_as_float(x[i + e + 4]));
+    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rowf;
+    if (__any_sync(0xffffffffu, top > m + kTcLazy)) {
+        const float mn = fmaxf(m, ceilf(top));
+        const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+        m = mn;
+        l *= f;
+        if (before) {
+            if (!warp_wait(before, parity, t)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t v[16];
+                tc_ld<16>(to + 16 * c, v);
+                tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(x[i + e])), __uint_as_float(x[i + e + 4]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rowf;
-        if (__any_sync(0xffffffffu, top > m + kTcLazy)) {
-            float a, b, a1, b1;
-            f2_unpack(sum[0], a, a1);
-            f2_unpack(sum[1], b, b1);
-            l += (a + a1) + (b + b1);
-            sum[0] = sum[1] = 0;
-            raise_max<BF16, D>(ts, to, has_o, 2 * c, top, m, l);
-        }
-        const float z = kTcOffset - (m == -INFINITY ? 0.f : m);
-        const f2 z2 = f2_pack(z, z);
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            uint32_t h[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                float x0, x1;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(x[32 * y + i]), __uint_as_float(x[32 * y + i + 1])), rowf2,
-                                 z2),
-                          x0, x1);
-                x0 = ex2(x0);
-                x1 = ex2(x1);
-                if constexpr (SPECIAL) {     // also where m is still -infinity, or the scale is 0
-                    x0 = (seen[2 * c + y] >> i) & 1u ? x0 : 0.f;
-                    x1 = (seen[2 * c + y] >> (i + 1)) & 1u ? x1 : 0.f;
-                }
-                sum[(i >> 1) & 1] = f2_add(sum[(i >> 1) & 1], f2_pack(x0, x1));
-                h[i / 2] = pack16<BF16>(x0, x1);
+                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(tc_after_wait(v[i])) * f);
+                tc_st_x16(to + 16 * c, v);
             }
-            tc_st_x16(ts + 32 * c + 16 * y, h);
         }
+    }
+    const float z = kTcOffset - (m == -INFINITY ? 0.f : m);
+    const f2 z2 = f2_pack(z, z);
+    f2 sum[2] = {0, 0};
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        uint32_t h[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[32 * y + i]), __uint_as_float(x[32 * y + i + 1])), rowf2, z2),
+                      x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            if constexpr (SPECIAL) {         // also where m is still -infinity, or the scale is 0
+                x0 = (seen[y] >> i) & 1u ? x0 : 0.f;
+                x1 = (seen[y] >> (i + 1)) & 1u ? x1 : 0.f;
+            }
+            sum[(i >> 1) & 1] = f2_add(sum[(i >> 1) & 1], f2_pack(x0, x1));
+            h[i / 2] = pack16<BF16>(x0, x1);
+        }
+        tc_st_x16(ts + 16 * y, h);
     }
     float a, b, a1, b1;
     f2_unpack(sum[0], a, a1);
     f2_unpack(sum[1], b, b1);
     l += (a + a1) + (b + b1);
+    tc_wait_st();
+    return true;
 }
 
 // ------------------------------------------------------------------ products
+// One MMA with both operands in shared memory.
 template <bool ACCUMULATE>
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc)
 {
@@ -662,71 +651,92 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_
         : "memory");
 }
 
-// One thread per stream issues its products: S of a tile, and once its weights
-// are there O += P V, then S of the next tile over them. (The tensor core
-// takes one thread's products in order.)
+// One warp per stream issues its products: S of a tile into one of two
+// buffers, and O += P V once the weights have taken its place; S runs two tiles
+// ahead of P V, so that scores are ready when the softmax warps want them. (The
+// tensor core takes one thread's products in order: S of a tile overwrites
+// weights that the P V two tiles before it, issued before, has read.) The whole
+// warp walks the tiles, so that what addresses them stays in uniform registers;
+// one lane issues.
 template <int FMT, int D, bool SHARED>
-__device__ __forceinline__ void multiply(const TreeArgs& t, const Cursor* from, uint8_t* smem, uint64_t* bar, uint32_t tmem,
-                                         int s)
+__device__ __forceinline__ bool multiply(const TreeArgs& t, const Cursor* from, uint8_t* smem, uint64_t* bar,
+                                         uint32_t tmem, int s, bool leader)
 {
     using P = TcPlan<FMT, D>;
     constexpr bool kBf16 = FMT == QG_KV_BF16;
     constexpr uint32_t id_s = tc_idesc_f16(128, kTcKeys, kBf16);
     constexpr uint32_t id_o = tc_idesc_f16(128, D, kBf16) | 1u << 16;   // B is N-major
-    const uint64_t dq = tile_desc(smem_u32(smem + P::kQ) + s * P::kTile, 16);
+    const uint64_t dq = tile_desc(smem_u32(smem + P::kQ) + s * P::kQTile, 16);
     const uint64_t dk = tile_desc(smem_u32(smem + P::kK), 16);
-    const uint64_t dv = tile_desc(smem_u32(smem + P::kV), kTcRows * 128);
-    const uint32_t ts = tmem + 128 * s, to = tmem + 256 + 128 * s;
-    auto wait = [&](int b, uint32_t parity) { return mbar_wait_bounded(&bar[b], parity, t.wait_ns, t.a.status); };
-    auto product_v = [&](uint32_t it, uint32_t np, bool first, bool last) {
-        const uint32_t st = it & 1u;
-        if (!wait(kVFull + st, (it >> 1) & 1u) || !wait(kPFull + s, np & 1u)) return false;
+    const uint64_t dv = tile_desc(smem_u32(smem + P::kV), kTcKeys * 128);
+    const uint32_t ts = tmem + 256 * s, to = ts + 128;
+    auto wait = [&](int b, uint32_t parity) { return warp_wait(&bar[b], parity, t); };
+    uint32_t n = 0, x = 0, y = 0, nq = 0;            // ring position; tiles with S and with P V issued; segments
+    uint32_t starts = 0;                             // bit x % 32: tile x is its segment's first
+    uint32_t rings[2] = {0, 0};                      // ring positions of the tiles between y and x
+    auto product_v = [&]() {
+        const uint32_t buf = y & 1u;
+        const Stage<SHARED> st(s, buf ? rings[1] : rings[0]);
+        if (!wait(kVFull + st.at, st.parity) || !wait(kPFull + 2 * s + buf, y / 2 & 1u)) return false;
         tc_fence_after();
-        const uint64_t d = dv + st * (P::kTile >> 4);
-        tc_mma_f16_ts(to, ts, d, id_o, !first);
+        const uint64_t d = dv + st.at * (P::kTile >> 4);
+        const uint32_t tp = ts + 64 * buf;
+        const bool keep = !(starts >> (y & 31u) & 1u);
+        if (leader) {
+            tc_mma_f16_ts(to, tp, d, id_o, keep);
 #pragma unroll
-        for (int x = 1; x < kTcKeys / 16; ++x) tc_mma_f16_ts(to, ts + 8 * x, d + x * (2048 >> 4), id_o, true);
-        tc_commit(&bar[kVEmpty + st]);
-        if (last) tc_commit(&bar[kODone + s]);
+            for (int i = 1; i < kTcKeys / 16; ++i) tc_mma_f16_ts(to, tp + 8 * i, d + i * (2048 >> 4), id_o, true);
+            tc_commit(&bar[kVEmpty + st.at]);
+            tc_commit(&bar[kPvDone + 2 * s + buf]);
+        }
+        __syncwarp();
+        ++y;
         return true;
     };
     Items<SHARED> items;
     items.start(t, from);
     Segment g;
     int j, owner;
-    uint32_t np = 0, nq = 0, before = 0;
-    bool waits = false, first = false, last = false;     // a product P V of tile `before`
-    for (uint32_t it = 0; (owner = items.next(t, g, j)) >= 0; ++it) {
-        const uint32_t st = it & 1u;
-        if (SHARED && s == 1 && g.n_rows <= kTcRows) {   // the other stream's alone: only counted
-            if (waits && !product_v(before, np++, first, last)) return;
-            waits = false;
-            if (!wait(kKFull + st, (it >> 1) & 1u)) return;
-            mbar_arrive(&bar[kKEmpty + st]);
-            if (!wait(kVFull + st, (it >> 1) & 1u)) return;
-            mbar_arrive(&bar[kVEmpty + st]);
+    while ((owner = items.next(t, g, j)) >= 0) {
+        if (!SHARED && owner != s) continue;
+        // before a segment's first S everything of the one before is issued: its Q is replaced after its epilogue
+        const bool idle = SHARED && s == 1 && g.n_rows <= kTcRows;      // the other stream's tile alone
+        while (y < x && (j == 0 || idle || x - y == 2))
+            if (!product_v()) return false;
+        const Stage<SHARED> st(s, n);
+        if (!wait(kKFull + st.at, st.parity)) return false;
+        if (idle) {                                  // only counted
+            if (leader) mbar_arrive(&bar[kKEmpty + st.at]);
+            if (!wait(kVFull + st.at, st.parity)) return false;
+            if (leader) mbar_arrive(&bar[kVEmpty + st.at]);
+            ++n;
             continue;
         }
-        if (!SHARED && owner != s) continue;
-        if (waits && !product_v(before, np++, first, last)) return;
-        if (!wait(kKFull + st, (it >> 1) & 1u)) return;
-        if (j == 0 && !wait(kQFull + s, nq++ & 1u)) return;
+        if (j == 0 && !wait(kQFull + s, nq++ & 1u)) return false;
         tc_fence_after();
-        const uint64_t d = dk + st * (P::kTile >> 4);
-        mma_ss<false>(ts, dq, d, id_s);
+        const uint32_t buf = x & 1u;
+        if (leader) {
+            const uint64_t d = dk + st.at * (P::kTile >> 4);
+            mma_ss<false>(ts + 64 * buf, dq, d, id_s);
 #pragma unroll
-        for (int y = 1; y < D / 16; ++y) {
-            const uint32_t off = ((y >> 2) * (kTcRows * 128) + (y & 3) * 32) >> 4;
-            mma_ss<true>(ts, dq + off, d + off, id_s);
+            for (int i = 1; i < D / 16; ++i)
+                mma_ss<true>(ts + 64 * buf, dq + (((i >> 2) * (kTcRows * 128) + (i & 3) * 32) >> 4),
+                             d + (((i >> 2) * (kTcKeys * 128) + (i & 3) * 32) >> 4), id_s);
+            tc_commit(&bar[kSFull + 2 * s + buf]);
+            tc_commit(&bar[kKEmpty + st.at]);
         }
-        tc_commit(&bar[kSFull + s]);
-        tc_commit(&bar[kKEmpty + st]);
-        waits = true;
-        before = it;
-        first = j == 0;
-        last = j == g.tiles - 1;
+        __syncwarp();
+        starts = (starts & ~(1u << (x & 31u))) | static_cast<uint32_t>(j == 0) << (x & 31u);
+        if (buf)
+            rings[1] = n;
+        else
+            rings[0] = n;
+        ++n;
+        ++x;
     }
-    if (waits) product_v(before, np, first, last);
+    while (y < x)
+        if (!product_v()) return false;
+    return true;
 }
 
 template <int FMT, int D, bool SHARED>
@@ -749,25 +759,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
     // what earlier kernels wrote is read by bulk copies too
     asm volatile("fence.proxy.async;" ::: "memory");
     Cursor* from = reinterpret_cast<Cursor*>(smem + 576);    // where the CTA's one or two ranges begin
-    RawInfo* infos = reinterpret_cast<RawInfo*>(smem + 704);
+    RawInfo* infos = reinterpret_cast<RawInfo*>(smem + 640);
     int64_t* prefix = reinterpret_cast<int64_t*>(smem + P::kQ);
     tree_prefix(t, prefix);
     if (threadIdx.x == 32) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bar[kKFull + s], kBf16 ? 1 : kConvertWarps);
+            mbar_init(&bar[kKFull + s], 1);
             mbar_init(&bar[kKEmpty + s], SHARED ? 2 : 1);
-            mbar_init(&bar[kVFull + s], kBf16 ? 1 : kConvertWarps);
+            mbar_init(&bar[kVFull + s], 1);
             mbar_init(&bar[kVEmpty + s], SHARED ? 2 : 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar[kQFull + s], 4);
-            mbar_init(&bar[kSFull + s], 1);
-            mbar_init(&bar[kPFull + s], 4);
-            mbar_init(&bar[kODone + s], 1);
+            mbar_init(&bar[kDrain + s], 1);
         }
-        for (int s = 0; s < kMaxRaw; ++s) {
-            mbar_init(&bar[kRawFull + s], 1);
-            mbar_init(&bar[kRawEmpty + s], kConvertWarps);
+        for (int x = 0; x < 4; ++x) {
+            mbar_init(&bar[kSFull + x], 1);
+            mbar_init(&bar[kPFull + x], 4);
+            mbar_init(&bar[kPvDone + x], 1);
+        }
+        for (int x = 0; x < kRawStages; ++x) {
+            mbar_init(&bar[kRawFull + x], 1);
+            mbar_init(&bar[kRawEmpty + x], 1);
         }
         mbar_init(&bar[kVLand], 1);
         *odd_flag = 0;
@@ -782,7 +795,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;                // S and P of stream s at 128 s, O at 256 + 128 s
+    const uint32_t tmem = *tmem_slot;                // stream s: S and P at 256 s (two buffers), O at 256 s + 128
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
@@ -790,8 +803,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
         const int s = warp >> 2;
         const int r = threadIdx.x & 127;             // row of the stream's tile = TMEM lane
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t ts = tmem + lanes + 128 * s, to = tmem + lanes + 256 + 128 * s;
-        uint32_t n_s = 0, n_seg = 0;
+        const uint32_t ts = tmem + lanes + 256 * s, to = ts + 128;
+        uint32_t x = 0;                              // tiles so far
         bool ok = true;
         Cursor mine = from[SHARED ? 0 : s];
         Segment g;
@@ -841,7 +854,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
                                               ldexp_exact(__uint_as_float(x & 0xFFFF0000u), pe)) ^
                                    flip;
                     }
-                    *reinterpret_cast<uint4*>(smem + P::kQ + s * P::kTile + tile_at(r, i)) =
+                    *reinterpret_cast<uint4*>(smem + P::kQ + s * P::kQTile + tile_at<kTcRows>(r, i)) =
                         make_uint4(h[0], h[1], h[2], h[3]);
                 }
                 rowf = ldexp_exact(fabsf(t.scale) * kLog2e * a.g[0], -pe);
@@ -858,17 +871,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
             if (lane == 0) mbar_arrive(&bar[kQFull + s]);
 
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < g.tiles; ++j) {
-                ok = warp_wait(&bar[kSFull + s], n_s++ & 1u, t);
+            for (int j = 0; j < g.tiles; ++j, ++x) {
+                const uint32_t buf = x & 1u;
+                ok = warp_wait(&bar[kSFull + 2 * s + buf], x / 2 & 1u, t);
                 if (!ok) break;
                 tc_fence_after();
                 if (busy) {
                     const int p0 = g.first + j * kTcKeys;
-                    const bool special = p0 + kTcKeys > g.len || bad;
-                    uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-                    if (special) {
+                    uint64_t* before = j > 0 ? &bar[kPvDone + 2 * s + (buf ^ 1u)] : nullptr;
+                    const uint32_t parity = (x - 1) / 2 & 1u;
+                    uint32_t seen[2] = {~0u, ~0u};
+                    if (p0 + kTcKeys > g.len || bad) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < 2; ++c) {
                             const int off = p0 + 32 * c - g.len;
                             seen[c] = off <= -32 ? ~0u
                                       : off < 0  ? ((1u << -off) - 1u) | static_cast<uint32_t>(mask << -off)
@@ -876,24 +891,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
                                                  : 0u;
                             if (bad)
 #pragma unroll
-                                for (int x = 0; x < 2; ++x) {
-                                    const int p = p0 + 32 * c + 16 * x;
-                                    if (p < g.end && kv_page(a, g.b, p) < 0) seen[c] &= ~(0xFFFFu << (16 * x));
+                                for (int y = 0; y < 2; ++y) {
+                                    const int p = p0 + 32 * c + 16 * y;
+                                    if (p < g.end && kv_page(a, g.b, p) < 0) seen[c] &= ~(0xFFFFu << (16 * y));
                                 }
                         }
+                        ok = weights<kBf16, true, D>(t, ts + 64 * buf, to, before, parity, rowf, seen, m, l);
+                    } else {
+                        ok = weights<kBf16, false, D>(t, ts + 64 * buf, to, before, parity, rowf, seen, m, l);
                     }
-                    if (special)
-                        weights<kBf16, true, D>(ts, to, j > 0, rowf, seen, m, l);
-                    else
-                        weights<kBf16, false, D>(ts, to, j > 0, rowf, seen, m, l);
-                    tc_wait_st();
+                    if (!ok) break;
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[kPFull + s]);
+                if (lane == 0) mbar_arrive(&bar[kPFull + 2 * s + buf]);
             }
             if (!ok) break;
-            ok = warp_wait(&bar[kODone + s], n_seg++ & 1u, t);
+            ok = warp_wait(&bar[kPvDone + 2 * s + ((x - 1) & 1u)], (x - 1) / 2 & 1u, t);
             if (!ok) break;
             tc_fence_after();
             if (!busy) continue;
@@ -961,12 +975,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
                                       &bar[kv ? kVFull : kKFull], &bar[kv ? kVEmpty : kKEmpty], &bar[kVLand], odd_flag,
                                       kv);
         } else {
-            convert<FMT, D>(t, smem, bar, infos, odd_flag, threadIdx.x - 256);
+            convert<FMT, D>(t, smem, bar, infos, odd_flag, warp - 8);
         }
     } else {
         regs_down<kIssueRegs>();
         if (warp < kMmaWarp + 2) {
-            if (lane == 0) multiply<FMT, D, SHARED>(t, from, smem, bar, tmem, warp - kMmaWarp);
+            const int s = warp - kMmaWarp;
+            const bool leader = elect_one();
+            if (!multiply<FMT, D, SHARED>(t, from, smem, bar, tmem, s, leader)) {
+                if (leader) tc_commit(&bar[kDrain + s]);     // given up: products on their way still end
+                warp_wait(&bar[kDrain + s], 0, t);
+            }
         } else if (!kBf16 && warp == kIssueWarp) {
             if constexpr (!kBf16) copy_coded<FMT, D, SHARED>(t, from, smem, bar, infos);
         }
