@@ -18,6 +18,14 @@ __host__ __device__ constexpr int kv_scale_bytes(int fmt, int dim)
     return fmt == QG_KV_BF16 ? 0 : fmt == QG_KV_FP8 ? 1 : dim / 16;
 }
 
+// Four E4M3 codes of a register as two f16x2, in order.
+__device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
 // Sequence b of a call: its rows [row0, row0 + rows) and the tokens the cache
 // held before. rows = 0 for a sequence whose entries do not fit (recorded).
 struct KvSeq {

@@ -58,9 +58,10 @@ struct MmaPlan {
     static constexpr int kStep = kMmaWarps * L::kKeys;
     static constexpr int kQ = RT * D * 32;                       // bytes of q fragments
     static constexpr int kHead = kQ + kRows * 16;                // + masks, exponents
-    // two CTAs per SM, one where three blocks per warp do not fit beside each other
-    static constexpr int kCtas = kHead + 3 * kMmaWarps * L::kStage <= 112 * 1024 ? 2 : 1;
-    static constexpr int kBudget = (kCtas == 2 ? 112 : 224) * 1024 - kHead;
+    // three CTAs per SM where the accumulators leave the registers for it, else
+    // two, one where two blocks per warp do not fit beside each other
+    static constexpr int kCtas = RT == 1 && D <= 128 ? 3 : kHead + 2 * kMmaWarps * L::kStage <= 112 * 1024 ? 2 : 1;
+    static constexpr int kBudget = (kCtas == 3 ? 74 : kCtas == 2 ? 112 : 224) * 1024 - kHead;
     static constexpr int kFit = kBudget / (kMmaWarps * L::kStage);
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kRing = kMmaWarps * kStages * L::kStage;
@@ -69,8 +70,18 @@ struct MmaPlan {
     static constexpr int kBoth = kRing > kJoin ? kRing : kJoin;
     static constexpr int kBody = kBoth > kPrefix ? kBoth : kPrefix;
     static constexpr int kSmem = kHead + kBody;
-    static_assert(kStages >= 3, "ring too short");
+    static_assert(kStages >= 2, "ring too short");
+    static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "too much shared memory");
 };
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
 
 template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool on)
@@ -135,16 +146,6 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi)
     return r;
 }
 
-// Zeroes each 16-bit half that is infinite or NaN.
-template <bool BF16>
-__device__ __forceinline__ uint32_t finite_halves(uint32_t x)
-{
-    const uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
-    if ((x & e) == e) x &= 0xFFFF0000u;
-    if (((x >> 16) & e) == e) x &= 0x0000FFFFu;
-    return x;
-}
-
 // Values of a key piece: the pairs that k-step w of the piece feeds to the MMA.
 template <int FMT, int WORDS>
 __device__ __forceinline__ void key_pair(const uint32_t (&r)[WORDS], int w, const uint32_t (&sc)[2], uint32_t& b0,
@@ -154,8 +155,7 @@ __device__ __forceinline__ void key_pair(const uint32_t (&r)[WORDS], int w, cons
         b0 = r[2 * w];
         b1 = r[2 * w + 1];
     } else if constexpr (FMT == QG_KV_FP8) {
-        b0 = e4m3x2_to_f16x2(r[w] & 0xFFFFu);
-        b1 = e4m3x2_to_f16x2(r[w] >> 16);
+        e4m3x4_to_f16x2x2(r[w], b0, b1);
     } else {
         const uint32_t x = r[w / 2] >> (16 * (w & 1));
         b0 = hmul2(e2m1x2_to_f16x2(x & 0xFFu), sc[w / 4]);
@@ -164,7 +164,8 @@ __device__ __forceinline__ void key_pair(const uint32_t (&r)[WORDS], int w, cons
 }
 
 // Values of two keys' pieces side by side: word i holds elements of both; out
-// gets one f16x2 / bf16x2 (key 0 low, key 1 high) per element, in order.
+// gets one f16x2 / bf16x2 (key 0 low, key 1 high) per element, in order. (FP8:
+// the codes' own values, their scales are in the weights.)
 template <int FMT>
 __device__ __forceinline__ void value_pairs(uint32_t w0, uint32_t w1, uint32_t sc,
                                             uint32_t (&out)[FMT == QG_KV_BF16 ? 2 : FMT == QG_KV_FP8 ? 4 : 8])
@@ -173,11 +174,8 @@ __device__ __forceinline__ void value_pairs(uint32_t w0, uint32_t w1, uint32_t s
         out[0] = __byte_perm(w0, w1, 0x5410);
         out[1] = __byte_perm(w0, w1, 0x7632);
     } else if constexpr (FMT == QG_KV_FP8) {
-        const uint32_t x = __byte_perm(w0, w1, 0x5140), y = __byte_perm(w0, w1, 0x7362);
-        out[0] = hmul2(e4m3x2_to_f16x2(x & 0xFFFFu), sc);
-        out[1] = hmul2(e4m3x2_to_f16x2(x >> 16), sc);
-        out[2] = hmul2(e4m3x2_to_f16x2(y & 0xFFFFu), sc);
-        out[3] = hmul2(e4m3x2_to_f16x2(y >> 16), sc);
+        e4m3x4_to_f16x2x2(__byte_perm(w0, w1, 0x5140), out[0], out[1]);
+        e4m3x4_to_f16x2x2(__byte_perm(w0, w1, 0x7362), out[2], out[3]);
     } else {
         const uint32_t even = (w0 & 0x0F0F0F0Fu) | ((w1 & 0x0F0F0F0Fu) << 4);
         const uint32_t odd = ((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u);
@@ -192,6 +190,46 @@ __device__ __forceinline__ void value_pairs(uint32_t w0, uint32_t w1, uint32_t s
     }
 }
 
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts8(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(v)) : "memory");
+}
+
+// The values of a block with drafts, or with places behind the last key, made
+// harmless where it lies: what is not finite becomes zero (0 times it would
+// reach rows that do not see the draft), and so do scales behind the last key,
+// whose codes are zeros already. True if a draft's value was not finite.
+template <int FMT, int D>
+__device__ __noinline__ bool clean_values(uint32_t values, uint32_t scales, int keys, int lane)
+{
+    using L = Lay<FMT, D>;
+    bool odd = false;
+    if constexpr (FMT == QG_KV_NVFP4) {
+        if (lane < L::kKeys)
+            for (int i = 0; i < L::kScale; ++i) {
+                const uint32_t at = scales + lane * L::kScale + i;
+                const bool nan = (lds8(at) & 0x7Fu) == 0x7Fu;
+                odd = odd || (nan && lane < keys);
+                if (nan || lane >= keys) sts8(at, 0);
+            }
+    } else {
+        for (int i = 0; i < L::kKBytes / 128; ++i) {          // this lane's words of its own pieces
+            const uint32_t at = values + i / (L::kVB / 4) * (32 * L::kVB) + lane * L::kVB + i % (L::kVB / 4) * 4;
+            const uint32_t w = lds32(at);
+            const uint32_t e = FMT == QG_KV_BF16 ? __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u)
+                                                 : __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            odd = odd || e;
+            if (e) sts32(at, w & ~e);
+        }
+    }
+    __syncwarp();
+    return __any_sync(0xffffffffu, odd);
+}
+
 // One warp's side of a unit: where its keys stand and what its ring holds.
 struct Walk {
     int b, head;
@@ -199,6 +237,45 @@ struct Walk {
     int len, keys;               // context and all keys of the sequence
     int n;                       // this warp's blocks
 };
+
+// Adds to four outputs of a row the drafts' values that are not finite and were
+// left out of the products, for the drafts that the row sees: whatever their
+// weights, they make it infinite or NaN. Rare.
+template <int D>
+__device__ __noinline__ float4 odd_values(const KvArgs& a, const Walk& k, uint64_t mask, int d, float4 v)
+{
+    float* o = reinterpret_cast<float*>(&v);
+    for (int p = max(k.first, k.len); p < k.end; ++p) {
+        if (!((mask >> (p - k.len)) & 1ull)) continue;
+        const int page = kv_page(a, k.b, p);
+        if (page < 0) continue;
+        const int64_t row = kv_row(a, page, k.head, p);
+        for (int i = 0; i < 4; ++i) {
+            const float x = kv_value(a, 1, row, d + i);
+            if (!(fabsf(x) < INFINITY)) o[i] += x;
+        }
+    }
+    return v;
+}
+
+// The copies of 16 keys of which only `left` are in the sequence: zeros behind
+// them (nothing is read there).
+template <int FMT, int D>
+__device__ __noinline__ void copy_partly(uint32_t kd, uint32_t vd, const uint8_t* kl, const uint8_t* vl, int left, int g,
+                                         int c)
+{
+    using L = Lay<FMT, D>;
+    for (int j = 0; j < 2; ++j)
+        for (int x = 0; x < L::kKP; ++x)
+            cp_async<L::kKB>(kd + (j * L::kKP + x) * 32 * L::kKB, kl + 8 * j * L::kRow + x * 4 * L::kKB,
+                             8 * j + g < left);
+    for (int y = 0; y < 4; ++y)
+        for (int x = 0; x < L::kVP; ++x) {
+            const int key = (y & 1) + 8 * (y >> 1);
+            cp_async<L::kVB>(vd + (y * L::kVP + x) * 32 * L::kVB, vl + key * L::kRow + x * 8 * L::kVB,
+                             2 * c + key < left);
+        }
+}
 
 template <int FMT, int D, int RT>
 __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_mma_kernel(const __grid_constant__ TreeArgs t)
@@ -226,9 +303,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
     tree_prefix(t, prefix);
     __syncthreads();
     const int64_t total = prefix[a.n_seqs];
-    const int64_t chunk = tree_chunk(total, t.grid);
-    const int64_t cta_first = blockIdx.x * chunk;
-    const int64_t cta_end = min(total, cta_first + chunk);
+    const int64_t cta_first = tree_first(total, t.grid, blockIdx.x);
+    const int64_t cta_end = tree_first(total, t.grid, blockIdx.x + 1);
     if (cta_first >= cta_end) return;
     int b = tree_find(prefix, a.n_seqs, cta_first);
     int64_t base = prefix[b];                        // first step of sequence b
@@ -263,14 +339,21 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
 
         // ---- the ring
         uint32_t bad = 0;                            // per ring place: groups whose page lies outside the cache
-        int page_next[L::kGroups];
+        int entry[L::kGroups], off[L::kGroups];      // the next block's page table entries, places in their pages
+        const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
         auto look_up = [&](int i) {
 #pragma unroll
             for (int s = 0; s < L::kGroups; ++s) {
                 const int p = k.first + (warp + i * kMmaWarps) * L::kKeys + 16 * s;
-                page_next[s] = i < k.n && p < k.end ? kv_entry(a, b, p) : 0;
+                const int x = kv_page_index(a, p);
+                off[s] = p - x * a.page_size;
+                entry[s] = p < k.end ? table[x] : 0;
             }
         };
+        const uint32_t page_rows = a.heads * a.page_size;
+        const uint32_t head_rows = head * a.page_size;
+        const uint8_t* k_lane = a.codes[0] + g * L::kRow + c * L::kKB;
+        const uint8_t* v_lane = a.codes[1] + 2 * c * L::kRow + g * L::kVB;
         auto issue = [&](int i) {
             const int place = i % P::kStages;
             const uint32_t dst = ring + place * L::kStage;
@@ -279,26 +362,33 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
 #pragma unroll
                 for (int s = 0; s < L::kGroups; ++s) {
                     const int p = k.first + (warp + i * kMmaWarps) * L::kKeys + 16 * s;
-                    const int page = p < k.end ? kv_valid(a, page_next[s]) : 0;
-                    if (page < 0) bad |= 1u << (2 * place + s);
-                    const int64_t row = kv_row(a, max(page, 0), head, p);
-                    const uint8_t* kp = a.codes[0] + row * L::kRow;
-                    const uint8_t* vp = a.codes[1] + row * L::kRow;
-                    const int left = page >= 0 ? k.end - p : 0;    // keys of this group
+                    int left = k.end - p;                        // keys of this group
+                    const bool in = static_cast<uint32_t>(entry[s]) < static_cast<uint32_t>(a.num_pages);
+                    if (!in) {
+                        set_device_status(a.status, QG_ERR_INVALID_ARG);
+                        bad |= 1u << (2 * place + s);
+                        left = 0;
+                    }
+                    const int64_t row = static_cast<int64_t>(in ? entry[s] : 0) * page_rows + (head_rows + off[s]);
+                    const uint8_t* kl = k_lane + row * L::kRow;
+                    const uint8_t* vl = v_lane + row * L::kRow;
+                    const uint32_t kd = dst + 2 * s * L::kKP * 32 * L::kKB + lane * L::kKB;
+                    const uint32_t vd = dst + L::kKBytes + 4 * s * L::kVP * 32 * L::kVB + lane * L::kVB;
+                    if (left >= 16) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                        for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int x = 0; x < L::kKP; ++x)
-                            cp_async<L::kKB>(dst + (((2 * s + j) * L::kKP + x) * 32 + lane) * L::kKB,
-                                             kp + (8 * j + g) * L::kRow + x * 4 * L::kKB + c * L::kKB,
-                                             8 * j + g < left);
+                            for (int x = 0; x < L::kKP; ++x)
+                                cp_async<L::kKB>(kd + (j * L::kKP + x) * 32 * L::kKB,
+                                                 kl + 8 * j * L::kRow + x * 4 * L::kKB);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int key = 2 * c + (y & 1) + 8 * (y >> 1);
+                        for (int y = 0; y < 4; ++y)
 #pragma unroll
-                        for (int x = 0; x < L::kVP; ++x)
-                            cp_async<L::kVB>(dst + L::kKBytes + (((4 * s + y) * L::kVP + x) * 32 + lane) * L::kVB,
-                                             vp + key * L::kRow + x * 8 * L::kVB + g * L::kVB, key < left);
+                            for (int x = 0; x < L::kVP; ++x)
+                                cp_async<L::kVB>(vd + (y * L::kVP + x) * 32 * L::kVB,
+                                                 vl + ((y & 1) + 8 * (y >> 1)) * L::kRow + x * 8 * L::kVB);
+                    } else {
+                        copy_partly<FMT, D>(kd, vd, kl, vl, left, g, c);
                     }
                     if constexpr (L::kScale > 0) {
                         // 16 keys' scales are kScale pieces of 16 bytes
@@ -381,6 +471,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
             }
         }
 
+        bool odd = false;                            // a draft's value was not finite
 #pragma unroll 1
         for (int i = 0; i < k.n; ++i) {
             cp_wait<P::kStages - 2>();
@@ -393,6 +484,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
             const int p0 = k.first + (warp + i * kMmaWarps) * L::kKeys;
             const uint32_t gone = (bad >> (2 * place)) & 3u;
             const bool special = p0 + L::kKeys > k.len || gone;
+            if (special) odd = clean_values<FMT, D>(src + L::kKBytes, v_sc, k.end - p0, lane) || odd;
 
             // ---- scores
             float s[RT][kNT][4];
@@ -434,20 +526,29 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
             }
 
             // ---- base-2 scores, masks, running maxima
+            float inv[kNT][2];                       // FP8: 2^-(exponent of the value's scale) ...
 #pragma unroll
             for (int j = 0; j < kNT; ++j) {
-                float cf[2] = {1.f, 1.f};
+                float cf[2], add[2];
                 if constexpr (FMT == QG_KV_FP8) {
-                    const uint32_t two = lds16(k_sc + 8 * j + 2 * c);
-                    cf[0] = __uint_as_float(((two & 0xFFu) + 112u) << 23);
-                    cf[1] = __uint_as_float(((two >> 8) + 112u) << 23);
+                    const uint32_t two = lds16(k_sc + 8 * j + 2 * c), vs = lds16(v_sc + 8 * j + 2 * c) & 0x1F1Fu;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        cf[e] = __uint_as_float((((two >> (8 * e)) & 0xFFu) + 112u) << 23);
+                        const int b = (vs >> (8 * e)) & 0xFFu;
+                        add[e] = static_cast<float>(b - 15);
+                        inv[j][e] = __int_as_float((142 - b) << 23);
+                    }
                 }
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[rt][j][e] *= rowf[rt][e >> 1];
-                        if constexpr (FMT == QG_KV_FP8) s[rt][j][e] *= cf[e & 1];
+                        // ... which the weights take in, as an addition to the score
+                        if constexpr (FMT == QG_KV_FP8)
+                            s[rt][j][e] = fmaf(s[rt][j][e] * cf[e & 1], rowf[rt][e >> 1], add[e & 1]);
+                        else
+                            s[rt][j][e] *= rowf[rt][e >> 1];
                     }
             }
             if (special) {
@@ -507,8 +608,13 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
                     s[rt][j][1] = ex2(s[rt][j][1] - z0);
                     s[rt][j][2] = ex2(s[rt][j][2] - z1);
                     s[rt][j][3] = ex2(s[rt][j][3] - z1);
-                    l[rt][0] += s[rt][j][0] + s[rt][j][1];
-                    l[rt][1] += s[rt][j][2] + s[rt][j][3];
+                    if constexpr (FMT == QG_KV_FP8) {
+                        l[rt][0] = fmaf(s[rt][j][0], inv[j][0], fmaf(s[rt][j][1], inv[j][1], l[rt][0]));
+                        l[rt][1] = fmaf(s[rt][j][2], inv[j][0], fmaf(s[rt][j][3], inv[j][1], l[rt][1]));
+                    } else {
+                        l[rt][0] += s[rt][j][0] + s[rt][j][1];
+                        l[rt][1] += s[rt][j][2] + s[rt][j][3];
+                    }
                 }
 #pragma unroll
                 for (int x = 0; x < L::kGroups; ++x) {
@@ -520,7 +626,6 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
             }
 
             // ---- values
-            uint32_t odd_values = 0;                 // a value of this lane's is not finite
 #pragma unroll
             for (int x = 0; x < L::kGroups; ++x) {
 #pragma unroll
@@ -531,45 +636,22 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
                         lds_words<L::kVB>(src + L::kKBytes + (((4 * x + z) * L::kVP + y) * 32 + lane) * L::kVB,
                                           raw[z]);
                     constexpr int kPer = kBf16 ? 2 : FMT == QG_KV_FP8 ? 4 : 8;   // values of a word
+                    uint32_t sc[2] = {0, 0};         // NVFP4: scales of keys (2c, 2c + 1) and (2c + 8, 2c + 9)
 #pragma unroll
                     for (int i4 = 0; i4 < L::kVB / 4; ++i4) {
-                        uint32_t sc[2] = {0, 0};     // scales of keys (2c, 2c + 1) and (2c + 8, 2c + 9)
-                        if constexpr (FMT == QG_KV_FP8) {
+                        if constexpr (FMT == QG_KV_NVFP4) {
+                            if (i4 % 2 == 0) {       // a block of 16 is two words
+                                const int blk = (y * 8 * L::kVE + g * L::kVE + i4 * 8) / 16;
 #pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const uint32_t two = lds16(v_sc + 16 * x + 8 * z + 2 * c);
-                                sc[z] = (two & 0xFFu) << 10 | (two >> 8) << 26;
-                            }
-                        } else if constexpr (FMT == QG_KV_NVFP4) {
-                            const int blk = (y * 8 * L::kVE + g * L::kVE + i4 * 8) / 16;
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const uint32_t at8 = v_sc + (16 * x + 8 * z + 2 * c) * L::kScale + blk;
-                                sc[z] = e4m3x2_to_f16x2(lds8(at8) | lds8(at8 + L::kScale) << 8);
-                            }
-                        }
-                        if (special && !kBf16) {
-                            // scales that stand behind the last key are not zeros like its codes
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const int p = p0 + 16 * x + 8 * z + 2 * c;
-                                if (p >= k.end || ((gone >> x) & 1u)) sc[z] &= 0xFFFF0000u;
-                                if (p + 1 >= k.end || ((gone >> x) & 1u)) sc[z] &= 0x0000FFFFu;
+                                for (int z = 0; z < 2; ++z) {
+                                    const uint32_t at8 = v_sc + (16 * x + 8 * z + 2 * c) * L::kScale + blk;
+                                    sc[z] = e4m3x2_to_f16x2(lds8(at8) | lds8(at8 + L::kScale) << 8);
+                                }
                             }
                         }
                         uint32_t b0[kPer], b1[kPer];
                         value_pairs<FMT>(raw[0][i4], raw[1][i4], sc[0], b0);
                         value_pairs<FMT>(raw[2][i4], raw[3][i4], sc[1], b1);
-                        if (special) {
-                            // 0 * infinity must not reach rows that do not see the key
-#pragma unroll
-                            for (int e = 0; e < kPer; ++e) {
-                                const uint32_t f0 = finite_halves<kBf16>(b0[e]), f1 = finite_halves<kBf16>(b1[e]);
-                                odd_values |= (f0 ^ b0[e]) | (f1 ^ b1[e]);
-                                b0[e] = f0;
-                                b1[e] = f1;
-                            }
-                        }
 #pragma unroll
                         for (int e = 0; e < kPer; ++e)
 #pragma unroll
@@ -578,43 +660,11 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
                     }
                 }
             }
-            if (special && __any_sync(0xffffffffu, odd_values != 0)) {
-                // the values left out above, one key at a time, to the rows that see them
-#pragma unroll
-                for (int j = 0; j < kNT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll 1
-                        for (int cc = 0; cc < 4; ++cc) {
-                            const int p = p0 + 8 * j + 2 * cc + e;
-                            float wt[RT][2];
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt) {
-                                wt[rt][0] = __shfl_sync(0xffffffffu, s[rt][j][e], (lane & ~3) | cc);
-                                wt[rt][1] = __shfl_sync(0xffffffffu, s[rt][j][2 + e], (lane & ~3) | cc);
-                            }
-                            if (p >= k.end || ((gone >> (j >> 1)) & 1u)) continue;
-                            const int64_t row = kv_row(a, kv_page(a, b, p), head, p);
-#pragma unroll
-                            for (int x = 0; x < kOT; ++x)
-#pragma unroll
-                                for (int n = 0; n < 2; ++n) {
-                                    const int d = x / L::kVE * (8 * L::kVE) + (2 * c + n) * L::kVE + x % L::kVE;
-                                    const float v = kv_value(a, 1, row, d);
-                                    if (fabsf(v) < INFINITY) continue;
-#pragma unroll
-                                    for (int rt = 0; rt < RT; ++rt) {
-                                        if (wt[rt][0] > 0.f) o[rt][x][n] += wt[rt][0] * v;
-                                        if (wt[rt][1] > 0.f) o[rt][x][2 + n] += wt[rt][1] * v;
-                                    }
-                                }
-                        }
-            }
         }
 
         // ---- join the warps and write
         cp_wait<0>();
-        __syncthreads();
+        odd = __syncthreads_or(odd);
         float* jo = reinterpret_cast<float*>(body);
         float2* jm = reinterpret_cast<float2*>(body + kMmaWarps * P::kRows * (D + 4) * 4);
 #pragma unroll
@@ -658,6 +708,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
                 v.z += f * z.z;
                 v.w += f * z.w;
             }
+            if (odd) v = odd_values<D>(a, k, row_mask[r], d, v);
             if (whole) {
                 const int tok = u.s.row0 + (row0 + r) / t.group;
                 const int64_t h = static_cast<int64_t>(tok) * t.q_heads + head * t.group + (row0 + r) % t.group;
@@ -692,7 +743,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
     tree_prefix(t, prefix);
     __syncthreads();
     const int64_t total = prefix[a.n_seqs];
-    const int64_t chunk = tree_chunk(total, t.grid);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
@@ -711,7 +761,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
     if (i < u.s.row0 || i - u.s.row0 >= u.s.rows) return;
     const int row = (i - u.s.row0) * t.group + h % t.group;
     const int64_t first = prefix[b] + static_cast<int64_t>(h / t.group * u.tiles + row / t.rows) * u.steps;
-    const int64_t c0 = first / chunk, c1 = (first + u.steps - 1) / chunk;
+    const int64_t c0 = tree_owner(total, t.grid, first), c1 = tree_owner(total, t.grid, first + u.steps - 1);
     if (c0 == c1) return;                            // written whole
     const int r = row % t.rows;
     float m = -INFINITY;
@@ -793,7 +843,7 @@ TreePlan plan_tree(int head_dim, int group, int max_tree)
     const int rows = group * max_tree;
     TreePlan p;
     p.rows = rows <= 16 || head_dim == 256 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
-    const size_t ctas = (p.rows == 256 ? 1 : 2) * static_cast<size_t>(sm_count(-1));
+    const size_t ctas = (p.rows == 256 ? 1 : p.rows == 16 ? 3 : 2) * static_cast<size_t>(sm_count(-1));
     const size_t rows_held = 2 * ctas * p.rows;
     p.o_bytes = rows_held * head_dim * sizeof(float);
     p.ml_bytes = rows_held * sizeof(float2);

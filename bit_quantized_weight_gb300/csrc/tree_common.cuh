@@ -4,8 +4,9 @@
 // A unit is (sequence, key/value head, tile of query rows): the rows of a
 // sequence's tokens that share a head, G per token, in tiles of R. A unit's
 // keys are cut into steps. All steps of a call, in order, are dealt out evenly:
-// CTA c takes [c * chunk, (c + 1) * chunk), whatever sequence they belong to,
-// so ragged lengths balance by themselves and lengths stay device data. A CTA
+// CTA c of the n that get work takes [c * total / n, (c + 1) * total / n), whatever sequence they
+// belong to, so ragged lengths balance by themselves and lengths stay device
+// data. A CTA
 // that holds only a piece of a unit writes it to the workspace: a unit's first
 // piece to slot 2c + 1 (it ends at the CTA's end), any other to slot 2c (it
 // starts at the CTA's start).
@@ -95,7 +96,19 @@ __device__ __forceinline__ int tree_find(const int64_t* prefix, int n, int64_t s
     return lo;
 }
 
-__device__ __forceinline__ int64_t tree_chunk(int64_t total, int grid) { return (total + grid - 1) / grid; }
+// The CTAs that get work: no more than there are steps, so that each of them
+// holds at least one. The first step of CTA c, and the CTA that holds a step:
+// the last c with c * total / n <= step.
+__device__ __forceinline__ int64_t tree_ctas(int64_t total, int grid) { return min(total, static_cast<int64_t>(grid)); }
+__device__ __forceinline__ int64_t tree_first(int64_t total, int grid, int64_t c)
+{
+    const int64_t n = tree_ctas(total, grid);
+    return c < n ? c * total / n : total;
+}
+__device__ __forceinline__ int64_t tree_owner(int64_t total, int grid, int64_t step)
+{
+    return ((step + 1) * tree_ctas(total, grid) - 1) / total;
+}
 
 // 1 / L with 0 for an empty row.
 __device__ __forceinline__ float tree_inverse(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }

@@ -149,10 +149,9 @@ struct Cursor {
     __device__ __forceinline__ void locate(const TreeArgs& t, const int64_t* prefix, int vcta)
     {
         const int64_t total = prefix[t.a.n_seqs];
-        const int64_t chunk = tree_chunk(total, t.grid);
         vc = vcta;
-        at = min(total, vcta * chunk);
-        end = min(total, at + chunk);
+        at = tree_first(total, t.grid, vcta);
+        end = tree_first(total, t.grid, vcta + 1);
         b = at < end ? tree_find(prefix, t.a.n_seqs, at) : 0;
         base = prefix[b];
     }
@@ -326,8 +325,10 @@ __device__ __forceinline__ void piece_values(const uint4 raw, uint32_t sc, uint4
         uint32_t h[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            h[2 * i] = hmul2(e4m3x2_to_f16x2(w[i] & 0xFFFFu), s2);
-            h[2 * i + 1] = hmul2(e4m3x2_to_f16x2(w[i] >> 16), s2);
+            uint32_t lo, hi;
+            e4m3x4_to_f16x2x2(w[i], lo, hi);
+            h[2 * i] = hmul2(lo, s2);
+            h[2 * i + 1] = hmul2(hi, s2);
         }
         out[0] = make_uint4(h[0], h[1], h[2], h[3]);
         out[1] = make_uint4(h[4], h[5], h[6], h[7]);
