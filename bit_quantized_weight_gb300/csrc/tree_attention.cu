@@ -66,9 +66,7 @@ struct MmaPlan {
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kRing = kMmaWarps * kStages * L::kStage;
     static constexpr int kJoin = kMmaWarps * kRows * (D + 4) * 4 + kMmaWarps * kRows * 8;
-    static constexpr int kPrefix = (kKvMaxSeqs + 1) * 8;
-    static constexpr int kBoth = kRing > kJoin ? kRing : kJoin;
-    static constexpr int kBody = kBoth > kPrefix ? kBoth : kPrefix;
+    static constexpr int kBody = kRing > kJoin ? kRing : kJoin;
     static constexpr int kSmem = kHead + kBody;
     static_assert(kStages >= 2, "ring too short");
     static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "too much shared memory");
@@ -299,27 +297,23 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
     // starts early, may read the batch as soon as it is launched.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    int64_t* prefix = reinterpret_cast<int64_t*>(body);
-    tree_prefix(t, prefix);
-    __syncthreads();
-    const int64_t total = prefix[a.n_seqs];
+    TreeScan scan;
+    scan.run(t);
+    const int64_t total = scan.total;
     const int64_t cta_first = tree_first(total, t.grid, blockIdx.x);
     const int64_t cta_end = tree_first(total, t.grid, blockIdx.x + 1);
     if (cta_first >= cta_end) return;
-    int b = tree_find(prefix, a.n_seqs, cta_first);
-    int64_t base = prefix[b];                        // first step of sequence b
-    __syncthreads();                                 // the ring takes the prefix sums' place
+    int64_t base;                                    // first step of sequence b
+    KvSeq seq;
+    int b = scan.find(t, cta_first, seq, base);
+    TreeSeq u = tree_seq_of(t, seq);
 
     const uint32_t ring = smem_u32(body) + warp * (P::kStages * L::kStage);
     int64_t at = cta_first;
     while (at < cta_end) {
-        TreeSeq u = tree_seq(t, b);
-        int64_t w = static_cast<int64_t>(u.steps) * u.tiles * a.heads;
-        while (at >= base + w) {
-            base += w;
-            ++b;
-            u = tree_seq(t, b);
-            w = static_cast<int64_t>(u.steps) * u.tiles * a.heads;
+        while (at >= base + tree_steps(t, u)) {
+            base += tree_steps(t, u);
+            u = tree_seq(t, ++b);
         }
         const int unit = static_cast<int>((at - base) / u.steps);
         const int s0 = static_cast<int>((at - base) % u.steps);
@@ -729,72 +723,102 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
 }
 
 // ------------------------------------------------------------------ join
-// One warp per (token, query head): the parts of its unit, if there are
-// several, in the CTAs' order. Bound by one chain of loads (batch, then the
-// parts' maxima and sums, then the parts).
+// One block per (token, query head) whose unit was read in several parts: its
+// warps take every fourth part, then join. Bound by two chained loads (the
+// batch's entries, before the wait; then the parts with their maxima and sums).
 constexpr int kJoinWarps = 4;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid_constant__ TreeArgs t)
 {
-    __shared__ int64_t prefix[kKvMaxSeqs + 1];
-    const KvArgs& a = t.a;
-    const int lane = threadIdx.x & 31;
-    tree_prefix(t, prefix);
-    __syncthreads();
-    const int64_t total = prefix[a.n_seqs];
+    constexpr int kPer = D / 32;
+    constexpr int kAhead = 4;                        // parts on their way per warp
+    __shared__ float part[kJoinWarps][D];
+    __shared__ float2 part_ml[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int i = blockIdx.x / t.q_heads, h = blockIdx.x % t.q_heads;
+    TreeScan scan;
+    scan.run(t);
+    int64_t base, c0 = 0, c1 = 0;
+    KvSeq seq;
+    int r = 0;
+    if (scan.total > 0 && scan.find_row(t, i, seq, base) >= 0) {
+        const TreeSeq u = tree_seq_of(t, seq);
+        const int row = (i - seq.row0) * t.group + h % t.group;
+        const int64_t first = base + static_cast<int64_t>(h / t.group * u.tiles + row / t.rows) * u.steps;
+        c0 = tree_owner(scan.total, t.grid, first);
+        c1 = tree_owner(scan.total, t.grid, first + u.steps - 1);
+        r = row % t.rows;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
-    const int i = static_cast<int>(x / t.q_heads), h = static_cast<int>(x % t.q_heads);
-    if (i >= a.n_tokens || total == 0) return;
-    // the sequence of row i: the number of sequences that end at or before it
-    int b = 0;
-    for (int j = 0; j < a.n_seqs; j += 32) {
-        const bool before = j + lane < a.n_seqs && a.start[j + lane + 1] <= i;
-        const int n = __popc(__ballot_sync(0xffffffffu, before));
-        b += n;
-        if (n < 32) break;
-    }
-    if (b >= a.n_seqs) return;
-    const TreeSeq u = tree_seq(t, b);
-    if (i < u.s.row0 || i - u.s.row0 >= u.s.rows) return;
-    const int row = (i - u.s.row0) * t.group + h % t.group;
-    const int64_t first = prefix[b] + static_cast<int64_t>(h / t.group * u.tiles + row / t.rows) * u.steps;
-    const int64_t c0 = tree_owner(total, t.grid, first), c1 = tree_owner(total, t.grid, first + u.steps - 1);
-    if (c0 == c1) return;                            // written whole
-    const int r = row % t.rows;
-    float m = -INFINITY;
-    for (int64_t y = c0 + lane; y <= c1; y += 32) m = fmaxf(m, t.part_ml[(2 * y + (y == c0)) * t.rows + r].x);
+    if (c0 == c1) return;                            // written whole, or nobody's row
+    float m = -INFINITY, l = 0.f, acc[kPer] = {};
+    for (int64_t y0 = c0 + warp; y0 <= c1; y0 += kAhead * kJoinWarps) {
+        float2 ml[kAhead];
+        float v[kAhead][kPer];
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    constexpr int kPer = D / 32;
-    float acc[kPer] = {}, l = 0.f;
-    // as many CTAs as there may be: a CTA's slot is 2c but for the unit's first
-#pragma unroll 4
-    for (int64_t y = c0; y <= c1; ++y) {
-        const int64_t at = (2 * y + (y == c0)) * t.rows + r;
-        const float2 ml = t.part_ml[at];
-        const bool some = ml.x != -INFINITY;         // else the part's row saw nothing
-        const float f = some ? ex2(ml.x - m) : 0.f;
-        l += some ? f * ml.y : 0.f;
-        float v[kPer];
-        if constexpr (kPer == 2) {
-            *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(t.part_o + at * D + lane * kPer);
-        } else {
+        for (int x = 0; x < kAhead; ++x) {
+            const int64_t y = y0 + x * kJoinWarps;
+            ml[x] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int z = 0; z < kPer; z += 4)
-                *reinterpret_cast<float4*>(v + z) = *reinterpret_cast<const float4*>(t.part_o + at * D + lane * kPer + z);
+            for (int z = 0; z < kPer; ++z) v[x][z] = 0.f;
+            if (y <= c1) {
+                const int64_t at = (2 * y + (y == c0)) * t.rows + r;   // a unit's first part is its CTA's last
+                ml[x] = t.part_ml[at];
+                const float* src = t.part_o + at * D + lane * kPer;
+                if constexpr (kPer == 2) {
+                    const float2 w = *reinterpret_cast<const float2*>(src);
+                    v[x][0] = w.x;
+                    v[x][1] = w.y;
+                } else {
+#pragma unroll
+                    for (int z = 0; z < kPer; z += 4) {
+                        const float4 w = *reinterpret_cast<const float4*>(src + z);
+                        v[x][z] = w.x;
+                        v[x][z + 1] = w.y;
+                        v[x][z + 2] = w.z;
+                        v[x][z + 3] = w.w;
+                    }
+                }
+            }
         }
 #pragma unroll
-        for (int z = 0; z < kPer; ++z) acc[z] += some ? f * v[z] : 0.f;
-    }
-    const float f = tree_inverse(l) * a.g[1];
-    const int64_t to = static_cast<int64_t>(i) * t.q_heads + h;
-    uint32_t* out = reinterpret_cast<uint32_t*>(t.out + to * D) + lane * (kPer / 2);
+        for (int x = 0; x < kAhead; ++x) {
+            if (ml[x].x == -INFINITY) continue;      // a part whose row saw nothing
+            const float mn = fmaxf(m, ml[x].x), f = ex2(m - mn), g = ex2(ml[x].x - mn);
+            m = mn;
+            l = l * f + ml[x].y * g;
 #pragma unroll
-    for (int z = 0; z < kPer / 2; ++z) out[z] = pack16<true>(acc[2 * z] * f, acc[2 * z + 1] * f);
-    if (t.lse && lane == 0) t.lse[to] = tree_lse(m, l);
+            for (int z = 0; z < kPer; ++z) acc[z] = acc[z] * f + v[x][z] * g;
+        }
+    }
+#pragma unroll
+    for (int z = 0; z < kPer; ++z) part[warp][lane * kPer + z] = acc[z];
+    if (lane == 0) part_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    m = -INFINITY;
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, part_ml[w].x);
+    l = 0.f;
+    float f[kJoinWarps];
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        f[w] = part_ml[w].x == -INFINITY ? 0.f : ex2(part_ml[w].x - m);
+        l += f[w] * part_ml[w].y;
+    }
+    const float scale = tree_inverse(l) * t.a.g[1];
+    const int64_t to = static_cast<int64_t>(i) * t.q_heads + h;
+    for (int d = 2 * threadIdx.x; d < D; d += 64 * kJoinWarps) {
+        float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            if (f[w] == 0.f) continue;               // also a warp without parts
+            x0 += f[w] * part[w][d];
+            x1 += f[w] * part[w][d + 1];
+        }
+        *reinterpret_cast<uint32_t*>(t.out + to * D + d) = pack16<true>(x0 * scale, x1 * scale);
+    }
+    if (t.lse && threadIdx.x == 0) t.lse[to] = tree_lse(m, l);
 }
 
 // ------------------------------------------------------------------ plans
@@ -854,8 +878,7 @@ TreePlan plan_tree(int head_dim, int group, int max_tree)
 
 cudaError_t launch_tree_join(const TreeArgs& t, cudaStream_t stream)
 {
-    const int64_t units = static_cast<int64_t>(t.a.n_tokens) * t.q_heads;
-    const dim3 grid(static_cast<unsigned>((units + kJoinWarps - 1) / kJoinWarps)), block(32 * kJoinWarps);
+    const dim3 grid(static_cast<unsigned>(t.a.n_tokens * t.q_heads)), block(32 * kJoinWarps);
     if (t.a.dim == 64) return launch_pdl(tree_join_kernel<64>, grid, block, 0, stream, t);
     if (t.a.dim == 128) return launch_pdl(tree_join_kernel<128>, grid, block, 0, stream, t);
     return launch_pdl(tree_join_kernel<256>, grid, block, 0, stream, t);

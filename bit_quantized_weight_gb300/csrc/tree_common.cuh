@@ -47,54 +47,95 @@ struct TreeSeq {
     int tiles;                // row tiles per head
 };
 
-__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& t, int b)
+__device__ __forceinline__ TreeSeq tree_seq_of(const TreeArgs& t, const KvSeq& s)
 {
     TreeSeq u;
-    u.s = kv_seq(t.a, b, t.max_tree);
-    u.keys = u.s.rows ? u.s.len + u.s.rows : 0;
+    u.s = s;
+    u.keys = s.rows ? s.len + s.rows : 0;
     u.steps = (u.keys - 1 + t.step) / t.step;
-    u.tiles = (u.s.rows * t.group + t.rows - 1) / t.rows;
+    u.tiles = (s.rows * t.group + t.rows - 1) / t.rows;
     return u;
 }
 
-// Exclusive prefix sums of the sequences' steps into `prefix`
-// [n_seqs + 1] (shared), by the first warp; the caller synchronises.
-__device__ __forceinline__ void tree_prefix(const TreeArgs& t, int64_t* prefix)
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& t, int b)
 {
-    if (threadIdx.x >= 32) return;
-    const int lane = threadIdx.x;
-    int64_t total = 0;
-    for (int j = 0; j < t.a.n_seqs; j += 32) {
-        int64_t w = 0;
-        if (j + lane < t.a.n_seqs) {
-            const TreeSeq u = tree_seq(t, j + lane);
-            w = static_cast<int64_t>(u.steps) * u.tiles * t.a.heads;
+    return tree_seq_of(t, kv_seq(t.a, b, t.max_tree));
+}
+
+__device__ __forceinline__ int64_t tree_steps(const TreeArgs& t, const TreeSeq& u)
+{
+    return static_cast<int64_t>(u.steps) * u.tiles * t.a.heads;
+}
+
+// The call's steps, scanned by one warp with its sequences' entries in its
+// lanes: 32 sequences at a time, and the first 32 (mostly all) read only once.
+struct TreeScan {
+    KvSeq mine;                  // sequence `first + lane`, the last chunk looked at
+    int first;
+    int64_t before, steps;       // steps ahead of it, and its own
+    int64_t total;
+
+    __device__ __forceinline__ void load(const TreeArgs& t, int chunk, int64_t ahead)
+    {
+        const int lane = threadIdx.x & 31;
+        first = chunk;
+        mine = KvSeq{0, 0, 0};
+        steps = 0;
+        if (chunk + lane < t.a.n_seqs) {
+            mine = kv_seq(t.a, chunk + lane, t.max_tree);
+            steps = tree_steps(t, tree_seq_of(t, mine));
         }
-        int64_t sum = w;
+        int64_t sum = steps;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int64_t up = __shfl_up_sync(0xffffffffu, sum, off);
             if (lane >= off) sum += up;
         }
-        if (j + lane < t.a.n_seqs) prefix[j + lane] = total + sum - w;
-        total += __shfl_sync(0xffffffffu, sum, 31);
+        before = ahead + sum - steps;
     }
-    if (lane == 0) prefix[t.a.n_seqs] = total;
-}
 
-// The last sequence whose first step is at or before `step`.
-__device__ __forceinline__ int tree_find(const int64_t* prefix, int n, int64_t step)
-{
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= step)
-            lo = mid;
-        else
-            hi = mid;
+    __device__ __forceinline__ int64_t end() const { return __shfl_sync(0xffffffffu, before + steps, 31); }
+
+    __device__ __forceinline__ void run(const TreeArgs& t)
+    {
+        load(t, 0, 0);
+        total = end();
+        for (int c = 32; c < t.a.n_seqs; c += 32) {
+            load(t, c, total);
+            total = end();
+        }
     }
-    return lo;
-}
+
+    // The sequence that holds a step (< total): its index, entries and first step.
+    __device__ __forceinline__ int find(const TreeArgs& t, int64_t step, KvSeq& s, int64_t& base)
+    {
+        if (first != 0) load(t, 0, 0);
+        while (step >= end()) load(t, first + 32, end());
+        const uint32_t hit = __ballot_sync(0xffffffffu, steps > 0 && before <= step && step < before + steps);
+        return pick(__ffs(hit) - 1, s, base);
+    }
+
+    // The sequence that row i belongs to, -1 for a row of none.
+    __device__ __forceinline__ int find_row(const TreeArgs& t, int i, KvSeq& s, int64_t& base)
+    {
+        if (first != 0) load(t, 0, 0);
+        for (;;) {
+            const uint32_t hit = __ballot_sync(0xffffffffu, mine.rows > 0 && i >= mine.row0 && i - mine.row0 < mine.rows);
+            if (hit) return pick(__ffs(hit) - 1, s, base);
+            if (first + 32 >= t.a.n_seqs) return -1;
+            load(t, first + 32, end());
+        }
+    }
+
+    __device__ __forceinline__ int pick(int from, KvSeq& s, int64_t& base) const
+    {
+        s.row0 = __shfl_sync(0xffffffffu, mine.row0, from);
+        s.rows = __shfl_sync(0xffffffffu, mine.rows, from);
+        s.len = __shfl_sync(0xffffffffu, mine.len, from);
+        base = __shfl_sync(0xffffffffu, before, from);
+        return first + from;
+    }
+};
 
 // The CTAs that get work: no more than there are steps, so that each of them
 // holds at least one. The first step of CTA c, and the CTA that holds a step:

@@ -71,7 +71,6 @@ struct TcPlan {
     static constexpr int kRawStage = FMT == QG_KV_BF16 ? 0 : kCodes + kTcKeys * kv_scale_bytes(FMT, D);
     static constexpr int kSmem = kRaw + kRawStages * kRawStage + 1024;   // + alignment
     static_assert(kSmem <= 227 * 1024, "too much shared memory");
-    static_assert(2 * kQTile >= (kKvMaxSeqs + 1) * 8, "prefix sums lie where Q goes");
     static_assert(kBars * 8 <= 512, "barriers");
 };
 
@@ -146,26 +145,25 @@ struct Cursor {
     int64_t at, end, base;
     int b, vc;
 
-    __device__ __forceinline__ void locate(const TreeArgs& t, const int64_t* prefix, int vcta)
+    // by a whole warp
+    __device__ __forceinline__ void locate(const TreeArgs& t, TreeScan& scan, int vcta)
     {
-        const int64_t total = prefix[t.a.n_seqs];
         vc = vcta;
-        at = tree_first(total, t.grid, vcta);
-        end = tree_first(total, t.grid, vcta + 1);
-        b = at < end ? tree_find(prefix, t.a.n_seqs, at) : 0;
-        base = prefix[b];
+        at = tree_first(scan.total, t.grid, vcta);
+        end = tree_first(scan.total, t.grid, vcta + 1);
+        b = 0;
+        base = 0;
+        KvSeq s;
+        if (at < end) b = scan.find(t, at, s, base);
     }
 
     __device__ __forceinline__ bool next(const TreeArgs& t, Segment& g)
     {
         if (at >= end) return false;
         TreeSeq u = tree_seq(t, b);
-        int64_t w = static_cast<int64_t>(u.steps) * u.tiles * t.a.heads;
-        while (at >= base + w) {
-            base += w;
-            ++b;
-            u = tree_seq(t, b);
-            w = static_cast<int64_t>(u.steps) * u.tiles * t.a.heads;
+        while (at >= base + tree_steps(t, u)) {
+            base += tree_steps(t, u);
+            u = tree_seq(t, ++b);
         }
         const int unit = static_cast<int>((at - base) / u.steps);
         const int s0 = static_cast<int>((at - base) % u.steps);
@@ -761,9 +759,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
     asm volatile("fence.proxy.async;" ::: "memory");
     Cursor* from = reinterpret_cast<Cursor*>(smem + 576);    // where the CTA's one or two ranges begin
     RawInfo* infos = reinterpret_cast<RawInfo*>(smem + 640);
-    int64_t* prefix = reinterpret_cast<int64_t*>(smem + P::kQ);
-    tree_prefix(t, prefix);
-    if (threadIdx.x == 32) {
+    if (warp < 2) {
+        TreeScan scan;
+        scan.run(t);
+        Cursor c;
+        c.locate(t, scan, warp * gridDim.x + blockIdx.x);
+        if (lane == 0) from[warp] = c;
+    }
+    if (threadIdx.x == 64) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bar[kKFull + s], 1);
             mbar_init(&bar[kKEmpty + s], SHARED ? 2 : 1);
@@ -791,8 +794,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
         tc_alloc(tmem_slot, 512);
         tc_relinquish();
     }
-    __syncthreads();
-    if (threadIdx.x < 2) from[threadIdx.x].locate(t, prefix, threadIdx.x * gridDim.x + blockIdx.x);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -469,7 +469,8 @@ QG_API qg_status kv_cache_accept(const qg_kv_cache* cache, const qg_kv_batch* ba
  * it, infinities and NaN included.
  *   q          bf16, row i at q + i * q_stride: q_heads * head_dim values;
  *              q_stride in elements, a multiple of 8
- *   q_heads    a multiple of kv_heads, at most 128 * kv_heads
+ *   q_heads    a multiple of kv_heads, at most 128 * kv_heads;
+ *              n_tokens * q_heads below 2^31
  *   max_tree   1..64, the largest number of tokens of a sequence of this
  *              call; a sequence that has more is left out, with
  *              QG_ERR_INVALID_ARG in the device status word
