@@ -42,7 +42,8 @@ __device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, int b, int max_rows)
     s.len = a.lens[b];
     s.rows = end - s.row0;
     const bool ok = s.row0 >= 0 && end >= s.row0 && end <= a.n_tokens && s.len >= 0 && s.rows <= max_rows &&
-                    static_cast<int64_t>(s.len) + s.rows <= static_cast<int64_t>(a.max_pages) * a.page_size;
+                    static_cast<int64_t>(s.len) + s.rows <=
+                        min(static_cast<int64_t>(a.max_pages) * a.page_size, static_cast<int64_t>(kKvMaxPositions));
     if (!ok) {
         set_device_status(a.status, QG_ERR_INVALID_ARG);
         s.rows = 0;

@@ -19,6 +19,7 @@ constexpr int kMaxRowsPerCta = 256;                   // TMA box limit
 constexpr int kMaxStages = 32;
 constexpr int kKvMaxSeqs = 1024;                      // sequences of a cache call
 constexpr int kKvMaxTokens = 1 << 24;                 // rows of a cache call
+constexpr int kKvMaxPositions = 1 << 30;              // of a sequence
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;    // 2 s
 
 // Per-stage shared-memory layout (byte offsets inside one stage buffer).

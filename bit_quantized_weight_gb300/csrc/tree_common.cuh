@@ -47,14 +47,20 @@ struct TreeSeq {
     int tiles;                // row tiles per head
 };
 
-__device__ __forceinline__ TreeSeq tree_seq_of(const TreeArgs& t, const KvSeq& s)
+// (step, rows: t.step and t.rows, or the constants that they are to a kernel)
+__device__ __forceinline__ TreeSeq tree_seq_of(const TreeArgs& t, const KvSeq& s, uint32_t step, uint32_t rows)
 {
     TreeSeq u;
     u.s = s;
     u.keys = s.rows ? s.len + s.rows : 0;
-    u.steps = (u.keys - 1 + t.step) / t.step;
-    u.tiles = (s.rows * t.group + t.rows - 1) / t.rows;
+    u.steps = (static_cast<uint32_t>(u.keys) + step - 1) / step;
+    u.tiles = (static_cast<uint32_t>(s.rows) * t.group + rows - 1) / rows;
     return u;
+}
+
+__device__ __forceinline__ TreeSeq tree_seq_of(const TreeArgs& t, const KvSeq& s)
+{
+    return tree_seq_of(t, s, t.step, t.rows);
 }
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& t, int b)

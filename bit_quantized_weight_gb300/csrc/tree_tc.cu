@@ -124,10 +124,23 @@ __device__ __forceinline__ void regs_down()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// A bounded wait of a whole warp: all of its lanes go on, or none.
+// A bounded wait of a whole warp: all of its lanes go on, or none. It sleeps
+// while it waits, so that it costs the other warps no issue slots.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const TreeArgs& t)
 {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, t.wait_ns, t.a.status));
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+        const uint64_t t0 = global_timer_ns();
+        while (!ok) {
+            ok = mbar_try_wait_sleep(bar, parity, 10000);
+            if (!ok && global_timer_ns() - t0 > t.wait_ns) {
+                set_device_status(t.a.status, QG_ERR_DEVICE_TIMEOUT);
+                break;
+            }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+    }
+    return ok;
 }
 
 // A piece of a unit: what one stream does between two epilogues.
@@ -140,46 +153,61 @@ struct Segment {
     int slot;                    // -1: the whole unit
 };
 
-// The segments of one virtual CTA's range of steps, in order.
+// The segments of one virtual CTA's range of steps, in order: where the next
+// begins, and the steps that are left.
 struct Cursor {
-    int64_t at, end, base;
-    int b, vc;
+    int64_t left;
+    int b, head, tile, step;
+    int vc;
 
     // by a whole warp
     __device__ __forceinline__ void locate(const TreeArgs& t, TreeScan& scan, int vcta)
     {
         vc = vcta;
-        at = tree_first(scan.total, t.grid, vcta);
-        end = tree_first(scan.total, t.grid, vcta + 1);
-        b = 0;
-        base = 0;
+        const int64_t at = tree_first(scan.total, t.grid, vcta);
+        left = tree_first(scan.total, t.grid, vcta + 1) - at;
+        b = head = tile = step = 0;
+        if (left <= 0) return;
         KvSeq s;
-        if (at < end) b = scan.find(t, at, s, base);
+        int64_t base;
+        b = scan.find(t, at, s, base);
+        const TreeSeq u = tree_seq_of(t, s);
+        const int64_t unit = (at - base) / u.steps;
+        step = static_cast<int>((at - base) % u.steps);
+        head = static_cast<int>(unit / u.tiles);
+        tile = static_cast<int>(unit % u.tiles);
     }
 
+    template <int ROWS>
     __device__ __forceinline__ bool next(const TreeArgs& t, Segment& g)
     {
-        if (at >= end) return false;
-        TreeSeq u = tree_seq(t, b);
-        while (at >= base + tree_steps(t, u)) {
-            base += tree_steps(t, u);
-            u = tree_seq(t, ++b);
-        }
-        const int unit = static_cast<int>((at - base) / u.steps);
-        const int s0 = static_cast<int>((at - base) % u.steps);
-        const int s1 = static_cast<int>(min(static_cast<int64_t>(u.steps), s0 + (end - at)));
+        if (left <= 0) return false;
+        TreeSeq u = tree_seq_of(t, kv_seq(t.a, b, t.max_tree), kTcKeys, ROWS);
+        while (u.steps == 0) u = tree_seq_of(t, kv_seq(t.a, ++b, t.max_tree), kTcKeys, ROWS);
+        const int n = static_cast<int>(min(static_cast<int64_t>(u.steps - step), left));
         g.b = b;
-        g.head = unit / u.tiles;
-        g.row0 = unit % u.tiles * t.rows;
-        g.n_rows = min(t.rows, u.s.rows * t.group - g.row0);
-        g.first = s0 * kTcKeys;
-        g.end = min(u.keys, s1 * kTcKeys);
+        g.head = head;
+        g.row0 = tile * ROWS;
+        g.n_rows = min(ROWS, u.s.rows * t.group - g.row0);
+        g.first = step * kTcKeys;
+        g.end = min(u.keys, (step + n) * kTcKeys);
         g.len = u.s.len;
         g.tok0 = u.s.row0;
         g.n_tok = u.s.rows;
-        g.tiles = s1 - s0;
-        g.slot = s0 == 0 && s1 == u.steps ? -1 : 2 * vc + (s0 == 0);
-        at += g.tiles;
+        g.tiles = n;
+        g.slot = n == u.steps ? -1 : 2 * vc + (step == 0);
+        left -= n;
+        step += n;
+        if (step == u.steps) {
+            step = 0;
+            if (++tile == u.tiles) {
+                tile = 0;
+                if (++head == t.a.heads) {
+                    head = 0;
+                    ++b;
+                }
+            }
+        }
         return true;
     }
 };
@@ -187,6 +215,7 @@ struct Cursor {
 // The tiles of a CTA in the order in which they are brought and multiplied:
 // SHARED, one cursor and every tile for both streams; else the two streams'
 // tiles in turn while both have some.
+template <int ROWS>
 struct Side {
     Cursor cur;
     Segment seg;
@@ -196,7 +225,7 @@ struct Side {
     __device__ __forceinline__ void start(const TreeArgs& t, const Cursor& from)
     {
         cur = from;
-        live = cur.next(t, seg);
+        live = cur.template next<ROWS>(t, seg);
         tile = 0;
     }
 
@@ -205,7 +234,7 @@ struct Side {
         g = seg;
         j = tile;
         if (++tile == g.tiles) {
-            live = cur.next(t, seg);
+            live = cur.template next<ROWS>(t, seg);
             tile = 0;
         }
     }
@@ -213,7 +242,7 @@ struct Side {
 
 template <bool SHARED>
 struct Items {
-    Side x, y;
+    Side<SHARED ? 2 * kTcRows : kTcRows> x, y;
     int turn;
 
     __device__ __forceinline__ void start(const TreeArgs& t, const Cursor* from)
@@ -369,6 +398,29 @@ __device__ __forceinline__ void announce(uint64_t* bar)
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
+// A tile of values with drafts, or with places that no key fills, by one warp:
+// the places become zeros, and so does what is not finite of a draft (0 times it
+// would reach rows that do not see the draft; it is flagged for the epilogue).
+// Rare, so small rather than fast.
+template <int D, bool BF16>
+__device__ __noinline__ void clear_places(uint8_t* tile, int left, int drafts, uint32_t groups, volatile int* odd_flag,
+                                          int lane)
+{
+    bool odd = false;
+#pragma unroll 1
+    for (int x = lane; x < kTcKeys * D / 8; x += 32) {
+        const int key = x / (D / 8);
+        const bool on = key < left && ((groups >> (key >> 4)) & 1u);
+        if (on && key < drafts) continue;
+        uint4* at = reinterpret_cast<uint4*>(tile + tile_at<kTcKeys>(key, x % (D / 8)));
+        uint4 y = on ? *at : make_uint4(0, 0, 0, 0);
+        drop_odd<BF16>(y, odd);
+        *at = y;
+    }
+    if (odd) *odd_flag = 1;
+    __syncwarp();
+}
+
 // Coded keys and values: one warp starts the copies of the tiles as they are
 // stored, keys and values in turn, into four raw stages. On a timeout it waits
 // for the copies that are on their way.
@@ -423,9 +475,7 @@ __device__ __forceinline__ void copy_coded(const TreeArgs& t, const Cursor* from
 }
 
 // ... and four warps, each a raw stage and every fourth tile of its own,
-// convert them to f16 tiles. Drafts' values that are not finite are left out
-// (0 times them would reach rows that do not see the draft) and flagged for the
-// epilogue; what no key fills is zero.
+// convert them to f16 tiles.
 template <int FMT, int D>
 __device__ __forceinline__ void convert(const TreeArgs& t, uint8_t* smem, uint64_t* bar, const RawInfo* infos,
                                         volatile int* odd_flag, int r)
@@ -434,8 +484,23 @@ __device__ __forceinline__ void convert(const TreeArgs& t, uint8_t* smem, uint64
     constexpr int kRow = kv_row_bytes(FMT, D), kScale = kv_scale_bytes(FMT, D);
     constexpr int kPerKey = kRow / 16;                       // pieces of a row
     constexpr int kN = kTcKeys * kPerKey / 32;               // pieces per lane
+    const int lane = threadIdx.x & 31, kv = r & 1;
+    constexpr int kBatch = 4;
+    // Piece x of this lane. At head_dim 128 eight neighbouring lanes take keys
+    // of all residues (mod 2 for FP8, mod 4 for NVFP4) and, by residue, one or
+    // the other half of the row: their reads and their swizzled writes then
+    // fall into eight different groups of banks.
+    auto key_of = [&](int x) {
+        if constexpr (D == 128 && FMT == QG_KV_FP8) return 2 * ((x * 4 + (lane >> 3)) >> 1) + (lane >> 2 & 1);
+        else if constexpr (D == 128) return 4 * ((x * 4 + (lane >> 3)) >> 1) + (lane >> 1 & 3);
+        else return (x * 32 + lane) / kPerKey;
+    };
+    // its place in the row (the same for every x: x * 4 is even)
+    const int half = lane >> 3 & 1;
+    const int c = D != 128 ? lane % kPerKey
+                  : FMT == QG_KV_FP8 ? (lane & 3) + 4 * ((lane >> 2 & 1) ^ half)
+                                     : (lane & 1) + 2 * ((lane >> 2 & 1) ^ half);
     constexpr int kChunks = FMT == QG_KV_FP8 ? 2 : 4;        // pieces of eight f16 from one of codes
-    const int lane = threadIdx.x & 31, c = lane % kPerKey, kv = r & 1;
     const uint32_t src = smem_u32(smem + P::kRaw + r * P::kRawStage);
     for (uint32_t n = 0;; ++n) {
         if (!warp_wait(&bar[kRawFull + r], n & 1u, t)) return;
@@ -443,39 +508,37 @@ __device__ __forceinline__ void convert(const TreeArgs& t, uint8_t* smem, uint64
         if (info.left < 0) return;
         if (!warp_wait(&bar[(kv ? kVEmpty : kKEmpty) + info.stage], info.parity ^ 1u, t)) return;
         uint8_t* tile = smem + (kv ? P::kV : P::kK) + info.stage * P::kTile;
-        auto piece = [&](int x, uint4* out) {
-            const int key = (x * 32 + lane) / kPerKey;
-            const uint32_t at = src + P::kCodes + key * kScale;
-            piece_values<FMT>(lds128(src + (x * 32 + lane) * 16), FMT == QG_KV_FP8 ? lds8(at) : lds16(at + 2 * c), out);
-            return key;
-        };
-        if (kv == 0 || !Runs<false>::special(info)) {
-#pragma unroll 4
-            for (int x = 0; x < kN; ++x) {
+#pragma unroll 1
+        for (int x0 = 0; x0 < kN; x0 += kBatch) {
+            // a batch of pieces is read before any is converted, so that one latency covers them all
+            uint4 raw[kBatch];
+            uint32_t sc[kBatch];
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+                const int key = key_of(x0 + x);
+                const uint32_t at = src + P::kCodes + key * kScale;
+                raw[x] = lds128(src + key * kRow + c * 16);
+                sc[x] = FMT == QG_KV_FP8 ? lds8(at) : lds16(at + 2 * c);
+            }
+            if (x0 + kBatch == kN) {                         // the raw stage can be filled again
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kRawEmpty + r]);
+            }
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
                 uint4 out[kChunks];
-                const int key = piece(x, out);
+                piece_values<FMT>(raw[x], sc[x], out);
+                const int key = key_of(x0 + x);
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i)
                     *reinterpret_cast<uint4*>(tile + tile_at<kTcKeys>(key, c * kChunks + i)) = out[i];
             }
-        } else {
-            bool odd = false;
-#pragma unroll 1
-            for (int x = 0; x < kN; ++x) {
-                uint4 out[kChunks];
-                const int key = piece(x, out);
-                const bool on = key < info.left && ((info.groups >> (key >> 4)) & 1u);
-#pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    if (!on) out[i] = make_uint4(0, 0, 0, 0);
-                    if (key >= info.drafts) drop_odd<false>(out[i], odd);
-                    *reinterpret_cast<uint4*>(tile + tile_at<kTcKeys>(key, c * kChunks + i)) = out[i];
-                }
-            }
-            if (odd) *odd_flag = 1;
+        }
+        if (kv == 1 && Runs<false>::special(info)) {
+            __syncwarp();
+            clear_places<D, false>(tile, info.left, info.drafts, info.groups, odd_flag, lane);
         }
         announce(&bar[(kv ? kVFull : kKFull) + info.stage]);
-        if (lane == 0) mbar_arrive(&bar[kRawEmpty + r]);
     }
 }
 
@@ -517,17 +580,8 @@ __device__ __forceinline__ void copy_plain(const TreeArgs& t, const CUtensorMap*
                             static_cast<int32_t>(runs.row), done);
         if (clear) {
             if (!warp_wait(land, landed++ & 1u, t)) return;
-            bool odd = false;
-            for (int x = lane; x < kTcKeys * D / 8; x += 32) {
-                const int key = x / (D / 8);
-                const bool on = key < runs.info.left && ((runs.info.groups >> (key >> 4)) & 1u);
-                if (on && key < runs.info.drafts) continue;
-                uint4* at = reinterpret_cast<uint4*>(tiles + st * kTile + tile_at<kTcKeys>(key, x % (D / 8)));
-                uint4 y = on ? *at : make_uint4(0, 0, 0, 0);
-                drop_odd<true>(y, odd);
-                *at = y;
-            }
-            if (odd) *odd_flag = 1;
+            clear_places<D, true>(tiles + st * kTile, runs.info.left, runs.info.drafts, runs.info.groups, odd_flag,
+                                  lane);
             announce(&full[st]);
         }
     }
@@ -738,6 +792,23 @@ __device__ __forceinline__ bool multiply(const TreeArgs& t, const Cursor* from, 
     return true;
 }
 
+// The sum of the values at column d that are not finite, of the drafts that a
+// row sees (they were left out of the tiles; whatever their weights, they make
+// the output infinite or NaN). Rare.
+__device__ __noinline__ float odd_sum(const KvArgs& a, int b, int head, int first, int end, int len, uint64_t mask,
+                                      int d)
+{
+    float sum = 0.f;
+    for (int p = max(first, len); p < end; ++p) {
+        if (!((mask >> (p - len)) & 1ull)) continue;
+        const int page = kv_page(a, b, p);
+        if (page < 0) continue;
+        const float x = kv_value(a, 1, kv_row(a, page, head, p), d);
+        if (!(fabsf(x) < INFINITY)) sum += x;
+    }
+    return sum;
+}
+
 template <int FMT, int D, bool SHARED>
 __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_constant__ TreeArgs t,
                                                                 const __grid_constant__ CUtensorMap k_map,
@@ -810,7 +881,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
         bool ok = true;
         Cursor mine = from[SHARED ? 0 : s];
         Segment g;
-        while (ok && mine.next(t, g)) {
+        while (ok && mine.template next<SHARED ? 2 * kTcRows : kTcRows>(t, g)) {
             const int base = SHARED ? 128 * s : 0;
             const int n_rows = g.n_rows - base;      // of this stream
             if (n_rows <= 0) continue;
@@ -927,17 +998,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
                 for (int i = 0; i < 32; ++i) v[i] = tc_after_wait(v[i]);
                 if (!on) continue;
                 if (fix) {
-                    // drafts' values that are not finite, left out of the tiles, to the rows that see them
-                    for (int p = max(g.first, g.len); p < g.end; ++p) {
-                        if (!((mask >> (p - g.len)) & 1ull)) continue;
-                        const int page = kv_page(a, g.b, p);
-                        if (page < 0) continue;
-                        const int64_t from = kv_row(a, page, g.head, p);
+#pragma unroll 1
+                    for (int i = 0; i < 32; ++i) {
+                        const float x = odd_sum(a, g.b, g.head, g.first, g.end, g.len, mask, 32 * c + i);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float x = kv_value(a, 1, from, 32 * c + i);
-                            if (!(fabsf(x) < INFINITY)) v[i] = __float_as_uint(__uint_as_float(v[i]) + x);
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (e == i) v[e] = __float_as_uint(__uint_as_float(v[e]) + x);
                     }
                 }
                 if (g.slot < 0) {

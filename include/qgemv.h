@@ -397,7 +397,7 @@ typedef struct {
  *   n_seqs       0..1024     max_pages >= 1     n_tokens 0..2^24 (rows)
  * Rows behind the last sequence are neither read nor written. A sequence
  * whose entries do not fit (a negative length, rows outside n_tokens,
- * positions beyond max_pages * page_size) is left out, and so is a token
+ * positions beyond max_pages * page_size or 2^30) is left out, and so is a token
  * whose page lies outside the cache; each records QG_ERR_INVALID_ARG in the
  * device status word. (Where token_start does not ascend, rows that two
  * sequences claim may be left out with the one that does not fit.) Sequences
