@@ -27,14 +27,14 @@ constexpr int kTcKeys = 64;                  // keys per tile
 constexpr int kTcRows = 128;                 // rows per stream
 constexpr int kTcThreads = 512;               // four warpgroups, 128 registers per thread at launch ...
 constexpr int kMmaWarp = 12;                  // of stream 0; the next warp is stream 1's
-constexpr int kIssueWarp = 14;                // starts the copies of coded keys and values
+constexpr int kCopyWarp = 14;                 // starts the copies of coded keys, the next of values
 constexpr int kLaunchRegs = 128;
 constexpr int kSoftmaxRegs = 144;            // ... dealt out anew: 2 * 144 + 104 + 120 = 4 * 128
 constexpr int kLoadRegs = 104;
 constexpr int kIssueRegs = 120;
 static_assert(2 * kSoftmaxRegs + kLoadRegs + kIssueRegs <= 4 * kLaunchRegs, "more registers than the block has");
 constexpr int kStages = 4;                   // tiles of keys and of values (SHARED; else two per stream)
-constexpr int kRawStages = 4;                // tiles as they are stored, one per converting warp
+constexpr int kMaxRaw = 4;                   // tiles of keys, and of values, as they are stored
 // Weights are 2^(s - m + 8) with m a whole number from the row's largest score
 // (rounded up), replaced only once a score passes it by 7: a weight is at most
 // 2^15, within f16, the largest at least 2^7, and a change of m scales what was
@@ -51,9 +51,9 @@ enum Bar : int {
     kSFull = kQFull + 2,                     // [2 * stream + buffer]
     kPFull = kSFull + 4,
     kPvDone = kPFull + 4,
-    kRawFull = kPvDone + 4,                  // [raw stage]
-    kRawEmpty = kRawFull + kRawStages,
-    kVLand = kRawEmpty + kRawStages,
+    kRawFull = kPvDone + 4,                  // [2 * raw stage + (0: keys, 1: values)]
+    kRawEmpty = kRawFull + 2 * kMaxRaw,
+    kVLand = kRawEmpty + 2 * kMaxRaw,
     kDrain = kVLand + 1,                     // [stream]
     kBars = kDrain + 2
 };
@@ -69,8 +69,10 @@ struct TcPlan {
     static constexpr int kRaw = kV + kStages * kTile;
     static constexpr int kCodes = kTcKeys * kv_row_bytes(FMT, D);
     static constexpr int kRawStage = FMT == QG_KV_BF16 ? 0 : kCodes + kTcKeys * kv_scale_bytes(FMT, D);
-    static constexpr int kSmem = kRaw + kRawStages * kRawStage + 1024;   // + alignment
-    static_assert(kSmem <= 227 * 1024, "too much shared memory");
+    static constexpr int kFit = kRawStage ? (227 * 1024 - 1024 - kRaw) / (2 * (kRawStage ? kRawStage : 1)) : 0;
+    static constexpr int kNRaw = kFit < kMaxRaw ? kFit : kMaxRaw;
+    static constexpr int kSmem = kRaw + 2 * kNRaw * kRawStage + 1024;    // + alignment
+    static_assert(kSmem <= 227 * 1024 && (FMT == QG_KV_BF16 || kNRaw >= 2), "too much shared memory");
     static_assert(kBars * 8 <= 512, "barriers");
 };
 
@@ -280,12 +282,14 @@ struct RawInfo {
     uint32_t groups;             // groups of 16 keys whose page lies in the cache
     uint32_t stage;              // where it goes, and the parity of its phase there
     uint32_t parity;
-    int pad[3];
+    uint32_t seq;                // which tile it is
+    int pad[2];
 };
 
 // The runs of a tile: consecutive keys of one page, t.run of them (the largest
-// of 16, 32 and 64 that divides the page size), one lane each. The page
-// table is read a tile ahead.
+// of 16, 32 and 64 that divides the page size), one lane each. The page table
+// is read 32 runs at a time, a lane each, and 32 runs ahead, so that a tile
+// waits for none of it but at a segment's start.
 template <bool SHARED>
 struct Runs {
     Items<SHARED> items;
@@ -295,21 +299,41 @@ struct Runs {
     RawInfo info;
     bool more;
     Segment g;
-    int j, entry, owner;
+    int j, owner;
+    int now[2], then[2];         // by stream: this lane's entries of the 32 runs at hand, and of the next 32
     uint32_t n[2];               // tiles of each ring so far
 
     __device__ __forceinline__ int key() const { return (threadIdx.x & 31); }
 
+    __device__ __forceinline__ int entry(const TreeArgs& t, int q) const
+    {
+        const int p = g.first + (q + key()) * t.run;
+        return p < g.end ? kv_entry(t.a, g.b, p) : 0;
+    }
+
+    // What the tile at hand needs of the page table is on its way.
+    template <int S>
     __device__ __forceinline__ void look_up(const TreeArgs& t)
     {
-        const int p = g.first + j * kTcKeys + key() * t.run;
-        entry = owner >= 0 && key() * t.run < kTcKeys && p < g.end ? kv_entry(t.a, g.b, p) : 0;
+        const int q = j * (kTcKeys / t.run);                 // its first run in the segment
+        if (q % 32) return;
+        now[S] = j ? then[S] : entry(t, 0);
+        then[S] = entry(t, q + 32);
+    }
+
+    __device__ __forceinline__ void look_up(const TreeArgs& t)
+    {
+        if (owner == 0)
+            look_up<0>(t);
+        else if (!SHARED && owner == 1)
+            look_up<SHARED ? 0 : 1>(t);
     }
 
     __device__ __forceinline__ void start(const TreeArgs& t, const Cursor* from)
     {
         items.start(t, from);
         n[0] = n[1] = 0;
+        now[0] = now[1] = then[0] = then[1] = 0;
         owner = items.next(t, g, j);
         look_up(t);
         step(t);
@@ -325,8 +349,9 @@ struct Runs {
         const int p0 = g.first + j * kTcKeys, k0 = key() * t.run;
         info.left = min(kTcKeys, g.end - p0);
         info.drafts = g.len - p0;
-        const bool mine = k0 < info.left;
-        const int page = mine ? kv_valid(t.a, entry) : -1;
+        const int at = j * (kTcKeys / t.run) % 32 + key();
+        const int found = __shfl_sync(0xffffffffu, !SHARED && owner ? now[1] : now[0], at & 31);
+        const int page = k0 < info.left ? kv_valid(t.a, found) : -1;
         on = page >= 0;
         row = on ? kv_row(t.a, page, g.head, p0 + k0) : 0;
         keys = on ? min(t.run, (info.left - k0 + 15) & ~15) : 0;
@@ -421,71 +446,78 @@ __device__ __noinline__ void clear_places(uint8_t* tile, int left, int drafts, u
     __syncwarp();
 }
 
-// Coded keys and values: one warp starts the copies of the tiles as they are
-// stored, keys and values in turn, into four raw stages. On a timeout it waits
+// Coded keys (kv = 0) or values (1): one warp each starts the copies of the
+// tiles as they are stored, into a ring of raw stages. On a timeout it waits
 // for the copies that are on their way.
 template <int FMT, int D, bool SHARED>
 __device__ __forceinline__ void copy_coded(const TreeArgs& t, const Cursor* from, uint8_t* smem, uint64_t* bar,
-                                           RawInfo* infos)
+                                           RawInfo* infos, int kv)
 {
     using P = TcPlan<FMT, D>;
     constexpr int kRow = kv_row_bytes(FMT, D), kScale = kv_scale_bytes(FMT, D);
-    const KvArgs& a = t.a;
     const int lane = threadIdx.x & 31;
+    const uint8_t* codes = t.a.codes[kv];
+    const uint8_t* scales = t.a.scales[kv];
+    const bool go = kv == 1 || !t.starve;
     Runs<SHARED> runs;
     runs.start(t, from);
-    uint32_t job = 0;
-    bool ok = true;
-    while (ok && runs.more) {
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++job) {
-            const uint32_t r = job % kRawStages;
-            ok = warp_wait(&bar[kRawEmpty + r], (job / kRawStages & 1u) ^ 1u, t);
-            if (!ok) break;
-            const uint32_t bytes = __popc(runs.info.groups) * 16 * (kRow + kScale);
-            uint8_t* dst = smem + P::kRaw + r * P::kRawStage;
-            if (lane == 0) {
-                infos[r] = runs.info;
-                if (!t.starve) mbar_arrive_expect_tx(&bar[kRawFull + r], bytes);
-            }
-            __syncwarp();
-            if (runs.on && !t.starve) {
-                const int k0 = lane * t.run;
-                bulk_load(dst + k0 * kRow, a.codes[kv] + runs.row * kRow, runs.keys * kRow, &bar[kRawFull + r]);
-                bulk_load(dst + P::kCodes + k0 * kScale, a.scales[kv] + runs.row * kScale, runs.keys * kScale,
-                          &bar[kRawFull + r]);
-            }
+    uint32_t r = 0, phase = 0, n = 0;                        // raw stage, its phase's parity, tiles
+    auto advance = [&]() {
+        ++n;
+        if (++r == P::kNRaw) {
+            r = 0;
+            phase ^= 1u;
         }
-        if (ok) runs.step(t);
-    }
-    if (!ok) {
-        if (!t.starve)
-            for (uint32_t x = job > kRawStages ? job - kRawStages : 0; x < job; ++x)
-                warp_wait(&bar[kRawFull + x % kRawStages], x / kRawStages & 1u, t);
-        return;
-    }
-    for (int x = 0; x < kRawStages; ++x, ++job) {                // no more: to every converting warp
-        const uint32_t r = job % kRawStages;
-        if (!warp_wait(&bar[kRawEmpty + r], (job / kRawStages & 1u) ^ 1u, t)) return;
+    };
+    for (; runs.more; advance()) {
+        const uint32_t x = 2 * r + kv;
+        if (!warp_wait(&bar[kRawEmpty + x], phase ^ 1u, t)) {
+            for (uint32_t y = go && n > P::kNRaw ? n - P::kNRaw : 0; go && y < n; ++y)
+                warp_wait(&bar[kRawFull + 2 * (y % P::kNRaw) + kv], y / P::kNRaw & 1u, t);
+            return;
+        }
+        uint8_t* dst = smem + P::kRaw + x * P::kRawStage;
         if (lane == 0) {
-            infos[r].left = -1;
-            mbar_arrive(&bar[kRawFull + r]);
+            runs.info.seq = n;
+            infos[x] = runs.info;
+            if (go) mbar_arrive_expect_tx(&bar[kRawFull + x], __popc(runs.info.groups) * 16 * (kRow + kScale));
         }
+        __syncwarp();
+        if (runs.on && go) {
+            const int k0 = lane * t.run;
+            bulk_load(dst + k0 * kRow, codes + runs.row * kRow, runs.keys * kRow, &bar[kRawFull + x]);
+            bulk_load(dst + P::kCodes + k0 * kScale, scales + runs.row * kScale, runs.keys * kScale,
+                      &bar[kRawFull + x]);
+        }
+        runs.step(t);
+    }
+    for (int y = 0; y < 2; ++y, advance()) {                 // no more: to both converting warps
+        const uint32_t x = 2 * r + kv;
+        if (!warp_wait(&bar[kRawEmpty + x], phase ^ 1u, t)) return;
+        if (lane == 0) {
+            infos[x].left = -1;
+            infos[x].seq = n;
+            mbar_arrive(&bar[kRawFull + x]);
+        }
+        __syncwarp();
     }
 }
 
-// ... and four warps, each a raw stage and every fourth tile of its own,
-// convert them to f16 tiles.
+// ... and two warps convert keys, two values, every second tile each, to f16
+// tiles. The two meet in a stage by turns, and a stage's parity alone would let
+// a warp pass that comes too early (while the tile one round before its own has
+// not landed): it looks at the tile's number too, and then at the parity again.
 template <int FMT, int D>
 __device__ __forceinline__ void convert(const TreeArgs& t, uint8_t* smem, uint64_t* bar, const RawInfo* infos,
-                                        volatile int* odd_flag, int r)
+                                        volatile int* odd_flag, int w)
 {
     using P = TcPlan<FMT, D>;
     constexpr int kRow = kv_row_bytes(FMT, D), kScale = kv_scale_bytes(FMT, D);
     constexpr int kPerKey = kRow / 16;                       // pieces of a row
     constexpr int kN = kTcKeys * kPerKey / 32;               // pieces per lane
-    const int lane = threadIdx.x & 31, kv = r & 1;
+    constexpr int kChunks = FMT == QG_KV_FP8 ? 2 : 4;        // pieces of eight f16 from one of codes
     constexpr int kBatch = 4;
+    const int lane = threadIdx.x & 31, kv = w & 1;
     // Piece x of this lane. At head_dim 128 eight neighbouring lanes take keys
     // of all residues (mod 2 for FP8, mod 4 for NVFP4) and, by residue, one or
     // the other half of the row: their reads and their swizzled writes then
@@ -500,35 +532,45 @@ __device__ __forceinline__ void convert(const TreeArgs& t, uint8_t* smem, uint64
     const int c = D != 128 ? lane % kPerKey
                   : FMT == QG_KV_FP8 ? (lane & 3) + 4 * ((lane >> 2 & 1) ^ half)
                                      : (lane & 1) + 2 * ((lane >> 2 & 1) ^ half);
-    constexpr int kChunks = FMT == QG_KV_FP8 ? 2 : 4;        // pieces of eight f16 from one of codes
-    const uint32_t src = smem_u32(smem + P::kRaw + r * P::kRawStage);
-    for (uint32_t n = 0;; ++n) {
-        if (!warp_wait(&bar[kRawFull + r], n & 1u, t)) return;
-        const RawInfo info = infos[r];
+    for (uint32_t n = w >> 1;; n += 2) {
+        const uint32_t x = 2 * (n % P::kNRaw) + kv, phase = n / P::kNRaw & 1u;
+        const volatile RawInfo* v = &infos[x];
+        const uint64_t t0 = global_timer_ns();
+        for (;;) {
+            if (!warp_wait(&bar[kRawFull + x], phase, t)) return;
+            if (__all_sync(0xffffffffu, v->seq == n)) break;
+            if (__any_sync(0xffffffffu, global_timer_ns() - t0 > t.wait_ns)) {
+                set_device_status(t.a.status, QG_ERR_DEVICE_TIMEOUT);
+                return;
+            }
+        }
+        if (!warp_wait(&bar[kRawFull + x], phase, t)) return;
+        const RawInfo info = infos[x];
         if (info.left < 0) return;
         if (!warp_wait(&bar[(kv ? kVEmpty : kKEmpty) + info.stage], info.parity ^ 1u, t)) return;
+        const uint32_t src = smem_u32(smem + P::kRaw + x * P::kRawStage);
         uint8_t* tile = smem + (kv ? P::kV : P::kK) + info.stage * P::kTile;
 #pragma unroll 1
-        for (int x0 = 0; x0 < kN; x0 += kBatch) {
+        for (int y0 = 0; y0 < kN; y0 += kBatch) {
             // a batch of pieces is read before any is converted, so that one latency covers them all
             uint4 raw[kBatch];
             uint32_t sc[kBatch];
 #pragma unroll
-            for (int x = 0; x < kBatch; ++x) {
-                const int key = key_of(x0 + x);
+            for (int y = 0; y < kBatch; ++y) {
+                const int key = key_of(y0 + y);
                 const uint32_t at = src + P::kCodes + key * kScale;
-                raw[x] = lds128(src + key * kRow + c * 16);
-                sc[x] = FMT == QG_KV_FP8 ? lds8(at) : lds16(at + 2 * c);
+                raw[y] = lds128(src + key * kRow + c * 16);
+                sc[y] = FMT == QG_KV_FP8 ? lds8(at) : lds16(at + 2 * c);
             }
-            if (x0 + kBatch == kN) {                         // the raw stage can be filled again
+            if (y0 + kBatch == kN) {                         // the raw stage can be filled again
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[kRawEmpty + r]);
+                if (lane == 0) mbar_arrive(&bar[kRawEmpty + x]);
             }
 #pragma unroll
-            for (int x = 0; x < kBatch; ++x) {
+            for (int y = 0; y < kBatch; ++y) {
                 uint4 out[kChunks];
-                piece_values<FMT>(raw[x], sc[x], out);
-                const int key = key_of(x0 + x);
+                piece_values<FMT>(raw[y], sc[y], out);
+                const int key = key_of(y0 + y);
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i)
                     *reinterpret_cast<uint4*>(tile + tile_at<kTcKeys>(key, c * kChunks + i)) = out[i];
@@ -853,11 +895,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
             mbar_init(&bar[kPFull + x], 4);
             mbar_init(&bar[kPvDone + x], 1);
         }
-        for (int x = 0; x < kRawStages; ++x) {
+        for (int x = 0; x < 2 * kMaxRaw; ++x) {
             mbar_init(&bar[kRawFull + x], 1);
             mbar_init(&bar[kRawEmpty + x], 1);
         }
         mbar_init(&bar[kVLand], 1);
+        for (int x = 0; x < 2 * kMaxRaw; ++x) infos[x].seq = ~0u;
         *odd_flag = 0;
         fence_barrier_init();
     }
@@ -1054,8 +1097,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
                 if (leader) tc_commit(&bar[kDrain + s]);     // given up: products on their way still end
                 warp_wait(&bar[kDrain + s], 0, t);
             }
-        } else if (!kBf16 && warp == kIssueWarp) {
-            if constexpr (!kBf16) copy_coded<FMT, D, SHARED>(t, from, smem, bar, infos);
+        } else if constexpr (!kBf16) {
+            copy_coded<FMT, D, SHARED>(t, from, smem, bar, infos, warp - kCopyWarp);
         }
     }
     tc_fence_before();
