@@ -56,39 +56,85 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi)
     return r;
 }
 
-__device__ __forceinline__ uint32_t max8_bits(const float (&y)[8])
+// x / d to nearest, for eight x: with r = 1 / d to nearest and q = x r, one
+// residual x - q d (exact in an fma) corrects q to the nearest quotient
+// (Markstein, IBM J. Res. Dev. 34, 1990). That holds while nothing leaves the
+// normal range: the largest |x|, `top`, and d lie within 2^+-60, and
+// an x so much smaller that its residual is not exact is a zero code whatever
+// its last bit. Else the division itself.
+__device__ __forceinline__ void divide8(float (&x)[8], float d, float top)
 {
-    uint32_t m = 0;
+    const uint32_t e = __float_as_uint(top) >> 23, ed = __float_as_uint(d) >> 23;
+    if (e > 67u && e < 187u && ed > 67u && ed < 187u) {
+        const float r = __frcp_rn(d);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 8; ++i) {
+            const float q = x[i] * r;
+            x[i] = fmaf(fmaf(-q, d, x[i]), r, q);
+        }
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            // x[i] = x[i] / d without indexing registers
+            float v = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v = i == j ? x[j] : v;
+            v = __fdiv_rn(v, d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = i == j ? v : x[j];
+        }
+    }
+}
+
+// The largest |y|, NaN left out; and with a NaN if there is one.
+__device__ __forceinline__ float max8(const float (&y)[8])
+{
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
     return m;
 }
 
-// The sequence that row i belongs to: the number of sequences that end at or
-// before it, by ballots over 32 sequences at a time (one load latency for up
-// to 32). n_seqs for a row behind the last sequence.
-__device__ __forceinline__ int seq_of_row(const KvArgs& a, int i, int lane)
+__device__ __forceinline__ float max_nan(float a, float b)
 {
-    int b = 0;
-    for (int j = 0; j < a.n_seqs; j += 32) {
-        const bool before = j + lane < a.n_seqs && a.start[j + lane + 1] <= i;
-        const int n = __popc(__ballot_sync(0xffffffffu, before));
-        b += n;
-        if (n < 32) break;
-    }
-    return b;
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
-// The place of row i: its page and position, or false if it has none.
-__device__ __forceinline__ bool place_of_row(const KvArgs& a, int i, int lane, int& page, int& pos)
+// The places of T consecutive rows: their pages and positions, page -2 for a
+// row that has none, -1 for one whose page lies outside the cache. A row's
+// sequence is the number of sequences that end at or before it, by ballots over
+// 32 sequences at a time; the T rows share each of the three chained loads
+// (token_start, the sequence, the page table).
+template <int T>
+__device__ __forceinline__ void places(const KvArgs& a, int i0, int lane, int (&page)[T], int (&pos)[T])
 {
-    const int b = seq_of_row(a, i, lane);
-    if (b >= a.n_seqs) return false;
-    const KvSeq s = kv_seq(a, b, a.n_tokens);
-    if (i < s.row0 || i - s.row0 >= s.rows) return false;
-    pos = s.len + (i - s.row0);
-    page = kv_page(a, b, pos);
-    return true;
+    int b[T] = {};
+    for (int j = 0; j < a.n_seqs; j += 32) {
+        const int end = j + lane < a.n_seqs ? a.start[j + lane + 1] : 0x7FFFFFFF;
+        bool more = false;
+#pragma unroll
+        for (int x = 0; x < T; ++x) {
+            const int n = __popc(__ballot_sync(0xffffffffu, end <= i0 + x));
+            if (b[x] == j) b[x] += n;
+            more = more || n == 32;
+        }
+        if (!more) break;
+    }
+    KvSeq s[T];
+#pragma unroll
+    for (int x = 0; x < T; ++x) s[x] = b[x] < a.n_seqs ? kv_seq(a, b[x], a.n_tokens) : KvSeq{0, 0, 0};
+    int entry[T];
+#pragma unroll
+    for (int x = 0; x < T; ++x) {
+        const int at = i0 + x - s[x].row0;
+        const bool on = at >= 0 && at < s[x].rows;
+        pos[x] = on ? s[x].len + at : -1;
+        entry[x] = on ? kv_entry(a, b[x], pos[x]) : 0;
+    }
+#pragma unroll
+    for (int x = 0; x < T; ++x) page[x] = pos[x] < 0 ? -2 : kv_valid(a, entry[x]);
 }
 
 // Every sequence's entries are looked at once per call, so that one that no
@@ -111,21 +157,13 @@ __device__ __forceinline__ void store8(const KvArgs& a, int kv, int64_t row, int
         float y[8];
         unpack8(raw, y);
         const float g = a.g[kv];
-        if (g != 1.f) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(y[i], g);
-        }
+        if (g != 1.f) divide8(y, g, max8(y));
         if constexpr (FMT == QG_KV_FP8) {
-            // a NaN (bits above infinity's) does not count for the maximum
-            uint32_t m = 0;
+            float top = max8(y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t v = __float_as_uint(y[i]) & 0x7FFFFFFFu;
-                m = max(m, v > 0x7F800000u ? 0u : v);
-            }
-#pragma unroll
-            for (int off = 1; off < DIM / 8; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-            // 448 = 1.75 * 2^8, so m <= 448 * 2^e first at e = exponent - 8, one more above 1.75
+            for (int off = 1; off < DIM / 8; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            // 448 = 1.75 * 2^8, so top <= 448 * 2^e first at e = exponent - 8, one more above 1.75
+            const uint32_t m = __float_as_uint(top);
             const int e = max(-14, min(7, static_cast<int>(m >> 23) - 135 + ((m & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
             const float up = __int_as_float((127 - e) << 23);
             uint32_t w[2];
@@ -138,18 +176,19 @@ __device__ __forceinline__ void store8(const KvArgs& a, int kv, int64_t row, int
                 if (c == 0) a.scales[kv][row] = static_cast<uint8_t>(e + 15);
             }
         } else {
-            uint32_t m = max8_bits(y);
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(y[i]));
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
             uint32_t sc, w = 0;
-            if (m > 0x7F800000u) {
+            if (top != top) {
                 sc = 0x7F;  // NaN
             } else {
-                sc = to_e4m3x2(__fdiv_rn(__uint_as_float(m), 6.f), 0.f) & 0xFFu;
+                sc = to_e4m3x2(__fdiv_rn(top, 6.f), 0.f) & 0xFFu;
                 if (sc) {
-                    const float f = half_bits_to_f32(e4m3x2_to_f16x2(sc) & 0xFFFFu);
+                    divide8(y, half_bits_to_f32(e4m3x2_to_f16x2(sc) & 0xFFFFu), top);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        w |= to_e2m1x2(__fdiv_rn(y[2 * i], f), __fdiv_rn(y[2 * i + 1], f)) << (8 * i);
+                    for (int i = 0; i < 4; ++i) w |= to_e2m1x2(y[2 * i], y[2 * i + 1]) << (8 * i);
                 }
             }
             if (row >= 0) {
@@ -160,118 +199,149 @@ __device__ __forceinline__ void store8(const KvArgs& a, int kv, int64_t row, int
     }
 }
 
-// A warp takes U * 32 lanes' worth of one token's rows (keys of every head,
-// then values).
-template <int FMT, int DIM, int U>
-__global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(KvArgs a, const uint16_t* k, int64_t k_stride,
+// A warp takes U * 32 lanes' worth of the rows (keys of every head, then
+// values) of T consecutive tokens.
+template <int FMT, int DIM, int T, int U>
+__global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const __grid_constant__ KvArgs a, const uint16_t* k, int64_t k_stride,
                                                                 const uint16_t* v, int64_t v_stride, int parts)
 {
     pdl_enter();
     check_all(a);
     const int lane = threadIdx.x & 31;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int i = static_cast<int>(unit / parts);
-    if (i >= a.n_tokens) return;
+    const int i0 = static_cast<int>(unit / parts) * T;
+    if (i0 >= a.n_tokens) return;
     constexpr int kLanes = DIM / 8;                 // lanes of a row
     const int per_side = a.heads * kLanes;
     const int first = static_cast<int>(unit % parts) * 32 * U + lane;
-    uint4 raw[U];
+    uint4 raw[T][U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int x = first + 32 * u;
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (x < 2 * per_side) {
-            const uint16_t* src = x < per_side ? k + i * k_stride + x * 8 : v + i * v_stride + (x - per_side) * 8;
-            raw[u] = *reinterpret_cast<const uint4*>(src);
+    for (int y = 0; y < T; ++y)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int x = first + 32 * u;
+            raw[y][u] = make_uint4(0, 0, 0, 0);
+            if (x < 2 * per_side && i0 + y < a.n_tokens) {
+                const int64_t i = i0 + y;
+                const uint16_t* src = x < per_side ? k + i * k_stride + x * 8 : v + i * v_stride + (x - per_side) * 8;
+                raw[y][u] = ldg_nc_128(src);
+            }
         }
-    }
-    int page, pos;
-    if (!place_of_row(a, i, lane, page, pos) || page < 0) return;
+    int page[T], pos[T];
+    places<T>(a, i0, lane, page, pos);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int x = first + 32 * u;
-        const int kv = x >= per_side;
-        const int y = x - kv * per_side;
-        const int64_t row = x < 2 * per_side ? kv_row(a, page, y / kLanes, pos) : -1;
-        store8<FMT, DIM>(a, kv, row, y % kLanes, raw[u], lane);
+    for (int y = 0; y < T; ++y) {
+        if (page[y] < 0) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int x = first + 32 * u;
+            const int kv = x >= per_side;
+            const int z = x - kv * per_side;
+            const int64_t row = x < 2 * per_side ? kv_row(a, page[y], z / kLanes, pos[y]) : -1;
+            store8<FMT, DIM>(a, kv, row, z % kLanes, raw[y][u], lane);
+        }
     }
 }
 
 // ------------------------------------------------------------------ read
-// The f16 values (code * scale, exact) of one lane's eight codes.
+// One lane's eight values as they are stored. All zeros read as zeros.
 template <int FMT>
-__device__ __forceinline__ void load8(const uint8_t* codes, const uint8_t* scales, int64_t row, int c, int dim,
-                                      float g, float (&f)[8])
-{
-    if constexpr (FMT == QG_KV_BF16) {
-        unpack8(ldg_nc_128(codes + row * (2 * dim) + c * 16), f);
-    } else {
-        uint32_t h[4], s;
-        if constexpr (FMT == QG_KV_FP8) {
-            const uint2 w = *reinterpret_cast<const uint2*>(codes + row * dim + c * 8);
-            h[0] = e4m3x2_to_f16x2(w.x & 0xFFFFu);
-            h[1] = e4m3x2_to_f16x2(w.x >> 16);
-            h[2] = e4m3x2_to_f16x2(w.y & 0xFFFFu);
-            h[3] = e4m3x2_to_f16x2(w.y >> 16);
-            s = static_cast<uint32_t>(scales[row]) << 10;   // 2^(s-15) as f16
+struct Stored {
+    uint4 codes;                 // FP8: two words, NVFP4: one
+    uint32_t scale;
+
+    __device__ __forceinline__ void load(const uint8_t* c, const uint8_t* s, int64_t row, int piece, int dim)
+    {
+        if constexpr (FMT == QG_KV_BF16) {
+            codes = ldg_nc_128(c + row * (2 * dim) + piece * 16);
+        } else if constexpr (FMT == QG_KV_FP8) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(c + row * dim + piece * 8));
+            codes.x = w.x;
+            codes.y = w.y;
+            scale = __ldg(s + row);
         } else {
-            e2m1x8_to_f16x2x4(*reinterpret_cast<const uint32_t*>(codes + row * (dim / 2) + c * 4), h);
-            s = e4m3x2_to_f16x2(scales[row * (dim / 16) + c / 2]) & 0xFFFFu;
-        }
-        s |= s << 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t p = hmul2(h[i], s);
-            f[2 * i] = half_bits_to_f32(p & 0xFFFFu) * g;
-            f[2 * i + 1] = half_bits_to_f32(p >> 16) * g;
+            codes.x = __ldg(reinterpret_cast<const uint32_t*>(c + row * (dim / 2) + piece * 4));
+            scale = __ldg(s + row * (dim / 16) + piece / 2);
         }
     }
-}
 
-template <int FMT, int DIM, int U>
-__global__ void __launch_bounds__(32 * kWarps) kv_read_kernel(KvArgs a, void* k_out, void* v_out, int f32, int parts)
+    // code * scale is an f16 number; times g in 32 bits
+    __device__ __forceinline__ void values(float g, float (&f)[8]) const
+    {
+        if constexpr (FMT == QG_KV_BF16) {
+            unpack8(codes, f);
+        } else {
+            uint32_t h[4], s2;
+            if constexpr (FMT == QG_KV_FP8) {
+                e4m3x4_to_f16x2x2(codes.x, h[0], h[1]);
+                e4m3x4_to_f16x2x2(codes.y, h[2], h[3]);
+                s2 = scale * 0x04000400u;                        // 2^(s-15) as f16, twice
+            } else {
+                e2m1x8_to_f16x2x4(codes.x, h);
+                const uint32_t e = e4m3x2_to_f16x2(scale);
+                s2 = __byte_perm(e, e, 0x1010);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t p = hmul2(h[i], s2);
+                f[2 * i] = half_bits_to_f32(p & 0xFFFFu) * g;
+                f[2 * i + 1] = half_bits_to_f32(p >> 16) * g;
+            }
+        }
+    }
+};
+
+template <int FMT, int DIM, int T, int U>
+__global__ void __launch_bounds__(32 * kWarps) kv_read_kernel(const __grid_constant__ KvArgs a, void* k_out, void* v_out, int f32, int parts)
 {
     pdl_enter();
     check_all(a);
     const int lane = threadIdx.x & 31;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int i = static_cast<int>(unit / parts);
-    if (i >= a.n_tokens) return;
+    const int i0 = static_cast<int>(unit / parts) * T;
+    if (i0 >= a.n_tokens) return;
     constexpr int kLanes = DIM / 8;
     const int per_side = a.heads * kLanes;
     const int first = static_cast<int>(unit % parts) * 32 * U + lane;
-    int page, pos;
-    if (!place_of_row(a, i, lane, page, pos)) return;
-    float f[U][8];
+    int page[T], pos[T];
+    places<T>(a, i0, lane, page, pos);
+    Stored<FMT> raw[T][U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int x = first + 32 * u;
+    for (int y = 0; y < T; ++y)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[u][j] = 0.f;
-        if (x < 2 * per_side && page >= 0) {
-            const int kv = x >= per_side;
-            const int y = x - kv * per_side;
-            load8<FMT>(a.codes[kv], a.scales[kv], kv_row(a, page, y / kLanes, pos), y % kLanes, DIM, a.g[kv], f[u]);
+        for (int u = 0; u < U; ++u) {
+            const int x = first + 32 * u;
+            raw[y][u] = Stored<FMT>{};
+            if (x < 2 * per_side && page[y] >= 0) {
+                const int kv = x >= per_side;
+                const int z = x - kv * per_side;
+                raw[y][u].load(a.codes[kv], a.scales[kv], kv_row(a, page[y], z / kLanes, pos[y]), z % kLanes, DIM);
+            }
         }
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int x = first + 32 * u;
-        if (x >= 2 * per_side) continue;
-        const int kv = x >= per_side;
-        const int64_t at = (static_cast<int64_t>(i) * per_side + (x - kv * per_side)) * 8;
-        void* out = kv ? v_out : k_out;
-        if (f32) {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-            o[0] = make_float4(f[u][0], f[u][1], f[u][2], f[u][3]);
-            o[1] = make_float4(f[u][4], f[u][5], f[u][6], f[u][7]);
-        } else {
-            uint4 o;
-            o.x = pack_bf16x2(f[u][0], f[u][1]);
-            o.y = pack_bf16x2(f[u][2], f[u][3]);
-            o.z = pack_bf16x2(f[u][4], f[u][5]);
-            o.w = pack_bf16x2(f[u][6], f[u][7]);
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = o;
+    for (int y = 0; y < T; ++y) {
+        if (page[y] < -1) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int x = first + 32 * u;
+            if (x >= 2 * per_side) continue;
+            const int kv = x >= per_side;
+            float f[8];
+            raw[y][u].values(a.g[kv], f);
+            const int64_t at = (static_cast<int64_t>(i0 + y) * per_side + (x - kv * per_side)) * 8;
+            void* out = kv ? v_out : k_out;
+            if (f32) {
+                float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+                o[0] = make_float4(f[0], f[1], f[2], f[3]);
+                o[1] = make_float4(f[4], f[5], f[6], f[7]);
+            } else {
+                uint4 o;
+                o.x = pack_bf16x2(f[0], f[1]);
+                o.y = pack_bf16x2(f[2], f[3]);
+                o.z = pack_bf16x2(f[4], f[5]);
+                o.w = pack_bf16x2(f[6], f[7]);
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = o;
+            }
         }
     }
 }
@@ -309,7 +379,7 @@ __device__ __forceinline__ void move_column(const KvArgs& a, const KvSeq& s, int
 // One block per sequence. It checks the path and the pages first (a sequence
 // is moved as a whole or not at all), and only then writes, new_lens last, so
 // that new_lens may be seq_lens.
-__global__ void __launch_bounds__(kAcceptThreads) kv_accept_kernel(KvArgs a, const int32_t* path,
+__global__ void __launch_bounds__(kAcceptThreads) kv_accept_kernel(const __grid_constant__ KvArgs a, const int32_t* path,
                                                                    const int32_t* n_accept, int32_t* new_lens)
 {
     pdl_enter();
@@ -345,21 +415,29 @@ __global__ void __launch_bounds__(kAcceptThreads) kv_accept_kernel(KvArgs a, con
     if (new_lens && threadIdx.x == 0) new_lens[b] = s.len + n;
 }
 
-// Warps of a call over every token's rows: U * 32 lanes each. Four pieces per
-// lane once that still fills the GPU several times over, else one, so that a
-// decode step's few rows spread over more SMs.
+// How a call's rows are dealt to warps: one token and 32 lanes each, so that a
+// decode step's few rows spread over many SMs, or 128 lanes of one token
+// (append) or two (read) once that still makes four warps per scheduler.
+// Measured on 32,256 tokens of 4 heads of 128, append in FP8 and read of NVFP4
+// (us): 1 x 128 lanes 26.2 and 20.2, 2 x 128 28.0 and 18.1, 2 x 64 29.3 and
+// 21.9, 4 x 64 30.4 and 20.3, 2 x 32 34.4 and 27.5.
+constexpr int kPieces = 4, kAppendTokens = 1, kReadTokens = 2;
+
 struct RowPlan {
-    int u, parts;
+    bool wide;
+    int parts;
     unsigned blocks;
 };
 
-RowPlan plan_rows(const KvArgs& a)
+RowPlan plan_rows(const KvArgs& a, int wide_tokens)
 {
     const int64_t lanes = 2LL * a.heads * (a.dim / 8);
     RowPlan p;
-    p.u = a.n_tokens * lanes >= 4LL * 32 * 64 * sm_count(-1) ? 4 : 1;
-    p.parts = static_cast<int>((lanes + 32 * p.u - 1) / (32 * p.u));
-    p.blocks = static_cast<unsigned>((static_cast<int64_t>(a.n_tokens) * p.parts + kWarps - 1) / kWarps);
+    p.wide = a.n_tokens * lanes >= 32LL * wide_tokens * kPieces * 16 * sm_count(-1);
+    const int per = 32 * (p.wide ? kPieces : 1), tokens = p.wide ? wide_tokens : 1;
+    p.parts = static_cast<int>((lanes + per - 1) / per);
+    const int64_t warps = (static_cast<int64_t>(a.n_tokens) + tokens - 1) / tokens * p.parts;
+    p.blocks = static_cast<unsigned>((warps + kWarps - 1) / kWarps);
     return p;
 }
 
@@ -367,23 +445,17 @@ template <int FMT, int DIM>
 cudaError_t append_dim(const KvArgs& a, const uint16_t* k, int64_t ks, const uint16_t* v, int64_t vs,
                        cudaStream_t stream)
 {
-    const RowPlan p = plan_rows(a);
-    if (p.u == 4)
-        return launch_pdl(kv_append_kernel<FMT, DIM, 4>, dim3(p.blocks), dim3(32 * kWarps), 0, stream, a, k, ks, v,
-                          vs, p.parts);
-    return launch_pdl(kv_append_kernel<FMT, DIM, 1>, dim3(p.blocks), dim3(32 * kWarps), 0, stream, a, k, ks, v, vs,
-                      p.parts);
+    const RowPlan p = plan_rows(a, kAppendTokens);
+    auto kern = p.wide ? kv_append_kernel<FMT, DIM, kAppendTokens, kPieces> : kv_append_kernel<FMT, DIM, 1, 1>;
+    return launch_pdl(kern, dim3(p.blocks), dim3(32 * kWarps), 0, stream, a, k, ks, v, vs, p.parts);
 }
 
 template <int FMT, int DIM>
 cudaError_t read_dim(const KvArgs& a, void* k, void* v, int f32, cudaStream_t stream)
 {
-    const RowPlan p = plan_rows(a);
-    if (p.u == 4)
-        return launch_pdl(kv_read_kernel<FMT, DIM, 4>, dim3(p.blocks), dim3(32 * kWarps), 0, stream, a, k, v, f32,
-                          p.parts);
-    return launch_pdl(kv_read_kernel<FMT, DIM, 1>, dim3(p.blocks), dim3(32 * kWarps), 0, stream, a, k, v, f32,
-                      p.parts);
+    const RowPlan p = plan_rows(a, kReadTokens);
+    auto kern = p.wide ? kv_read_kernel<FMT, DIM, kReadTokens, kPieces> : kv_read_kernel<FMT, DIM, 1, 1>;
+    return launch_pdl(kern, dim3(p.blocks), dim3(32 * kWarps), 0, stream, a, k, v, f32, p.parts);
 }
 
 // fn(std::integral_constant fmt, std::integral_constant dim)
@@ -400,7 +472,6 @@ cudaError_t by_format(const KvArgs& a, Fn fn)
     return with(Int<QG_KV_NVFP4>{});
 }
 
-// The call's grid may pass 2^31 - 1 blocks only for more than 10^9 rows.
 bool with_status(const KvArgs& in, KvArgs& a)
 {
     a = in;
