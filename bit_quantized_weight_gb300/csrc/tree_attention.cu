@@ -16,6 +16,7 @@
 //     pairs up two keys' bytes with byte permutes before the conversion.
 // Nothing is transposed through shared memory and no lane reads another's copy
 // (block scales apart).
+#include <atomic>
 #include <type_traits>
 
 #include "tree_common.cuh"
@@ -829,7 +830,8 @@ cudaError_t run_mma(TreeArgs t, cudaStream_t stream)
     t.step = P::kStep;
     t.grid = P::kCtas * sm_count(-1);
     auto kern = tree_mma_kernel<FMT, D, RT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kern, P::kSmem, done);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(static_cast<unsigned>(t.grid)), dim3(kMmaThreads), P::kSmem, stream, t);
     if (e != cudaSuccess) return e;

@@ -12,6 +12,8 @@
 // starts at the CTA's start).
 #pragma once
 
+#include <atomic>
+
 #include "kv_common.cuh"
 
 namespace qg {
@@ -187,6 +189,21 @@ __device__ __forceinline__ float kv_value(const KvArgs& a, int kv, int64_t row, 
         s = e4m3x2_to_f16x2(a.scales[kv][row * sb + d / 16]);
     }
     return half_bits_to_f32(hmul2(h, s & 0xFFFFu) & 0xFFFFu);
+}
+
+// Lets a kernel have its dynamic shared memory, once per device (a bit of
+// `done` each; other devices than the first 64 set it every time).
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& done)
+{
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = d < 64 ? 1ull << d : 0;
+    if (done.load() & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
 }
 
 cudaError_t launch_tree_tc(const TreeArgs& t, cudaStream_t stream);

@@ -15,6 +15,7 @@
 // (two "virtual CTAs" with their own ranges of steps).
 // Warps: 0-3 and 4-7 softmax of streams 0 and 1 (a thread per row), 8-9 bring
 // keys, 10-11 values, 12 and 13 issue the two streams' MMAs.
+#include <atomic>
 #include <type_traits>
 
 #include "tcgen05.cuh"
@@ -1121,7 +1122,8 @@ cudaError_t run_tc(TreeArgs t, cudaStream_t stream)
         return cudaFuncGetAttributes(&f, kern) == cudaSuccess && f.numRegs >= kLaunchRegs;
     }();
     if (!fits) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kern, P::kSmem, done);
     if (e != cudaSuccess) return e;
     const int sms = sm_count(-1);
     t.step = kTcKeys;

@@ -350,16 +350,12 @@ def _kv_check(name, dtype, *ts):
 
 
 class _OnDevice:
-    """The device of a call's tensors as the current one: nothing to do when
-    it is already, else it is switched for the call."""
+    """The device of a call's tensors as the current one: switched for the
+    call where it is not already."""
 
-    def __init__(self, like, *others):
+    def __init__(self, index):
         import torch
-        self.index = like.get_device()
-        for t in others:
-            if t is not None and t.get_device() != self.index:
-                raise ValueError("a call's tensors must be on one device")
-        self.guard = None if self.index == torch.cuda.current_device() else torch.cuda.device(self.index)
+        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
 
     def __enter__(self):
         if self.guard is not None:
@@ -368,6 +364,12 @@ class _OnDevice:
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
+
+
+def _kv_tensors(index, *ts):
+    for t in ts:
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            raise ValueError("a call's tensors must be contiguous CUDA tensors on one device")
 
 
 class KVCache:
@@ -382,7 +384,10 @@ class KVCache:
         import torch
         if fmt not in _KV_FORMATS:
             raise ValueError(f"fmt must be one of {sorted(_KV_FORMATS)}")
-        _cuda(k, v, k_scales, v_scales)
+        self.index = k.get_device()
+        if self.index < 0:
+            raise ValueError("a cache's tensors must be CUDA tensors")
+        _kv_tensors(self.index, k, v, k_scales, v_scales)
         if k.dim() != 4 or v.shape != k.shape:
             raise ValueError("k and v must have one shape [pages][kv_heads][page_size][row]")
         _kv_check("codes", torch.bfloat16 if fmt == "bf16" else torch.uint8, k, v)
@@ -395,7 +400,6 @@ class KVCache:
         _kv_check("scales", torch.uint8, k_scales, v_scales)
         self.fmt, self.head_dim, self.kv_heads, self.page_size = fmt, dim, heads, page
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        _OnDevice(k, v, k_scales, v_scales)
         self.rec = QgKvCache(_KV_FORMATS[fmt], pages, page, heads, dim, _ptr(k), _ptr(v), _ptr(k_scales),
                              _ptr(v_scales), float(k_gscale), float(v_gscale))
         self.ref = ctypes.byref(self.rec)
@@ -426,12 +430,14 @@ class KVBatch:
 
     def __init__(self, page_table, seq_lens, token_start, n_tokens):
         import torch
-        _cuda(page_table, seq_lens, token_start)
+        self.index = page_table.get_device()
+        if self.index < 0:
+            raise ValueError("a batch's tensors must be CUDA tensors")
+        _kv_tensors(self.index, page_table, seq_lens, token_start)
         _kv_check("page_table, seq_lens and token_start", torch.int32, page_table, seq_lens, token_start)
         n = seq_lens.shape[0]
         if page_table.dim() != 2 or page_table.shape[0] != n or tuple(token_start.shape) != (n + 1,):
             raise ValueError("page_table [n][max_pages], seq_lens [n] and token_start [n + 1] must agree")
-        _OnDevice(page_table, seq_lens, token_start)
         self.page_table, self.seq_lens, self.token_start = page_table, seq_lens, token_start
         self.n_seqs, self.n_tokens = n, int(n_tokens)
         self.rec = QgKvBatch(_ptr(page_table), _ptr(seq_lens), _ptr(token_start), n, page_table.shape[1],
@@ -439,25 +445,34 @@ class KVBatch:
         self.ref = ctypes.byref(self.rec)
 
 
-def _token_rows(name, t, batch, heads, dim):
-    """The token stride of a [n_tokens][heads][dim] bf16 tensor whose tokens
-    may lie apart (columns of a fused projection's output)."""
+def _kv_call(cache, batch):
+    if batch.index != cache.index:
+        raise ValueError("cache and batch must be on one device")
+    return cache.index
+
+
+def _token_rows(name, t, index, n, heads, dim):
+    """The token stride of a bf16 tensor [n][heads][dim] whose tokens may lie
+    apart (columns of a fused projection's output)."""
     import torch
-    _kv_check(name, torch.bfloat16, t)
-    if not t.is_cuda or tuple(t.shape) != (batch.n_tokens, heads, dim):
-        raise ValueError(f"{name} must be a CUDA tensor [n_tokens][{heads}][{dim}]")
-    if batch.n_tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+    if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != (n, heads, dim):
+        raise ValueError(f"{name} must be a bfloat16 tensor [{n}][{heads}][{dim}] on the cache's device")
+    if n == 0:
+        return heads * dim
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != dim):
         raise ValueError(f"{name}: each token's heads must be contiguous")
-    return t.stride(0) if batch.n_tokens > 1 else heads * dim
+    return s[0] if n > 1 else heads * dim
 
 
 def kv_cache_append(cache, batch, k, v, stream=None):
     """Quantise rows of k and v (bf16 [n_tokens][kv_heads][head_dim], tokens may
     be strided) into their tokens' positions."""
-    ks = _token_rows("k", k, batch, cache.kv_heads, cache.head_dim)
-    vs = _token_rows("v", v, batch, cache.kv_heads, cache.head_dim)
-    with _OnDevice(cache.k, batch.seq_lens, k, v):
-        _check("kv_cache_append", lib().kv_cache_append(cache.ref, batch.ref, _ptr(k), ks, _ptr(v), vs,
+    dev = _kv_call(cache, batch)
+    ks = _token_rows("k", k, dev, batch.n_tokens, cache.kv_heads, cache.head_dim)
+    vs = _token_rows("v", v, dev, batch.n_tokens, cache.kv_heads, cache.head_dim)
+    with _OnDevice(dev):
+        _check("kv_cache_append", lib().kv_cache_append(cache.ref, batch.ref, k.data_ptr(), ks, v.data_ptr(), vs,
                                                         _stream(stream, cache.k)))
 
 
@@ -465,15 +480,16 @@ def kv_cache_read(cache, batch, k_out, v_out, stream=None):
     """The stored values of the batch's tokens into k_out and v_out
     [n_tokens][kv_heads][head_dim] (both bf16 or both fp32)."""
     import torch
-    _cuda(k_out, v_out)
+    dev = _kv_call(cache, batch)
+    _kv_tensors(dev, k_out, v_out)
     want = (batch.n_tokens, cache.kv_heads, cache.head_dim)
-    if tuple(k_out.shape) != want or tuple(v_out.shape) != want:
+    if k_out.shape != want or v_out.shape != want:
         raise ValueError(f"k_out and v_out must have shape {want}")
     if k_out.dtype not in (torch.bfloat16, torch.float32) or v_out.dtype != k_out.dtype:
         raise ValueError("k_out and v_out must both be bfloat16 or both float32")
     out = QG_OUT_F32 if k_out.dtype == torch.float32 else QG_OUT_BF16
-    with _OnDevice(cache.k, batch.seq_lens, k_out, v_out):
-        _check("kv_cache_read", lib().kv_cache_read(cache.ref, batch.ref, _ptr(k_out), _ptr(v_out), out,
+    with _OnDevice(dev):
+        _check("kv_cache_read", lib().kv_cache_read(cache.ref, batch.ref, k_out.data_ptr(), v_out.data_ptr(), out,
                                                     _stream(stream, cache.k)))
     return k_out, v_out
 
@@ -483,20 +499,22 @@ def kv_cache_accept(cache, batch, path, n_accept, new_lens=None, stream=None):
     (path int32 [n_tokens], n_accept int32 [n]); new_lens int32 [n] receives
     the sequences' new lengths and may be the batch's seq_lens."""
     import torch
-    _cuda(path, n_accept, new_lens)
+    dev = _kv_call(cache, batch)
+    _kv_tensors(dev, path, n_accept, new_lens)
     _kv_check("path, n_accept and new_lens", torch.int32, path, n_accept, new_lens)
-    if tuple(path.shape) != (batch.n_tokens,) or tuple(n_accept.shape) != (batch.n_seqs,) or (
-            new_lens is not None and tuple(new_lens.shape) != (batch.n_seqs,)):
+    if path.shape != (batch.n_tokens,) or n_accept.shape != (batch.n_seqs,) or (
+            new_lens is not None and new_lens.shape != (batch.n_seqs,)):
         raise ValueError("path [n_tokens], n_accept [n_seqs] and new_lens [n_seqs] must agree with the batch")
-    with _OnDevice(cache.k, batch.seq_lens, path, n_accept, new_lens):
+    with _OnDevice(dev):
         _check("kv_cache_accept", lib().kv_cache_accept(cache.ref, batch.ref, _ptr(path), _ptr(n_accept),
                                                         _ptr(new_lens), _stream(stream, cache.k)))
     return new_lens
 
 
 def tree_attention_workspace_size(cache, q_heads, max_tree) -> int:
+    """Bytes of tree_attention's workspace for this cache on its device."""
     b = ctypes.c_size_t(0)
-    with _OnDevice(cache.k):
+    with _OnDevice(cache.index):
         _check("tree_attention_workspace_size",
                lib().tree_attention_workspace_size(cache.ref, int(q_heads), int(max_tree), ctypes.byref(b)))
     return b.value
@@ -507,26 +525,26 @@ def tree_attention(cache, batch, q, out, max_tree, tree_mask=None, scale=None, l
     cache: q bf16 [n_tokens][q_heads][head_dim] (tokens may be strided), out
     bf16 of that shape, tree_mask int64 [n_tokens] of 64 bits (None: chains),
     lse fp32 [n_tokens][q_heads] or None; scale defaults to 1/sqrt(head_dim).
-    workspace: a uint8 tensor of tree_attention_workspace_size bytes."""
+    workspace: a uint8 tensor of tree_attention_workspace_size bytes, not
+    shared by calls that may overlap on the GPU."""
     import torch
     if q.dim() != 3:
         raise ValueError("q must be [n_tokens][q_heads][head_dim]")
-    heads, dim = q.shape[1], cache.head_dim
-    qs = _token_rows("q", q, batch, heads, dim)
-    _cuda(out, tree_mask, lse, workspace)
-    _kv_check("out", torch.bfloat16, out)
-    _kv_check("tree_mask", torch.int64, tree_mask)
-    _kv_check("lse", torch.float32, lse)
-    if tuple(out.shape) != tuple(q.shape) or (tree_mask is not None and tuple(tree_mask.shape) != (batch.n_tokens,)) \
-            or (lse is not None and tuple(lse.shape) != (batch.n_tokens, heads)):
-        raise ValueError("out, tree_mask and lse must agree with q")
-    if scale is None:
-        scale = dim ** -0.5
+    dev, n, heads, dim = _kv_call(cache, batch), batch.n_tokens, q.shape[1], cache.head_dim
+    qs = _token_rows("q", q, dev, n, heads, dim)
+    _kv_tensors(dev, out, tree_mask, lse, workspace)
+    if out.dtype is not torch.bfloat16 or out.shape != q.shape:
+        raise ValueError("out must be bfloat16 in q's shape")
+    if tree_mask is not None and (tree_mask.dtype is not torch.int64 or tree_mask.shape != (n,)):
+        raise ValueError("tree_mask must be int64 [n_tokens]")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n, heads)):
+        raise ValueError("lse must be float32 [n_tokens][q_heads]")
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _OnDevice(cache.k, batch.seq_lens, q, out, tree_mask, lse, workspace):
+    with _OnDevice(dev):
         _check("tree_attention", lib().tree_attention(
-            cache.ref, batch.ref, _ptr(q), qs, heads, int(max_tree), _ptr(tree_mask), float(scale), _ptr(out),
-            _ptr(lse), _ptr(workspace), nbytes, _stream(stream, cache.k)))
+            cache.ref, batch.ref, q.data_ptr(), qs, heads, int(max_tree), _ptr(tree_mask),
+            dim ** -0.5 if scale is None else float(scale), out.data_ptr(), _ptr(lse), _ptr(workspace), nbytes,
+            _stream(stream, cache.k)))
     return out
 
 
