@@ -118,6 +118,25 @@ def test_many_ragged_sequences(fmt):
     attend(P, 3, U.ancestor_masks(r, counts), tree=4)
 
 
+@pytest.mark.parametrize("group,tree", [(1, 2), (20, 2)])
+def test_as_many_sequences_as_a_call_takes(group, tree):
+    """1,024 sequences, every seventh without tokens of its own."""
+    r = np.random.default_rng(51)
+    lens = [int(v) for v in r.integers(0, 40, 1024)]
+    counts = [0 if b % 7 == 0 else 1 + b % tree for b in range(1024)]
+    P = U.Paged(52, "fp8", 64, 16, 1, lens, counts)
+    attend(P, group, U.ancestor_masks(r, counts), tree=tree)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("group", [2, 20])
+def test_lengths_around_every_tile(fmt, group):
+    """Contexts that end just before, at and after each step and tile of 16, 32, 64, 128 and 256 keys."""
+    lens = [n + d for n in (16, 32, 64, 128, 192, 256, 512) for d in (-3, -2, -1, 0, 1)]
+    P = U.Paged(53, fmt, 64, 16, 1, lens, [2] * len(lens))
+    attend(P, group, U.ancestor_masks(np.random.default_rng(54), P.counts))
+
+
 def test_chain_without_a_mask_and_without_lse():
     P = U.Paged(27, "fp8", 128, 64, 2, [50, 0], [5, 64])
     attend(P, 4, None, with_lse=False)
@@ -160,31 +179,51 @@ def test_nan_and_infinity_in_unseen_places(fmt, group, t, n):
     attend(P, group, masks)
 
 
-def test_nan_reaches_the_rows_that_see_it():
+@pytest.mark.parametrize("fmt", ("bf16", "fp8"))
+@pytest.mark.parametrize("group,n", [(2, 70), (5, 70), (12, 70), (12, 0), (40, 200)])
+def test_nan_reaches_the_rows_that_see_it(fmt, group, n):
     """A draft with a NaN value: rows that see it get NaN there, others do not."""
     t = 5
-    P = U.Paged(32, "bf16", 64, 16, 1, [70], [t])
+    P = U.Paged(32, fmt, 64, 16, 1, [n], [t])
     masks = U.ancestor_masks(np.random.default_rng(33), [t])
     masks[:] = masks & ~np.int64(4)
     masks[3] |= 4
-    pg, off = P.at(0, 72, 1)
-    P.parts[1][0][pg, :, off, 7] = 0x7FC0
-    x = O.round_bf16(np.random.default_rng(34).standard_normal((t, 2, 64)))
+    pg, off = P.at(0, n + 2, 1)
+    P.parts[1][0][pg, :, off, 7] = 0x7FC0 if fmt == "bf16" else 0x7F
+    x = O.round_bf16(np.random.default_rng(34).standard_normal((t, group, 64)))
     cache, batch = P.device(torch, q)
-    out = torch.empty((t, 2, 64), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty((t, group, 64), dtype=torch.bfloat16, device="cuda")
     q.tree_attention(cache, batch, to_dev(O.bf16_bits(x)), out, t, tree_mask=torch.from_numpy(masks).cuda(),
-                     workspace=workspace(cache, 2, t))
+                     workspace=workspace(cache, group, t))
     nan = torch.isnan(out).cpu().numpy()
     want = np.zeros_like(nan)
     want[3, :, 7] = True
     assert np.array_equal(nan, want)
 
 
+def test_an_infinite_value_reaches_the_rows_that_see_it():
+    for group in (2, 12):
+        P = U.Paged(50, "bf16", 128, 16, 1, [33], [3])
+        pg, off = P.at(0, 34, 1)
+        P.parts[1][0][pg, :, off, 100] = 0xFF80                 # -infinity in draft 1
+        masks = np.array([1, 3, 5], np.int64)
+        cache, batch = P.device(torch, q)
+        x = torch.randn((3, group, 128), device="cuda").to(torch.bfloat16)
+        out = torch.empty_like(x)
+        q.tree_attention(cache, batch, x, out, 3, tree_mask=torch.from_numpy(masks).cuda(),
+                         workspace=workspace(cache, group, 3))
+        got = out.float().cpu().numpy()
+        assert (got[1, :, 100] == -np.inf).all()
+        got[1, :, 100] = 0
+        assert np.isfinite(got).all()
+
+
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("group", [2, 4, 12, 40])
 @pytest.mark.parametrize("qstd,scale", [(30.0, None), (0.0, None), (1e-3, 1000.0), (1e18, 1e-18), (1.0, 0.0), (3.0, -0.5)])
-def test_sharp_flat_and_wide_range_scores(fmt, qstd, scale):
+def test_sharp_flat_and_wide_range_scores(fmt, group, qstd, scale):
     P = U.Paged(35, fmt, 128, 64, 1, [700], [6])
-    attend(P, 4, U.ancestor_masks(np.random.default_rng(36), [6]), scale=scale, qstd=qstd)
+    attend(P, group, U.ancestor_masks(np.random.default_rng(36), [6]), scale=scale, qstd=qstd)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -389,6 +428,28 @@ def test_two_streams_with_their_own_workspaces():
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o, ref)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("t", [6, 16])
+def test_bounded_waits_report_a_timeout_and_recover(fmt, t):
+    """The tensor-core kernel's key tiles are never announced: the call ends
+    with QG_ERR_DEVICE_TIMEOUT, and a clean one right after is right."""
+    P = U.Paged(49, fmt, 128, 64, 1, [900], [t])
+    masks = U.ancestor_masks(np.random.default_rng(50), [t])
+    x = O.round_bf16(np.random.default_rng(55).standard_normal((t, 12, 128)))
+    cache, batch = P.device(torch, q)
+    d, out, ws = to_dev(O.bf16_bits(x)), torch.empty((t, 12, 128), dtype=torch.bfloat16, device="cuda"), workspace(cache, 12, t)
+    md = torch.from_numpy(masks).cuda()
+    q.qg_debug_set_wait(20_000_000, True)
+    try:
+        q.tree_attention(cache, batch, d, out, t, tree_mask=md, workspace=ws)
+        assert q.qg_last_device_status() == q.QG_ERR_DEVICE_TIMEOUT
+    finally:
+        q.qg_debug_set_wait(0, False)
+    q.tree_attention(cache, batch, d, out, t, tree_mask=md, workspace=ws)
+    assert q.qg_last_device_status() == q.QG_OK
+    check(P, x, masks, 128 ** -0.5, out, None)
 
 
 def test_refusals():
