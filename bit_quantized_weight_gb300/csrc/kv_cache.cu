@@ -105,31 +105,40 @@ __device__ __forceinline__ float max_nan(float a, float b)
 // The places of T consecutive rows: their pages and positions, page -2 for a
 // row that has none, -1 for one whose page lies outside the cache. A row's
 // sequence is the number of sequences that end at or before it, by ballots over
-// 32 sequences at a time; the T rows share each of the three chained loads
-// (token_start, the sequence, the page table).
+// 32 sequences at a time whose entries the lanes hold; two chained loads in all
+// (the sequences' entries, the page table), shared by the T rows.
 template <int T>
 __device__ __forceinline__ void places(const KvArgs& a, int i0, int lane, int (&page)[T], int (&pos)[T])
 {
-    int b[T] = {};
+    KvSeq s[T];
+    int b[T];
+#pragma unroll
+    for (int x = 0; x < T; ++x) {
+        b[x] = -1;
+        s[x] = KvSeq{0, 0, 0};
+    }
     for (int j = 0; j < a.n_seqs; j += 32) {
-        const int end = j + lane < a.n_seqs ? a.start[j + lane + 1] : 0x7FFFFFFF;
+        const bool on = j + lane < a.n_seqs;
+        const int row0 = on ? a.start[j + lane] : 0, end = on ? a.start[j + lane + 1] : 0x7FFFFFFF;
+        const int len = on ? a.lens[j + lane] : 0;
         bool more = false;
 #pragma unroll
         for (int x = 0; x < T; ++x) {
             const int n = __popc(__ballot_sync(0xffffffffu, end <= i0 + x));
-            if (b[x] == j) b[x] += n;
             more = more || n == 32;
+            const int r0 = __shfl_sync(0xffffffffu, row0, n & 31), e = __shfl_sync(0xffffffffu, end, n & 31);
+            const int l = __shfl_sync(0xffffffffu, len, n & 31);
+            if (b[x] >= 0 || n == 32 || j + n >= a.n_seqs) continue;
+            b[x] = j + n;
+            s[x] = kv_seq_of(a, r0, e, l, a.n_tokens);
         }
         if (!more) break;
     }
-    KvSeq s[T];
-#pragma unroll
-    for (int x = 0; x < T; ++x) s[x] = b[x] < a.n_seqs ? kv_seq(a, b[x], a.n_tokens) : KvSeq{0, 0, 0};
     int entry[T];
 #pragma unroll
     for (int x = 0; x < T; ++x) {
         const int at = i0 + x - s[x].row0;
-        const bool on = at >= 0 && at < s[x].rows;
+        const bool on = b[x] >= 0 && at >= 0 && at < s[x].rows;
         pos[x] = on ? s[x].len + at : -1;
         entry[x] = on ? kv_entry(a, b[x], pos[x]) : 0;
     }
@@ -138,11 +147,13 @@ __device__ __forceinline__ void places(const KvArgs& a, int i0, int lane, int (&
 }
 
 // Every sequence's entries are looked at once per call, so that one that no
-// row finds is recorded too.
-__device__ __forceinline__ void check_all(const KvArgs& a)
+// row finds is recorded too: by a block of its own behind those that have rows,
+// where nothing waits for it.
+__device__ __forceinline__ bool checks_all(const KvArgs& a)
 {
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < a.n_seqs; b += blockDim.x) kv_seq(a, b, a.n_tokens);
+    if (blockIdx.x + 1 != gridDim.x) return false;
+    for (int b = threadIdx.x; b < a.n_seqs; b += blockDim.x) kv_seq(a, b, a.n_tokens);
+    return true;
 }
 
 // ------------------------------------------------------------------ append
@@ -206,7 +217,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const __grid_con
                                                                 const uint16_t* v, int64_t v_stride, int parts)
 {
     pdl_enter();
-    check_all(a);
+    if (checks_all(a)) return;
     const int lane = threadIdx.x & 31;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const int i0 = static_cast<int>(unit / parts) * T;
@@ -295,7 +306,7 @@ template <int FMT, int DIM, int T, int U>
 __global__ void __launch_bounds__(32 * kWarps) kv_read_kernel(const __grid_constant__ KvArgs a, void* k_out, void* v_out, int f32, int parts)
 {
     pdl_enter();
-    check_all(a);
+    if (checks_all(a)) return;
     const int lane = threadIdx.x & 31;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const int i0 = static_cast<int>(unit / parts) * T;
@@ -437,7 +448,7 @@ RowPlan plan_rows(const KvArgs& a, int wide_tokens)
     const int per = 32 * (p.wide ? kPieces : 1), tokens = p.wide ? wide_tokens : 1;
     p.parts = static_cast<int>((lanes + per - 1) / per);
     const int64_t warps = (static_cast<int64_t>(a.n_tokens) + tokens - 1) / tokens * p.parts;
-    p.blocks = static_cast<unsigned>((warps + kWarps - 1) / kWarps);
+    p.blocks = static_cast<unsigned>((warps + kWarps - 1) / kWarps) + 1;
     return p;
 }
 

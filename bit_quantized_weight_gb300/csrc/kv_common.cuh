@@ -34,13 +34,12 @@ struct KvSeq {
     int len;
 };
 
-__device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, int b, int max_rows)
+__device__ __forceinline__ KvSeq kv_seq_of(const KvArgs& a, int row0, int end, int len, int max_rows)
 {
     KvSeq s;
-    s.row0 = a.start[b];
-    const int end = a.start[b + 1];
-    s.len = a.lens[b];
-    s.rows = end - s.row0;
+    s.row0 = row0;
+    s.len = len;
+    s.rows = static_cast<int>(static_cast<unsigned>(end) - static_cast<unsigned>(row0));
     const bool ok = s.row0 >= 0 && end >= s.row0 && end <= a.n_tokens && s.len >= 0 && s.rows <= max_rows &&
                     static_cast<int64_t>(s.len) + s.rows <=
                         min(static_cast<int64_t>(a.max_pages) * a.page_size, static_cast<int64_t>(kKvMaxPositions));
@@ -57,6 +56,11 @@ __device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, int b, int max_rows)
 __device__ __forceinline__ int kv_page_index(const KvArgs& a, int p)
 {
     return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(p) >> 4) * a.page_magic) >> 36);
+}
+
+__device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, int b, int max_rows)
+{
+    return kv_seq_of(a, a.start[b], a.start[b + 1], a.lens[b], max_rows);
 }
 
 // The table's entry for position p of sequence b, which kv_valid then checks:
