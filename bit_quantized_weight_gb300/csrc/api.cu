@@ -9,7 +9,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "qgemv_internal.h"
+#include "kv_internal.h"
 
 namespace qg {
 

@@ -367,7 +367,7 @@ template <typename T>
 __device__ __forceinline__ void move_column(const KvArgs& a, const KvSeq& s, int b, int head, uint8_t* base,
                                             int64_t row_bytes, int col, const int32_t* path, int n)
 {
-    constexpr int kBatch = 8;
+    constexpr int kBatch = 16;
     for (int i0 = 0; i0 < n; i0 += kBatch) {
         T v[kBatch];
 #pragma unroll

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "kv_internal.h"
 
 namespace qg {
 

@@ -17,9 +17,6 @@ constexpr int kChunkK = 256;                          // k per pipeline stage
 constexpr int kMaxTokens = 8;                         // MMA n dimension
 constexpr int kMaxRowsPerCta = 256;                   // TMA box limit
 constexpr int kMaxStages = 32;
-constexpr int kKvMaxSeqs = 1024;                      // sequences of a cache call
-constexpr int kKvMaxTokens = 1 << 24;                 // rows of a cache call
-constexpr int kKvMaxPositions = 1 << 30;              // of a sequence
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;    // 2 s
 
 // Per-stage shared-memory layout (byte offsets inside one stage buffer).
@@ -212,36 +209,5 @@ qg_status launch_chain(const qg_gemv_op* ops, int n_ops, int M, uint32_t* sync, 
 size_t chain_workspace_bytes(const qg_gemv_op* ops, int n_ops, int M);
 qg_status launch_chain_ws(const qg_gemv_op* ops, int n_ops, int M, uint32_t* sync, void* workspace,
                           cudaStream_t stream);
-
-// A paged cache and a call's batch of sequences as the kernels read them
-// (qg_kv_cache and qg_kv_batch after validation).
-struct KvArgs {
-    int fmt;                    // qg_kv_format
-    int num_pages;
-    int page_size;
-    int heads;                  // key/value heads
-    int dim;
-    uint8_t* codes[2];          // keys, values
-    uint8_t* scales[2];
-    float g[2];
-    const int32_t* table;
-    const int32_t* lens;
-    const int32_t* start;
-    int n_seqs;
-    int max_pages;
-    int n_tokens;
-    uint64_t page_magic;        // ceil(2^36 / (page_size / 16)), see kv_page_index
-    int* status;
-};
-
-qg_status launch_kv_append(const KvArgs& a, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
-                           cudaStream_t stream);
-qg_status launch_kv_read(const KvArgs& a, void* k_out, void* v_out, int f32, cudaStream_t stream);
-qg_status launch_kv_accept(const KvArgs& a, const int32_t* path, const int32_t* n_accept, int32_t* new_lens,
-                           cudaStream_t stream);
-size_t tree_attention_workspace_bytes(int head_dim, int group, int max_tree);
-qg_status launch_tree_attention(const KvArgs& a, const uint16_t* q, int64_t q_stride, int q_heads, int max_tree,
-                                const uint64_t* mask, float scale, uint16_t* out, float* lse, void* workspace,
-                                cudaStream_t stream);
 
 }  // namespace qg
