@@ -6,15 +6,29 @@
 // per head already asks for 650 (bf16) to 2,300 TFLOP/s (NVFP4). So the keys
 // and values are brought into shared memory once per CTA as exact f16 (bf16)
 // tiles and multiplied by tcgen05.mma:
-//   S = Q K^T   both operands in shared memory, 128 rows x 128 keys -> TMEM
+//   S = Q K^T   both operands in shared memory, 128 rows x 64 keys -> TMEM
 //   O += P V    P in TMEM (written over S by the softmax warps), V in shared
 //               memory as it is stored (head_dim contiguous: N-major)
-// A CTA runs two streams of row tiles, so that one's softmax overlaps the
-// other's products: either the two halves of a unit of 256 rows over the same
-// tiles of keys, or two units' worth of work of up to 128 rows each
-// (two "virtual CTAs" with their own ranges of steps).
-// Warps: 0-3 and 4-7 softmax of streams 0 and 1 (a thread per row), 8-9 bring
-// keys, 10-11 values, 12 and 13 issue the two streams' MMAs.
+// A CTA (one per SM) runs two streams of row tiles, so that one's softmax
+// overlaps the other's products: either the two halves of a unit of 256 rows
+// over the same tiles of keys, or two ranges of steps with up to 128 rows each
+// (two "virtual CTAs"). Each stream has two buffers of S and one of O: 512
+// columns of TMEM for both at head_dim 128.
+// Warps: 0-3 and 4-7 softmax of streams 0 and 1 (a thread per row); 8-11 convert
+// coded tiles, two of keys and two of values (bf16: 8 and 9 copy keys and
+// values); 12 and 13 issue the streams' MMAs; 14 and 15 start the copies of
+// coded keys and values.
+//
+// Bound: at 256 rows the tensor core, by how fast it is fed: an MMA of 128 x 64 x
+// 16 with both operands in shared memory takes about 85 cycles for 32 of
+// arithmetic, P V 71 for 64, so that a tile of 64 keys takes about 2,060 cycles
+// for both streams where the arithmetic alone is 1,020. Measured on a GB300: 8
+// lanes of up to 16,384 tokens, trees of 64, 32 query and 4 key/value heads of
+// 128, bf16: 141 us (620 TFLOP/s of 1,946 measured); one lane of 260,096 tokens,
+// 16 drafts, 48 heads, FP8: 132 us (770 TFLOP/s). At up to 128 rows the bytes
+// (bf16, 8 x 65,536 tokens, trees of 7: 187 us, 5.7 TB/s) or the conversion (FP8,
+// NVFP4: 8 x 16,384 tokens, trees of 7: 81 and 72 us). S for 128 keys at a time
+// halves the tensor core's work on S, but waits for both halves of P: no faster.
 #include <atomic>
 #include <type_traits>
 
