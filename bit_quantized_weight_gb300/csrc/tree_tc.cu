@@ -1145,10 +1145,12 @@ cudaError_t run_tc(TreeArgs t, cudaStream_t stream)
     t.run = 16;
     while (t.run < kTcKeys && t.a.page_size % (2 * t.run) == 0) t.run *= 2;
     CUtensorMap maps[2] = {};
+    const uint64_t rows = static_cast<uint64_t>(t.a.num_pages) * t.a.heads * t.a.page_size;
     if (FMT == QG_KV_BF16)
         for (int kv = 0; kv < 2; ++kv)
-            if (!encode_tmap_2d(&maps[kv], t.a.codes[kv], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D,
-                                static_cast<uint64_t>(t.a.num_pages) * t.a.heads * t.a.page_size, 64, t.run, true))
+            if (rows > 0x7FFFFFFFu ||                // a coordinate has 31 bits; 2^31 rows would be 256 GB or more
+                !encode_tmap_2d(&maps[kv], t.a.codes[kv], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, rows, 64, t.run,
+                                true))
                 return cudaErrorInvalidValue;
     e = launch_pdl(kern, dim3(static_cast<unsigned>(sms)), dim3(kTcThreads), P::kSmem, stream, t, maps[0], maps[1]);
     if (e != cudaSuccess) return e;

@@ -151,6 +151,7 @@ def test_read_is_the_stored_values(fmt, dim, heads, page, lens, counts):
     (64, 1, 16, [5, 0, 31, 9], [3, 17, 1, 4], [0, 17, 1, 2]),
     (256, 3, 48, [47, 48, 0], [64, 1, 64], [33, 1, 64]),
     (128, 8, 16, [3] * 33, [5] * 33, [2] * 33),
+    (64, 2, 32, [11, 0], [300, 70], [150, 70]),
 ])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_accept_moves_the_path(fmt, dim, heads, page, lens, counts, kept, in_place):

@@ -129,6 +129,18 @@ def test_as_many_sequences_as_a_call_takes(group, tree):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dim,group,tree,lens,counts", [
+    (128, 12, 64, [300, 0, 65, 700, 1], [1, 3, 20, 0, 64]),   # a plan for 768 rows, units of 12 to 768
+    (64, 8, 33, [1000, 200], [1, 17]),                        # 264 rows planned, 8 and 136 there
+    (128, 16, 8, [64, 63, 1], [1, 8, 2]),
+    (128, 4, 8, [500, 9], [1, 2]),                            # 32 rows planned
+])
+def test_a_larger_max_tree_than_there_are_tokens(fmt, dim, group, tree, lens, counts):
+    P = U.Paged(56, fmt, dim, 32, 2, lens, counts)
+    attend(P, group, U.ancestor_masks(np.random.default_rng(57), counts), tree=tree)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("group", [2, 20])
 def test_lengths_around_every_tile(fmt, group):
     """Contexts that end just before, at and after each step and tile of 16, 32, 64, 128 and 256 keys."""
