@@ -735,12 +735,14 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
 }
 
 // ------------------------------------------------------------------ join
-// One block per (token, query head) whose unit was read in several parts: its
-// warps take every fourth part, then join. Bound by two chained loads (the
-// batch's entries, before the wait; then the parts with their maxima and sums).
+// The rows (token, query head) whose unit was read in several parts. Bound by
+// two chained loads (the batch's entries, before the wait; then the parts with
+// their maxima and sums). W warps share a row, taking every W-th part: four for
+// a decode step, whose few rows have many parts, one where there are rows enough
+// to fill the GPU (16,384 rows of four parts: 36 us with four warps each).
 constexpr int kJoinWarps = 4;
 
-template <int D>
+template <int D, int W>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid_constant__ TreeArgs t)
 {
     constexpr int kPer = D / 32;
@@ -748,7 +750,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
     __shared__ float part[kJoinWarps][D];
     __shared__ float2 part_ml[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i = blockIdx.x / t.q_heads, h = blockIdx.x % t.q_heads;
+    const int64_t row_at = static_cast<int64_t>(blockIdx.x) * (kJoinWarps / W) + warp / W;
+    const int i = static_cast<int>(row_at / t.q_heads), h = static_cast<int>(row_at % t.q_heads);
     TreeScan scan;
     scan.run(t);
     int64_t base, c0 = 0, c1 = 0;
@@ -766,12 +769,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (c0 == c1) return;                            // written whole, or nobody's row
     float m = -INFINITY, l = 0.f, acc[kPer] = {};
-    for (int64_t y0 = c0 + warp; y0 <= c1; y0 += kAhead * kJoinWarps) {
+    for (int64_t y0 = c0 + warp % W; y0 <= c1; y0 += kAhead * W) {
         float2 ml[kAhead];
         float v[kAhead][kPer];
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) {
-            const int64_t y = y0 + x * kJoinWarps;
+            const int64_t y = y0 + x * W;
             ml[x] = make_float2(-INFINITY, 0.f);
 #pragma unroll
             for (int z = 0; z < kPer; ++z) v[x][z] = 0.f;
@@ -805,32 +808,40 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
             for (int z = 0; z < kPer; ++z) acc[z] = acc[z] * f + v[x][z] * g;
         }
     }
-#pragma unroll
-    for (int z = 0; z < kPer; ++z) part[warp][lane * kPer + z] = acc[z];
-    if (lane == 0) part_ml[warp] = make_float2(m, l);
-    __syncthreads();
-    m = -INFINITY;
-    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, part_ml[w].x);
-    l = 0.f;
-    float f[kJoinWarps];
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        f[w] = part_ml[w].x == -INFINITY ? 0.f : ex2(part_ml[w].x - m);
-        l += f[w] * part_ml[w].y;
-    }
-    const float scale = tree_inverse(l) * t.a.g[1];
     const int64_t to = static_cast<int64_t>(i) * t.q_heads + h;
-    for (int d = 2 * threadIdx.x; d < D; d += 64 * kJoinWarps) {
-        float x0 = 0.f, x1 = 0.f;
+    if constexpr (W == 1) {
+        const float scale = tree_inverse(l) * t.a.g[1];
+        uint32_t* out = reinterpret_cast<uint32_t*>(t.out + to * D) + lane * (kPer / 2);
+#pragma unroll
+        for (int z = 0; z < kPer / 2; ++z) out[z] = pack16<true>(acc[2 * z] * scale, acc[2 * z + 1] * scale);
+        if (t.lse && lane == 0) t.lse[to] = tree_lse(m, l);
+    } else {
+#pragma unroll
+        for (int z = 0; z < kPer; ++z) part[warp][lane * kPer + z] = acc[z];
+        if (lane == 0) part_ml[warp] = make_float2(m, l);
+        __syncthreads();
+        m = -INFINITY;
+        for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, part_ml[w].x);
+        l = 0.f;
+        float f[kJoinWarps];
 #pragma unroll
         for (int w = 0; w < kJoinWarps; ++w) {
-            if (f[w] == 0.f) continue;               // also a warp without parts
-            x0 += f[w] * part[w][d];
-            x1 += f[w] * part[w][d + 1];
+            f[w] = part_ml[w].x == -INFINITY ? 0.f : ex2(part_ml[w].x - m);
+            l += f[w] * part_ml[w].y;
         }
-        *reinterpret_cast<uint32_t*>(t.out + to * D + d) = pack16<true>(x0 * scale, x1 * scale);
+        const float scale = tree_inverse(l) * t.a.g[1];
+        for (int d = 2 * threadIdx.x; d < D; d += 64 * kJoinWarps) {
+            float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) {
+                if (f[w] == 0.f) continue;               // also a warp without parts
+                x0 += f[w] * part[w][d];
+                x1 += f[w] * part[w][d + 1];
+            }
+            *reinterpret_cast<uint32_t*>(t.out + to * D + d) = pack16<true>(x0 * scale, x1 * scale);
+        }
+        if (t.lse && threadIdx.x == 0) t.lse[to] = tree_lse(m, l);
     }
-    if (t.lse && threadIdx.x == 0) t.lse[to] = tree_lse(m, l);
 }
 
 // ------------------------------------------------------------------ plans
@@ -896,10 +907,14 @@ TreePlan plan_tree(int head_dim, int group, int max_tree)
 
 cudaError_t launch_tree_join(const TreeArgs& t, cudaStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>(t.a.n_tokens * t.q_heads)), block(32 * kJoinWarps);
-    if (t.a.dim == 64) return launch_pdl(tree_join_kernel<64>, grid, block, 0, stream, t);
-    if (t.a.dim == 128) return launch_pdl(tree_join_kernel<128>, grid, block, 0, stream, t);
-    return launch_pdl(tree_join_kernel<256>, grid, block, 0, stream, t);
+    const int64_t rows = static_cast<int64_t>(t.a.n_tokens) * t.q_heads;
+    const bool many = rows >= 64LL * sm_count(-1);   // four rows to each of 16 blocks per SM
+    const dim3 grid(static_cast<unsigned>(many ? (rows + kJoinWarps - 1) / kJoinWarps : rows)), block(32 * kJoinWarps);
+    auto run = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        return launch_pdl(many ? tree_join_kernel<D, 1> : tree_join_kernel<D, kJoinWarps>, grid, block, 0, stream, t);
+    };
+    return t.a.dim == 64 ? run(Int<64>{}) : t.a.dim == 128 ? run(Int<128>{}) : run(Int<256>{});
 }
 
 size_t tree_attention_workspace_bytes(int head_dim, int group, int max_tree)
