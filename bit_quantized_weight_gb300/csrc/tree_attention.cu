@@ -908,7 +908,7 @@ TreePlan plan_tree(int head_dim, int group, int max_tree)
 cudaError_t launch_tree_join(const TreeArgs& t, cudaStream_t stream)
 {
     const int64_t rows = static_cast<int64_t>(t.a.n_tokens) * t.q_heads;
-    const bool many = rows >= 64LL * sm_count(-1);   // four rows to each of 16 blocks per SM
+    const bool many = rows >= 16LL * sm_count(-1);
     const dim3 grid(static_cast<unsigned>(many ? (rows + kJoinWarps - 1) / kJoinWarps : rows)), block(32 * kJoinWarps);
     auto run = [&](auto d) {
         constexpr int D = decltype(d)::value;

@@ -56,6 +56,7 @@ constexpr int kMaxRaw = 4;                   // tiles of keys, and of values, as
 // summed by a power of two, without rounding.
 constexpr float kTcOffset = 8.f;
 constexpr float kTcLazy = 7.f;
+constexpr int kStagePitch = 20;              // floats per row of 16 columns on their way out: no bank twice
 
 enum Bar : int {
     kKFull = 0,                              // [stage]
@@ -947,6 +948,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
             const bool busy = 32 * (warp & 3) < n_rows;
             const int row = g.row0 + base + (on ? r : 0);
             const int tok = row / t.group, qh = g.head * t.group + row % t.group;
+            // on their way together with the row of Q
+            const uint64_t mask_word = t.mask ? t.mask[g.tok0 + tok] : (2ull << tok) - 1;
+            int p_check = g.first - g.first % a.page_size + lane * a.page_size;
+            const int entry = p_check < g.end ? kv_entry(a, g.b, p_check) : 0;
             // ---- this row of Q, times a power of two that brings its largest value to f16's upper range
             float rowf = 0.f;
             {
@@ -991,10 +996,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
                 rowf = ldexp_exact(fabsf(t.scale) * kLog2e * a.g[0], -pe);
             }
             const uint64_t own = g.n_tok < 64 ? (1ull << g.n_tok) - 1 : ~0ull;
-            const uint64_t mask = (t.mask ? t.mask[g.tok0 + tok] : (2ull << tok) - 1) & own;
-            bool bad = false;                        // a page of these keys lies outside the cache
-            for (int p = g.first - g.first % a.page_size + lane * a.page_size; p < g.end; p += 32 * a.page_size)
-                bad = kv_page(a, g.b, p) < 0 || bad;
+            const uint64_t mask = mask_word & own;
+            bool bad = kv_valid(a, entry) < 0 && p_check < g.end;   // a page of these keys lies outside the cache
+            for (p_check += 32 * a.page_size; p_check < g.end; p_check += 32 * a.page_size)
+                bad = kv_page(a, g.b, p_check) < 0 || bad;
             bad = __any_sync(0xffffffffu, bad);
             fence_proxy_async_smem();
             tc_fence_before();
@@ -1043,48 +1048,56 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
             tc_fence_after();
             if (!busy) continue;
             const int64_t h = static_cast<int64_t>(g.tok0 + tok) * t.q_heads + qh;
+            const bool some = l > 0.f || l != l;     // the row saw a key
             const float scale = g.slot < 0 ? tree_inverse(l) * a.g[1] : 1.f;
             const int64_t at = static_cast<int64_t>(g.slot) * t.rows + base + r;
             const bool fix = g.end > g.len && *odd_flag;
+            // Rows are stored 16 columns at a time through shared memory, where this warp's rows of Q were, so
+            // that a store's lanes write whole runs of a few rows rather than 16 bytes of each.
+            uint8_t* row_out = !on         ? nullptr
+                               : g.slot < 0 ? reinterpret_cast<uint8_t*>(t.out + h * D)
+                                            : reinterpret_cast<uint8_t*>(t.part_o + at * D);
+            float* stage = reinterpret_cast<float*>(smem + P::kQ + s * P::kQTile + (warp & 3) * 4096);
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t v[32];
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t v[16];
                 __syncwarp();
-                tc_ld<32>(to + 32 * c, v);
+                tc_ld<16>(to + 16 * c, v);
                 tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = tc_after_wait(v[i]);
-                if (!on) continue;
-                if (fix) {
+                for (int i = 0; i < 16; ++i) v[i] = tc_after_wait(v[i]);
+                if (fix && on) {
 #pragma unroll 1
-                    for (int i = 0; i < 32; ++i) {
-                        const float x = odd_sum(a, g.b, g.head, g.first, g.end, g.len, mask, 32 * c + i);
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = odd_sum(a, g.b, g.head, g.first, g.end, g.len, mask, 16 * c + i);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             if (e == i) v[e] = __float_as_uint(__uint_as_float(v[e]) + x);
                     }
                 }
-                if (g.slot < 0) {
-                    uint4* dst = reinterpret_cast<uint4*>(t.out + h * D + 32 * c);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t y[4];
+                for (int i = 0; i < 4; ++i) {
+                    float y[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            y[e] = l > 0.f || l != l
-                                       ? pack16<true>(__uint_as_float(v[8 * i + 2 * e]) * scale,
-                                                      __uint_as_float(v[8 * i + 2 * e + 1]) * scale)
-                                       : 0u;
-                        dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
-                } else {
-                    float4* dst = reinterpret_cast<float4*>(t.part_o + at * D + 32 * c);
+                    for (int e = 0; e < 4; ++e) y[e] = some ? __uint_as_float(v[4 * i + e]) * scale : 0.f;
+                    *reinterpret_cast<float4*>(stage + lane * kStagePitch + 4 * i) = make_float4(y[0], y[1], y[2], y[3]);
+                }
+                __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        dst[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                             __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                for (int i = 0; i < 4; ++i) {        // eight rows at a time, four lanes each
+                    const int from = 8 * i + lane / 4;
+                    const float4 y = *reinterpret_cast<const float4*>(stage + from * kStagePitch + lane % 4 * 4);
+                    uint8_t* dst = reinterpret_cast<uint8_t*>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row_out), from));
+                    if (!dst) continue;
+                    if (g.slot < 0)
+                        *reinterpret_cast<uint2*>(dst + c * 32 + lane % 4 * 8) =
+                            make_uint2(pack16<true>(y.x, y.y), pack16<true>(y.z, y.w));
+                    else
+                        *reinterpret_cast<float4*>(dst + c * 64 + lane % 4 * 16) = y;
                 }
             }
+            __syncwarp();                            // before the next row of Q takes the place
             if (on) {
                 if (g.slot >= 0)
                     t.part_ml[at] = make_float2(m - kTcOffset, l);
