@@ -578,10 +578,6 @@ __device__ __forceinline__ void convert(const TreeArgs& t, uint8_t* smem, uint64
                 raw[y] = lds128(src + key * kRow + c * 16);
                 sc[y] = FMT == QG_KV_FP8 ? lds8(at) : lds16(at + 2 * c);
             }
-            if (y0 + kBatch == kN) {                         // the raw stage can be filled again
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[kRawEmpty + x]);
-            }
 #pragma unroll
             for (int y = 0; y < kBatch; ++y) {
                 uint4 out[kChunks];
@@ -592,6 +588,10 @@ __device__ __forceinline__ void convert(const TreeArgs& t, uint8_t* smem, uint64
                     *reinterpret_cast<uint4*>(tile + tile_at<kTcKeys>(key, c * kChunks + i)) = out[i];
             }
         }
+        // The raw stage can be filled again: only now, when every lane has stored what it made of it. (Once the
+        // reads are merely issued is too early: the arrival does not wait for them, the next copy could come first.)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kRawEmpty + x]);
         if (kv == 1 && Runs<false>::special(info)) {
             __syncwarp();
             clear_places<D, false>(tile, info.left, info.drafts, info.groups, odd_flag, lane);

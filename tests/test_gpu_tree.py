@@ -443,6 +443,49 @@ def test_two_streams_with_their_own_workspaces():
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dim,lanes,tokens,group,t", [
+    (128, 1, 65536, 12, 16), (128, 8, 8192, 8, 64), (64, 1, 65536, 12, 16), (128, 1, 65536, 12, 7),
+    (128, 2, 30001, 12, 1), (256, 1, 20000, 4, 4)])
+def test_calls_back_to_back_give_what_they_give_alone(fmt, dim, lanes, tokens, group, t):
+    """Calls that run one right behind the other (their tiles all in the L2
+    cache, the next kernel waiting for the last) against calls that the host
+    waits for."""
+    r = np.random.default_rng(53)
+    heads, page = 4, 64
+    need = (tokens + t + page - 1) // page
+    shape = (lanes * need, heads, page, dim)
+
+    def store(seed):
+        x = torch.from_numpy(np.random.default_rng(seed).integers(0, 256, shape, dtype=np.uint8))
+        if fmt == "bf16":
+            return x.cuda().to(torch.bfloat16).sub_(128).div_(64), None
+        if fmt == "fp8":
+            return (x & 0xBF).cuda(), torch.from_numpy(r.integers(10, 16, shape[:3], dtype=np.uint8)).cuda()
+        codes = x[..., :dim // 2].contiguous()
+        return codes.cuda(), torch.from_numpy(r.integers(0x30, 0x40, shape[:3] + (dim // 16,), dtype=np.uint8)).cuda()
+
+    (k, ks), (v, vs) = store(1), store(2)
+    cache = q.KVCache(fmt, k, v, ks, vs)
+    table = torch.from_numpy(r.permutation(lanes * need).astype(np.int32).reshape(lanes, need)).cuda()
+    batch = q.KVBatch(table, torch.full((lanes,), tokens, dtype=torch.int32, device="cuda"),
+                      torch.arange(0, lanes * t + 1, t, dtype=torch.int32, device="cuda"), lanes * t)
+    xs = [torch.randn((lanes * t, heads * group, dim), device="cuda").to(torch.bfloat16) for _ in range(2)]
+    spaces = [workspace(cache, heads * group, t) for _ in range(2)]
+    outs = [torch.empty_like(xs[i % 2]) for i in range(8)]
+    for i in range(2):
+        q.tree_attention(cache, batch, xs[i], outs[i], t, workspace=spaces[i])
+        torch.cuda.synchronize()
+    assert torch.isfinite(outs[0]).all()
+    for _ in range(4):
+        for i in range(2, 8):
+            q.tree_attention(cache, batch, xs[i % 2], outs[i], t, workspace=spaces[i % 2])
+        torch.cuda.synchronize()
+        for i in range(2, 8):
+            assert torch.equal(outs[i], outs[i % 2]), i
+            outs[i].zero_()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("t", [6, 16])
 def test_bounded_waits_report_a_timeout_and_recover(fmt, t):
     """The tensor-core kernel's key tiles are never announced: the call ends
