@@ -49,7 +49,7 @@ constexpr int kLoadRegs = 104;
 constexpr int kIssueRegs = 120;
 static_assert(2 * kSoftmaxRegs + kLoadRegs + kIssueRegs <= 4 * kLaunchRegs, "more registers than the block has");
 constexpr int kStages = 4;                   // tiles of keys and of values (SHARED; else two per stream)
-constexpr int kMaxRaw = 4;                   // tiles of keys, and of values, as they are stored
+constexpr int kMaxRaw = 3;                   // tiles of keys, and of values, as they are stored: see convert()
 // Weights are 2^(s - m + 8) with m a whole number from the row's largest score
 // (rounded up), replaced only once a score passes it by 7: a weight is at most
 // 2^15, within f16, the largest at least 2^7, and a change of m scales what was
@@ -523,6 +523,12 @@ __device__ __forceinline__ void copy_coded(const TreeArgs& t, const Cursor* from
 // tiles. The two meet in a stage by turns, and a stage's parity alone would let
 // a warp pass that comes too early (while the tile one round before its own has
 // not landed): it looks at the tile's number too, and then at the parity again.
+// Of the tiles before the one that a warp converts, all but the last are in
+// place then: its own last one, and those whose raw stages were filled anew. So
+// no tile before it can still wait for the same stage of the ring (the last has
+// another), and the parity it waits for there is that of its own phase. That
+// holds for up to three raw stages: with four, and one stream at its end, a warp
+// could find its tile while the other still waits for that stage.
 template <int FMT, int D>
 __device__ __forceinline__ void convert(const TreeArgs& t, uint8_t* smem, uint64_t* bar, const RawInfo* infos,
                                         volatile int* odd_flag, int w)
