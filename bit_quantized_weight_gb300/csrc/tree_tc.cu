@@ -770,9 +770,12 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_
 
 // One warp per stream issues its products: S of a tile into one of two
 // buffers, and O += P V once the weights have taken its place; S runs two tiles
-// ahead of P V, so that scores are ready when the softmax warps want them. (The
-// tensor core takes one thread's products in order: S of a tile overwrites
-// weights that the P V two tiles before it, issued before, has read.) The whole
+// ahead of P V, so that scores are ready when the softmax warps want them. S of a
+// tile overwrites the weights that the P V two tiles before reads, and waits for
+// its end: products with different accumulators are not promised to run in the
+// order in which they were issued. (Without the wait nothing was ever seen to go
+// wrong; it costs 133 -> 141 us over 260,096 keys in FP8 with 16 drafts, 156 ->
+// 162 us for 8 x 16,384 with trees of 64, and 1 us in most others.) The whole
 // warp walks the tiles, so that what addresses them stays in uniform registers;
 // one lane issues.
 template <int FMT, int D, bool SHARED>
@@ -803,8 +806,8 @@ __device__ __forceinline__ bool multiply(const TreeArgs& t, const Cursor* from, 
             tc_mma_f16_ts(to, tp, d, id_o, keep);
 #pragma unroll
             for (int i = 1; i < kTcKeys / 16; ++i) tc_mma_f16_ts(to, tp + 8 * i, d + i * (2048 >> 4), id_o, true);
-            tc_commit(&bar[kVEmpty + st.at]);
             tc_commit(&bar[kPvDone + 2 * s + buf]);
+            tc_commit(&bar[kVEmpty + st.at]);
         }
         __syncwarp();
         ++y;
@@ -830,8 +833,10 @@ __device__ __forceinline__ bool multiply(const TreeArgs& t, const Cursor* from, 
             continue;
         }
         if (j == 0 && !wait(kQFull + s, nq++ & 1u)) return false;
-        tc_fence_after();
         const uint32_t buf = x & 1u;
+        // these scores take the place of weights that P V of two tiles before reads
+        if (x >= 2 && !wait(kPvDone + 2 * s + buf, (x / 2 - 1) & 1u)) return false;
+        tc_fence_after();
         if (leader) {
             const uint64_t d = dk + st.at * (P::kTile >> 4);
             mma_ss<false>(ts + 64 * buf, dq, d, id_s);
