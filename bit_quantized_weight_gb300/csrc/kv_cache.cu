@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const __grid_con
             if (x < 2 * per_side && i0 + y < a.n_tokens) {
                 const int64_t i = i0 + y;
                 const uint16_t* src = x < per_side ? k + i * k_stride + x * 8 : v + i * v_stride + (x - per_side) * 8;
-                raw[y][u] = ldg_nc_128(src);
+                raw[y][u] = ldg_cg_128(src);
             }
         }
     int page[T], pos[T];
@@ -260,7 +260,9 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------ read
-// One lane's eight values as they are stored. All zeros read as zeros.
+// One lane's eight values as they are stored. All zeros read as zeros. (Plain
+// loads: the kernel before, which may run on while this one starts, may be what
+// wrote them, and the read-only path is for what nothing writes meanwhile.)
 template <int FMT>
 struct Stored {
     uint4 codes;                 // FP8: two words, NVFP4: one
@@ -269,15 +271,15 @@ struct Stored {
     __device__ __forceinline__ void load(const uint8_t* c, const uint8_t* s, int64_t row, int piece, int dim)
     {
         if constexpr (FMT == QG_KV_BF16) {
-            codes = ldg_nc_128(c + row * (2 * dim) + piece * 16);
+            codes = ldg_cg_128(c + row * (2 * dim) + piece * 16);
         } else if constexpr (FMT == QG_KV_FP8) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(c + row * dim + piece * 8));
+            const uint2 w = *reinterpret_cast<const uint2*>(c + row * dim + piece * 8);
             codes.x = w.x;
             codes.y = w.y;
-            scale = __ldg(s + row);
+            scale = s[row];
         } else {
-            codes.x = __ldg(reinterpret_cast<const uint32_t*>(c + row * (dim / 2) + piece * 4));
-            scale = __ldg(s + row * (dim / 16) + piece / 2);
+            codes.x = *reinterpret_cast<const uint32_t*>(c + row * (dim / 2) + piece * 4);
+            scale = s[row * (dim / 16) + piece / 2];
         }
     }
 
