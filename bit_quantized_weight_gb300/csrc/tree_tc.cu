@@ -24,10 +24,10 @@
 // arithmetic, P V 71 for 64, so that a tile of 64 keys takes about 2,060 cycles
 // for both streams where the arithmetic alone is 1,020. Measured on a GB300: 8
 // lanes of up to 16,384 tokens, trees of 64, 32 query and 4 key/value heads of
-// 128, bf16: 141 us (620 TFLOP/s of 1,946 measured); one lane of 260,096 tokens,
-// 16 drafts, 48 heads, FP8: 132 us (770 TFLOP/s). At up to 128 rows the bytes
-// (bf16, 8 x 65,536 tokens, trees of 7: 187 us, 5.7 TB/s) or the conversion (FP8,
-// NVFP4: 8 x 16,384 tokens, trees of 7: 81 and 72 us). S for 128 keys at a time
+// 128, bf16: 120 us (730 TFLOP/s of 1,946 measured); one lane of 260,096 tokens,
+// 16 drafts, 48 heads, FP8: 140 us (730 TFLOP/s). At up to 128 rows the bytes
+// (bf16, 8 x 65,536 tokens, trees of 7: 188 us, 5.7 TB/s) or the conversion (FP8,
+// NVFP4: 8 x 16,384 tokens, trees of 7: 82 and 73 us). S for 128 keys at a time
 // halves the tensor core's work on S, but waits for both halves of P: no faster.
 #include <atomic>
 #include <type_traits>
