@@ -800,8 +800,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
         }
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) {
-            if (ml[x].x == -INFINITY) continue;      // a part whose row saw nothing
-            const float mn = fmaxf(m, ml[x].x), f = ex2(m - mn), g = ex2(ml[x].x - mn);
+            // A part without a maximum has a factor of 0: its row saw nothing (zeros), or all its scores are NaN,
+            // which raise no maximum, and its NaN sums make the row's NaN.
+            const float mn = fmaxf(m, ml[x].x);
+            const float f = mn == -INFINITY ? 1.f : ex2(m - mn), g = ml[x].x == -INFINITY ? 0.f : ex2(ml[x].x - mn);
             m = mn;
             l = l * f + ml[x].y * g;
 #pragma unroll
@@ -834,7 +836,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
             float x0 = 0.f, x1 = 0.f;
 #pragma unroll
             for (int w = 0; w < kJoinWarps; ++w) {
-                if (f[w] == 0.f) continue;               // also a warp without parts
+                // with a factor of 0 too: a warp without parts holds zeros, and sums that are not finite arrive
                 x0 += f[w] * part[w][d];
                 x1 += f[w] * part[w][d + 1];
             }

@@ -1,0 +1,158 @@
+"""tree_attention (GPU) where inputs are not finite, scores are far beyond the
+exponential's range, or a row sees a single key: against the plain 64-bit form,
+on every route (16, 32, 128 and 256 rows per unit, split over the GPU or not,
+joined by four warps per row or by one)."""
+import numpy as np
+import pytest
+
+import kv_util as U
+import oracle as O
+from checks import check_bf16
+from gpu_util import bits16, to_dev
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+q = pytest.importorskip("bit_quantized_weight_gb300")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.set_device(0)
+    q.qg_debug_set_wait(0, False)
+    yield
+    assert q.qg_last_device_status() == q.QG_OK
+
+
+FMTS = ("bf16", "fp8", "nvfp4")
+
+
+def chains(counts):
+    return np.array([(1 << (i + 1)) - 1 for t in counts for i in range(t)], dtype=np.uint64).view(np.int64)
+
+
+def own_only(counts):
+    return np.array([1 << i for t in counts for i in range(t)], dtype=np.uint64).view(np.int64)
+
+
+def attend(P, x, masks, scale=None, change=None):
+    """(out as 64-bit values, its bits, lse) of queries x [total][Hq][D]; change(batch) edits the device batch."""
+    cache, batch = P.device(torch, q)
+    if change:
+        change(batch)
+    bits = O.bf16_bits(np.where(np.isnan(x), 0.0, x))
+    bits[np.isnan(x)] = 0x7FC0
+    heads, tree = x.shape[1], max(P.counts)
+    out = torch.zeros((P.total, heads, P.dim), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((P.total, heads), device="cuda")
+    ws = torch.empty(q.tree_attention_workspace_size(cache, heads, tree), dtype=torch.uint8, device="cuda")
+    q.tree_attention(cache, batch, to_dev(bits), out, tree, tree_mask=torch.from_numpy(masks).cuda(), scale=scale,
+                     lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    got = bits16(out)
+    return O.bf16_array(got), got, lse.cpu().numpy().astype(np.float64)
+
+
+def seen_by(P, b, masks):
+    n, t, first = P.lens[b], P.counts[b], int(P.start[b])
+    seen = np.ones((t, n + t), bool)
+    for i in range(t):
+        seen[i, n:] = [bool(int(masks[first + i]) >> j & 1) for j in range(t)]
+    return seen
+
+
+def check_rows(P, x, masks, got, lse, ok, scale=None):
+    """The rows ok [total][Hq] against the oracle."""
+    scale = P.dim ** -0.5 if scale is None else scale
+    for b, (n, t) in enumerate(zip(P.lens, P.counts)):
+        rows = slice(int(P.start[b]), int(P.start[b]) + t)
+        if not ok[rows].any():
+            continue
+        with np.errstate(invalid="ignore", over="ignore"):
+            ref, ref_lse, a, ds = U.attention(x[rows], P.stored(0, b, 0, n + t), P.stored(1, b, 0, n + t),
+                                              seen_by(P, b, masks), scale)
+        B, Bl = U.attention_bounds(a, ds, ref_lse, n + t, P.dim, P.fmt)
+        check_bf16(got[rows][ok[rows]], ref[ok[rows]], B[ok[rows]], f"sequence {b}")
+        off = np.abs(lse[rows] - ref_lse)[ok[rows]]
+        assert (off <= Bl[ok[rows]]).all(), np.max(off / Bl[ok[rows]])
+
+
+# (group, tokens per sequence, sequences, heads): 12 and 24 rows per unit, 72, 192, and calls of 2,560 and 2,592 rows
+ROUTES = [(12, 1, 1, 2), (12, 2, 1, 2), (12, 6, 1, 2), (12, 16, 1, 1), (4, 4, 40, 4), (12, 6, 9, 4)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n", [9, 1300])
+@pytest.mark.parametrize("group,t,lanes,heads", ROUTES)
+def test_a_nan_query_gives_nan(fmt, n, group, t, lanes, heads):
+    """A row of q that holds a NaN is NaN in out and lse, whether its keys were
+    read by one CTA or by many; the other rows are as ever."""
+    counts = [t] * lanes
+    P = U.Paged(71, fmt, 64, 64, heads, [n] * lanes, counts)
+    r = np.random.default_rng(72)
+    masks = U.ancestor_masks(r, counts)
+    x = O.round_bf16(r.standard_normal((P.total, group * heads, 64)))
+    bad = np.zeros(x.shape[:2], bool)
+    bad[::2, 1::3] = True
+    x[bad, 17] = np.nan
+    got, bits, lse = attend(P, x, masks)
+    assert np.isnan(got[bad]).all() and np.isnan(lse[bad]).all()
+    assert np.isfinite(got[~bad]).all() and np.isfinite(lse[~bad]).all()
+    few = ~bad
+    few[2 * t:] = False                                          # two sequences by the oracle
+    check_rows(P, np.nan_to_num(x), masks, bits, lse, few)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n", [0, 40, 4096])
+@pytest.mark.parametrize("group,t,lanes,heads", ROUTES)
+def test_a_nan_key_gives_nan_to_the_rows_that_see_it(fmt, n, group, t, lanes, heads):
+    """The key is the only one that its row sees in the last part of the unit
+    (4,096 positions end with a step, and each draft sees itself alone)."""
+    if n * lanes > 100000:
+        n = 1024
+    counts = [t] * lanes
+    P = U.Paged(73, fmt, 64, 64, heads, [n] * lanes, counts)
+    masks = own_only(counts)
+    j = t - 1
+    for b in range(lanes):
+        pg, off = P.at(b, n + j, 1)
+        codes, scales = P.parts[0]
+        if fmt == "nvfp4":
+            scales[pg, :, off] = 0x7F
+        else:
+            codes[pg, :, off, 5] = 0x7FC0 if fmt == "bf16" else 0x7F
+    x = O.round_bf16(np.random.default_rng(74).standard_normal((P.total, group * heads, 64)))
+    got, bits, lse = attend(P, x, masks)
+    bad = np.zeros(x.shape[:2], bool)
+    bad[P.start[1:] - 1] = True
+    assert np.isnan(got[bad]).all() and np.isnan(lse[bad]).all()
+    assert np.isfinite(got[~bad]).all() and np.isfinite(lse[~bad]).all()
+
+
+@pytest.mark.parametrize("fmt", ("bf16", "fp8"))
+@pytest.mark.parametrize("n", [128, 1024])
+@pytest.mark.parametrize("group,t,lanes,heads", ROUTES)
+def test_an_odd_value_arrives_however_small_its_weight(fmt, n, group, t, lanes, heads):
+    """The last draft's value is infinite (FP8: NaN) and its weight is 2^-500 of
+    the row's largest: the output that it belongs to is not finite, the others
+    are. (At 128 positions the draft's part is a warp's only one in the join.)"""
+    counts = [t] * lanes
+    P = U.Paged(75, fmt, 64, 64, heads, [n] * lanes, counts)
+    for b in range(lanes):
+        for p, v in ((5, 4.0), (n + t - 1, -4.0)):
+            codes, scales = U.quantise(np.full((1, heads, 64), v), fmt, 1.0)
+            pg, off = P.at(b, p, 1)
+            P.parts[0][0][pg, :, off] = codes
+            if scales is not None:
+                P.parts[0][1][pg, :, off] = scales
+        P.parts[1][0][pg, :, off, 9] = 0x7F80 if fmt == "bf16" else 0x7F
+    masks = own_only(counts)
+    x = np.full((P.total, group * heads, 64), 6.0)               # scores 192 and -192, times log2(e)
+    got, bits, lse = attend(P, x, masks)
+    last = P.start[1:] - 1
+    assert not np.isfinite(got[last][:, :, 9]).any()
+    got[last, :, 9] = 0.0
+    assert np.isfinite(got).all() and np.isfinite(lse).all()
