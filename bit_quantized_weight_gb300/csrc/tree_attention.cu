@@ -210,16 +210,18 @@ __device__ __forceinline__ void sts8(uint32_t addr, uint32_t v)
 }
 
 // The values of a block with drafts, or with places behind the last key, made
-// harmless where it lies: what is not finite becomes zero (0 times it would
-// reach rows that do not see the draft), and so do scales behind the last key,
-// whose codes are zeros already. True if a draft's value was not finite.
+// harmless where it lies: from key `context` on, what is not finite becomes zero
+// (0 times it would reach rows that do not see the draft), and so do scales
+// behind the last key, whose codes are zeros already. The keys before it are the
+// context's: every row sees them, and what is not finite there reaches them all.
+// True if a draft's value was not finite.
 template <int FMT, int D>
-__device__ __noinline__ bool clean_values(uint32_t values, uint32_t scales, int keys, int lane)
+__device__ __noinline__ bool clean_values(uint32_t values, uint32_t scales, int context, int keys, int lane)
 {
     using L = Lay<FMT, D>;
     bool odd = false;
     if constexpr (FMT == QG_KV_NVFP4) {
-        if (lane < L::kKeys)
+        if (lane < L::kKeys && lane >= min(context, keys))
             for (int i = 0; i < L::kScale; ++i) {
                 const uint32_t at = scales + lane * L::kScale + i;
                 const bool nan = (lds8(at) & 0x7Fu) == 0x7Fu;
@@ -228,7 +230,10 @@ __device__ __noinline__ bool clean_values(uint32_t values, uint32_t scales, int 
             }
     } else {
         for (int i = 0; i < L::kKBytes / 128; ++i) {          // this lane's words of its own pieces
-            const uint32_t at = values + i / (L::kVB / 4) * (32 * L::kVB) + lane * L::kVB + i % (L::kVB / 4) * 4;
+            const int piece = i / (L::kVB / 4), y = piece / L::kVP;
+            const int key = 16 * (y >> 2) + 2 * (lane & 3) + (y & 1) + 8 * (y >> 1 & 1);
+            if (key < context) continue;
+            const uint32_t at = values + piece * (32 * L::kVB) + lane * L::kVB + i % (L::kVB / 4) * 4;
             const uint32_t w = lds32(at);
             const uint32_t e = FMT == QG_KV_BF16 ? __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u)
                                                  : __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
@@ -490,7 +495,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
             const int p0 = k.first + (warp + i * kMmaWarps) * L::kKeys;
             const uint32_t gone = (bad >> (2 * place)) & 3u;
             const bool special = p0 + L::kKeys > k.len || gone;
-            if (special) odd = clean_values<FMT, D>(src + L::kKBytes, v_sc, k.end - p0, lane) || odd;
+            if (special) odd = clean_values<FMT, D>(src + L::kKBytes, v_sc, k.len - p0, k.end - p0, lane) || odd;
 
             // ---- scores
             float s[RT][kNT][4];

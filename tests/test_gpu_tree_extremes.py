@@ -156,3 +156,61 @@ def test_an_odd_value_arrives_however_small_its_weight(fmt, n, group, t, lanes, 
     assert not np.isfinite(got[last][:, :, 9]).any()
     got[last, :, 9] = 0.0
     assert np.isfinite(got).all() and np.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n", [1, 16, 45, 70, 640])
+@pytest.mark.parametrize("back", [1, 2, 15, 33])
+@pytest.mark.parametrize("dim,group,t", [(64, 2, 3), (128, 3, 5), (128, 8, 3), (64, 12, 5), (128, 40, 5), (256, 12, 3)])
+def test_odd_values_of_the_context_reach_every_row(fmt, n, back, dim, group, t):
+    """A value `back` positions before the drafts is NaN (and in bf16 another is
+    infinite): every row sees the context, so every row has it."""
+    if back > n:
+        pytest.skip("no such position")
+    P = U.Paged(76, fmt, dim, 16, 1, [n], [t])
+    pg, off = P.at(0, n - back, 1)
+    codes, scales = P.parts[1]
+    want = np.zeros(dim, bool)
+    if fmt == "nvfp4":
+        scales[pg, :, off, 2] = 0x7F
+        want[32:48] = True
+    else:
+        codes[pg, :, off, 7] = 0x7FC0 if fmt == "bf16" else 0x7F
+        want[7] = True
+    if fmt == "bf16":
+        codes[pg, :, off, 11] = 0xFF80
+    masks = U.ancestor_masks(np.random.default_rng(77), [t])
+    masks[-1] = 0                                                # sees the context alone
+    x = O.round_bf16(np.random.default_rng(78).standard_normal((t, group, dim)))
+    got, _, lse = attend(P, x, masks)
+    assert np.isnan(got[:, :, want]).all()
+    if fmt == "bf16":
+        assert (got[:, :, 11] == -np.inf).all()
+        want[11] = True
+    assert np.isfinite(got[:, :, ~want]).all() and np.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("group", [2, 8, 12, 40])
+def test_an_odd_value_beside_a_page_outside_the_cache(fmt, group):
+    """A page of 16 keys lies outside the cache: its neighbours' NaN still
+    reaches every row, and nothing of the page does."""
+    P = U.Paged(79, fmt, 64, 16, 1, [200], [3])
+    pg, off = P.at(0, 70, 1)                                     # page 4; page 5 shares a block of 32 keys with it
+    codes, scales = P.parts[1]
+    want = np.zeros(64, bool)
+    if fmt == "nvfp4":
+        scales[pg, :, off, 1] = 0x7F
+        want[16:32] = True
+    else:
+        codes[pg, :, off, 20] = 0x7FC0 if fmt == "bf16" else 0x7F
+        want[20] = True
+    x = O.round_bf16(np.random.default_rng(80).standard_normal((3, group, 64)))
+
+    def change(batch):
+        batch.page_table[0, 5] = -1
+
+    got, _, lse = attend(P, x, chains([3]), change=change)
+    assert q.qg_last_device_status() == q.QG_ERR_INVALID_ARG
+    assert np.isnan(got[:, :, want]).all()
+    assert np.isfinite(got[:, :, ~want]).all() and np.isfinite(lse).all()
