@@ -232,11 +232,11 @@ __device__ __noinline__ bool clean_values(uint32_t values, uint32_t scales, int 
         for (int i = 0; i < L::kKBytes / 128; ++i) {          // this lane's words of its own pieces
             const int piece = i / (L::kVB / 4), y = piece / L::kVP;
             const int key = 16 * (y >> 2) + 2 * (lane & 3) + (y & 1) + 8 * (y >> 1 & 1);
-            if (key < context) continue;
             const uint32_t at = values + piece * (32 * L::kVB) + lane * L::kVB + i % (L::kVB / 4) * 4;
             const uint32_t w = lds32(at);
-            const uint32_t e = FMT == QG_KV_BF16 ? __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u)
-                                                 : __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            const uint32_t bad = FMT == QG_KV_BF16 ? __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u)
+                                                   : __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            const uint32_t e = key < context ? 0u : bad;      // (no branch before the load: the loads overlap)
             odd = odd || e;
             if (e) sts32(at, w & ~e);
         }
@@ -805,10 +805,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const __grid
         }
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) {
-            // A part without a maximum has a factor of 0: its row saw nothing (zeros), or all its scores are NaN,
-            // which raise no maximum, and its NaN sums make the row's NaN.
-            const float mn = fmaxf(m, ml[x].x);
-            const float f = mn == -INFINITY ? 1.f : ex2(m - mn), g = ml[x].x == -INFINITY ? 0.f : ex2(ml[x].x - mn);
+            // a part whose row saw nothing (not one whose scores are all NaN: they raise no maximum, and its NaN
+            // sums make the row's NaN)
+            if (ml[x].x == -INFINITY && ml[x].y == 0.f) continue;
+            const float mn = fmaxf(m, ml[x].x), f = ex2(m - mn), g = ex2(ml[x].x - mn);
             m = mn;
             l = l * f + ml[x].y * g;
 #pragma unroll
