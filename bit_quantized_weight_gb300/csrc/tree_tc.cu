@@ -50,12 +50,17 @@ constexpr int kIssueRegs = 120;
 static_assert(2 * kSoftmaxRegs + kLoadRegs + kIssueRegs <= 4 * kLaunchRegs, "more registers than the block has");
 constexpr int kStages = 4;                   // tiles of keys and of values (SHARED; else two per stream)
 constexpr int kMaxRaw = 3;                   // tiles of keys, and of values, as they are stored: see convert()
-// Weights are 2^(s - m + 8) with m a whole number from the row's largest score
-// (rounded up), replaced only once a score passes it by 7: a weight is at most
-// 2^15, within f16, the largest at least 2^7, and a change of m scales what was
-// summed by a power of two, without rounding.
+// Weights are 2^(s - z) with z = m - 8, m the row's largest score rounded up to a
+// whole number, replaced only once a score passes z by 15: a weight is at most
+// 2^15, within f16, the largest at least 2^7, and a change of z scales what was
+// summed by a power of two, without rounding. The exponent takes the product of
+// score and factor unrounded, which is off from the rounded one in m by half a
+// last place: too much from 2^24 on. Rows with a z of 2^23 or more ("far") round
+// every product first, so that the largest is m itself, and take z = m, since
+// m - 8 may round to anything between m - 16 and m there.
 constexpr float kTcOffset = 8.f;
-constexpr float kTcLazy = 7.f;
+constexpr float kTcMost = 15.f;
+constexpr float kTcFar = 8388608.f;
 constexpr int kStagePitch = 20;              // floats per row of 16 columns on their way out: no bank twice
 
 enum Bar : int {
@@ -676,17 +681,49 @@ __device__ __forceinline__ f2 f2_add(f2 a, f2 b)
     return r;
 }
 
+// The weights of a tile for a warp with far rows, 32 keys at a time: their sum.
+// Rare, and out of line: 64 products with a factor in the way of every tile cost up
+// to 8 % (4-bit, 260,096 keys: 131 -> 141 us).
+template <bool BF16>
+__device__ __noinline__ float far_weights(uint32_t ts, float rowf, float z, uint32_t seen0, uint32_t seen1)
+{
+    const bool far = fabsf(z) >= kTcFar;
+    const float first = far ? rowf : 1.f, then = far ? 1.f : rowf;
+    const float zs = z == -INFINITY ? 0.f : -z;
+    float sum = 0.f;
+#pragma unroll 1
+    for (int y = 0; y < 2; ++y) {
+        const uint32_t seen = y ? seen1 : seen0;
+        uint32_t x[32], h[16];
+        tc_ld<32>(ts + 32 * y, x);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float s = __fmul_rn(__uint_as_float(tc_after_wait(x[i + e])), first);
+                w[e] = (seen >> (i + e)) & 1u ? ex2(fmaf(s, then, zs)) : 0.f;
+                sum += w[e];
+            }
+            h[i / 2] = pack16<BF16>(w[0], w[1]);
+        }
+        tc_st_x16(ts + 16 * y, h);
+        tc_wait_st();
+    }
+    return sum;
+}
+
 // One tile's 64 scores of this thread's row to weights, in place: the weights
 // of 32 keys take the columns of 16 scores that were read before. A row whose
-// scores became too large for its m has m raised, and what was summed with the
+// scores became too large for its z has z raised, and what was summed with the
 // old one is scaled: l and the row of O, once the products of the tile before
 // are complete (those before it are: they came ahead of these scores). That is
 // rare, so small rather than fast.
 template <bool BF16, bool SPECIAL, int D>
 __device__ __forceinline__ bool weights(const TreeArgs& t, uint32_t ts, uint32_t to, uint64_t* before, uint32_t parity,
-                                        float rowf, const uint32_t (&seen)[2], float& m, float& l)
+                                        float rowf, const uint32_t (&seen)[2], float& z, float& l, bool& far)
 {
-    const f2 rowf2 = f2_pack(rowf, rowf);
     uint32_t x[64];
     tc_ld<32>(ts, x);
     tc_ld<32>(ts + 32, x + 32);
@@ -707,10 +744,12 @@ __device__ __forceinline__ bool weights(const TreeArgs& t, uint32_t ts, uint32_t
         for (int e = 0; e < 4; ++e)
             mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(x[i + e])), __uint_as_float(x[i + e + 4]));
     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rowf;
-    if (__any_sync(0xffffffffu, top > m + kTcLazy)) {
-        const float mn = fmaxf(m, ceilf(top));
-        const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
-        m = mn;
+    if (__any_sync(0xffffffffu, top - z > kTcMost)) {
+        const float m = ceilf(top);
+        const float zn = fmaxf(z, fabsf(m) < kTcFar ? m - kTcOffset : m);   // fmaxf: z where m is NaN
+        const float f = zn == -INFINITY ? 1.f : ex2(z - zn);
+        z = zn;
+        far = __any_sync(0xffffffffu, fabsf(z) >= kTcFar && fabsf(z) < INFINITY);
         l *= f;
         if (before) {
             if (!warp_wait(before, parity, t)) return false;
@@ -726,8 +765,12 @@ __device__ __forceinline__ bool weights(const TreeArgs& t, uint32_t ts, uint32_t
             }
         }
     }
-    const float z = kTcOffset - (m == -INFINITY ? 0.f : m);
-    const f2 z2 = f2_pack(z, z);
+    if (far) {
+        l += far_weights<BF16>(ts, rowf, z, SPECIAL ? seen[0] : ~0u, SPECIAL ? seen[1] : ~0u);
+        return true;
+    }
+    const float zs = z == -INFINITY ? 0.f : -z;
+    const f2 rowf2 = f2_pack(rowf, rowf), z2 = f2_pack(zs, zs);
     f2 sum[2] = {0, 0};
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
@@ -739,7 +782,7 @@ __device__ __forceinline__ bool weights(const TreeArgs& t, uint32_t ts, uint32_t
                       x0, x1);
             x0 = ex2(x0);
             x1 = ex2(x1);
-            if constexpr (SPECIAL) {         // also where m is still -infinity, or the scale is 0
+            if constexpr (SPECIAL) {         // also where z is still -infinity, or the scale is 0
                 x0 = (seen[y] >> i) & 1u ? x0 : 0.f;
                 x1 = (seen[y] >> (i + 1)) & 1u ? x1 : 0.f;
             }
@@ -1017,7 +1060,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[kQFull + s]);
 
-            float m = -INFINITY, l = 0.f;
+            float z = -INFINITY, l = 0.f;
+            bool far = false;
             for (int j = 0; j < g.tiles; ++j, ++x) {
                 const uint32_t buf = x & 1u;
                 ok = warp_wait(&bar[kSFull + 2 * s + buf], x / 2 & 1u, t);
@@ -1043,9 +1087,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
                                     if (p < g.end && kv_page(a, g.b, p) < 0) seen[c] &= ~(0xFFFFu << (16 * y));
                                 }
                         }
-                        ok = weights<kBf16, true, D>(t, ts + 64 * buf, to, before, parity, rowf, seen, m, l);
+                        ok = weights<kBf16, true, D>(t, ts + 64 * buf, to, before, parity, rowf, seen, z, l, far);
                     } else {
-                        ok = weights<kBf16, false, D>(t, ts + 64 * buf, to, before, parity, rowf, seen, m, l);
+                        ok = weights<kBf16, false, D>(t, ts + 64 * buf, to, before, parity, rowf, seen, z, l, far);
                     }
                     if (!ok) break;
                 }
@@ -1111,9 +1155,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const __grid_con
             __syncwarp();                            // before the next row of Q takes the place
             if (on) {
                 if (g.slot >= 0)
-                    t.part_ml[at] = make_float2(m - kTcOffset, l);
+                    t.part_ml[at] = make_float2(z, l);
                 else if (t.lse)
-                    t.lse[h] = tree_lse(m - kTcOffset, l);
+                    t.lse[h] = tree_lse(z, l);
             }
         }
     } else if (warp < kMmaWarp) {

@@ -214,3 +214,81 @@ def test_an_odd_value_beside_a_page_outside_the_cache(fmt, group):
     assert q.qg_last_device_status() == q.QG_ERR_INVALID_ARG
     assert np.isnan(got[:, :, want]).all()
     assert np.isfinite(got[:, :, ~want]).all() and np.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("size", [1e8, 1e9, 4e9, 1e12, 1e20])
+@pytest.mark.parametrize("group,t,n", [(12, 6, 700), (12, 6, 5000), (40, 6, 700)])
+def test_scores_far_beyond_the_exponentials_range(fmt, size, group, t, n):
+    """Scores of about `size`: neighbours lie so far apart that each row's output
+    is the value of its largest key, unless two are closer than the error of a
+    32-bit score allows to tell (few rows). A score is off by at most
+    ds (D + 10) 2^-22, as in kv_util.attention_bounds, the weight of the largest
+    by half a step of its 16-bit type and 2^-20 for the sum and the exponential."""
+    dim, g = 64, 1.0 if fmt == "bf16" else 4.0
+    P = U.Paged(81, fmt, dim, 64, 1, [n], [t], kg=g, vg=g, std=1e3)
+    r = np.random.default_rng(83)
+    x = O.round_bf16(r.standard_normal((t, group, dim)) * size / 1e3)
+    masks = U.ancestor_masks(r, [t])
+    got, bits, lse = attend(P, x, masks)
+    assert np.isfinite(got).all() and np.isfinite(lse).all()
+    k, v = P.stored(0, 0, 0, n + t)[:, 0], P.stored(1, 0, 0, n + t)[:, 0]
+    seen = seen_by(P, 0, masks)
+    told = 0
+    for i in range(t):
+        keys = np.nonzero(seen[i])[0]
+        for h in range(group):
+            s = k[keys] @ x[i, h] * dim ** -0.5
+            err = (np.abs(k[keys]) @ np.abs(x[i, h])).max() * dim ** -0.5 * (dim + 10) * 2.0 ** -22
+            assert abs(lse[i, h] - s.max()) <= err + 2.0 ** -20 * abs(s.max()) + 20
+            order = np.argsort(s)
+            if s[order[-1]] - s[order[-2]] <= 2 * err + 40:
+                continue
+            told += 1
+            ref = v[keys[order[-1]]]
+            check_bf16(bits[i, h], ref, np.abs(ref) * (2.0 ** (-8 if fmt == "bf16" else -11) + 2.0 ** -20) + 1e-15)
+    assert told > t * group // 2
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("group,t", [(40, 1), (128, 2)])
+def test_a_maximum_that_grows_by_eight_where_scores_are_whole(fmt, group, t):
+    """Base-2 scores B + 8 in the first half of the context and B + 16 behind it,
+    B = 2^24 or a little more, exact in 32 bits but without a bit to spare: the
+    weights of the second half are 2^8 times those of the first, and no sum of a
+    maximum and a small number is exact. Scores are exact here (scale = ln 2 in 32
+    bits makes the factor 1), so only the weights' rounding is left of the bound."""
+    dim, heads, lanes, n = 64, 4, 5, 4000
+    P = U.Paged(84, fmt, dim, 64, heads, [n] * lanes, [t] * lanes)
+    r = np.random.default_rng(85)
+    for b in range(lanes):
+        k = np.zeros((n + t, heads, dim))
+        k[:, :, 0] = 66.0 if fmt == "nvfp4" else 64.0            # 6 times an E4M3 scale
+        k[:, :, 16] = np.where(np.arange(n + t) < n // 2, 4.0, 8.0)[:, None]
+        k[:, :, 17] = 12.0
+        v = r.standard_normal((n + t, heads, dim)) * 100.0
+        v[:, :, 0] = 300.0                                       # FP8: the same scale for every token, and it is 1
+        v = np.clip(v, -300.0, 300.0)
+        pg, off = P.at(b, 0, n + t)
+        for kv, y in ((0, k), (1, O.round_bf16(v))):
+            codes, scales = U.quantise(y, fmt, 1.0)
+            P.parts[kv][0][pg, :, off] = codes
+            if scales is not None:
+                P.parts[kv][1][pg, :, off] = scales
+        assert np.array_equal(P.stored(0, b, 0, n + t), k)
+    x = np.zeros((P.total, heads * group, dim))
+    x[:, :, 0], x[:, :, 16] = 2.0 ** 18, 2.0
+    masks = chains(P.counts)
+    scale = float(np.float32(np.log(2.0)))
+    got, bits, lse = attend(P, x, masks, scale=scale)
+    assert np.isfinite(got).all() and np.isfinite(lse).all()
+    for b in range(lanes):
+        rows = slice(int(P.start[b]), int(P.start[b]) + t)
+        ref, ref_lse, a, _ = U.attention(x[rows, ::group], P.stored(0, b, 0, n + t), P.stored(1, b, 0, n + t),
+                                         seen_by(P, b, masks), scale)
+        B, _ = U.attention_bounds(a, np.zeros(ref_lse.shape), ref_lse, n + t, dim, fmt)
+        # ln 2 is off by 2^-25: 8 of them in a ratio of weights
+        B = B + a[0] * 2.0 ** -20
+        for h in range(group):
+            check_bf16(bits[rows, h::group], ref, B, f"sequence {b}")
+            assert (np.abs(lse[rows, h::group] - ref_lse) <= 2.0 ** -20 * np.abs(ref_lse)).all()
