@@ -37,8 +37,12 @@ namespace {
 
 constexpr int kMmaWarps = 4;
 constexpr int kMmaThreads = 32 * kMmaWarps;
-constexpr float kOffset = 7.f;   // weights are 2^(s - m + 7): f16 keeps 11 bits down to 2^-21 of the largest
-constexpr float kLazy = 8.f;     // ... and a maximum is replaced only once it is passed by 2^8 (2^15 < 65504)
+// Weights are 2^(s - (m - 7)), m the row's largest score at some time: f16 keeps 11
+// bits down to 2^-21 of the largest. m is replaced only once a weight passes 2^15
+// (< 65504). That is asked of s - (m - 7) as the weights have it: from 2^24 on,
+// m - 7 is not exact, and s > m + 8 would let weights of 2^16 pass.
+constexpr float kOffset = 7.f;
+constexpr float kMost = 15.f;
 
 template <int V>
 using Int = std::integral_constant<int, V>;
@@ -559,7 +563,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
                         if constexpr (FMT == QG_KV_FP8)
                             s[rt][j][e] = fmaf(s[rt][j][e] * cf[e & 1], rowf[rt][e >> 1], add[e & 1]);
                         else
-                            s[rt][j][e] *= rowf[rt][e >> 1];
+                            s[rt][j][e] = __fmul_rn(s[rt][j][e], rowf[rt][e >> 1]);   // the score that m is of too
                     }
             }
             if (special) {
@@ -589,7 +593,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaPlan<FMT, D, RT>::kCtas) tree_
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
                     top[rt][e] = x;
-                    raise = raise || x > m[rt][e] + kLazy;
+                    raise = raise || x - (m[rt][e] - kOffset) > kMost;
                 }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll

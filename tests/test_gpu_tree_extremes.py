@@ -218,7 +218,7 @@ def test_an_odd_value_beside_a_page_outside_the_cache(fmt, group):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("size", [1e8, 1e9, 4e9, 1e12, 1e20])
-@pytest.mark.parametrize("group,t,n", [(12, 6, 700), (12, 6, 5000), (40, 6, 700)])
+@pytest.mark.parametrize("group,t,n", [(2, 3, 700), (12, 2, 700), (12, 6, 700), (12, 6, 5000), (40, 6, 700)])
 def test_scores_far_beyond_the_exponentials_range(fmt, size, group, t, n):
     """Scores of about `size`: neighbours lie so far apart that each row's output
     is the value of its largest key, unless two are closer than the error of a
@@ -251,14 +251,16 @@ def test_scores_far_beyond_the_exponentials_range(fmt, size, group, t, n):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("group,t", [(40, 1), (128, 2)])
+@pytest.mark.parametrize("group,t", [(2, 1), (24, 1), (40, 1), (128, 2)])
 def test_a_maximum_that_grows_by_eight_where_scores_are_whole(fmt, group, t):
     """Base-2 scores B + 8 in the first half of the context and B + 16 behind it,
     B = 2^24 or a little more, exact in 32 bits but without a bit to spare: the
     weights of the second half are 2^8 times those of the first, and no sum of a
     maximum and a small number is exact. Scores are exact here (scale = ln 2 in 32
     bits makes the factor 1), so only the weights' rounding is left of the bound."""
-    dim, heads, lanes, n = 64, 4, 5, 4000
+    dim, heads, lanes, n = 64, 4, 8, 6000
+    if group * t > 32:
+        lanes, n = 5, 4000
     P = U.Paged(84, fmt, dim, 64, heads, [n] * lanes, [t] * lanes)
     r = np.random.default_rng(85)
     for b in range(lanes):
