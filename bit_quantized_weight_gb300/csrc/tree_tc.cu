@@ -50,14 +50,17 @@ constexpr int kIssueRegs = 120;
 static_assert(2 * kSoftmaxRegs + kLoadRegs + kIssueRegs <= 4 * kLaunchRegs, "more registers than the block has");
 constexpr int kStages = 4;                   // tiles of keys and of values (SHARED; else two per stream)
 constexpr int kMaxRaw = 3;                   // tiles of keys, and of values, as they are stored: see convert()
-// Weights are 2^(s - z) with z = m - 8, m the row's largest score rounded up to a
-// whole number, replaced only once a score passes z by 15: a weight is at most
-// 2^15, within f16, the largest at least 2^7, and a change of z scales what was
-// summed by a power of two, without rounding. The exponent takes the product of
-// score and factor unrounded, which is off from the rounded one in m by half a
-// last place: too much from 2^24 on. Rows with a z of 2^23 or more ("far") round
-// every product first, so that the largest is m itself, and take z = m, since
-// m - 8 may round to anything between m - 16 and m there.
+// Weights are 2^(s - z) with z = m - 8, replaced only once a score passes z by 15:
+// a weight is at most 2^15, within f16, the largest at least 2^7. m is the row's
+// largest score; for f16 weights rounded up to a whole number, so that a change of
+// z scales what was summed by a power of two, without rounding. Not for bf16 ones:
+// they have 8 bits, so the largest is 2^8 itself there, which they hold exactly (a
+// row with one key gets its value as it is, where 2^-9 of it would show). The sum
+// that divides has the weights before that rounding: lse is made of it. The
+// exponent takes the product of score and factor unrounded, which is off from the
+// rounded one in m by half a last place: too much from 2^24 on. Rows with a z of
+// 2^23 or more ("far") round every product first, so that the largest is m itself,
+// and take z = m, since m - 8 may round to anything between m - 16 and m there.
 constexpr float kTcOffset = 8.f;
 constexpr float kTcMost = 15.f;
 constexpr float kTcFar = 8388608.f;
@@ -745,7 +748,7 @@ __device__ __forceinline__ bool weights(const TreeArgs& t, uint32_t ts, uint32_t
             mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(x[i + e])), __uint_as_float(x[i + e + 4]));
     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rowf;
     if (__any_sync(0xffffffffu, top - z > kTcMost)) {
-        const float m = ceilf(top);
+        const float m = BF16 ? top : ceilf(top);
         const float zn = fmaxf(z, fabsf(m) < kTcFar ? m - kTcOffset : m);   // fmaxf: z where m is NaN
         const float f = zn == -INFINITY ? 1.f : ex2(z - zn);
         z = zn;

@@ -294,3 +294,20 @@ def test_a_maximum_that_grows_by_eight_where_scores_are_whole(fmt, group, t):
         for h in range(group):
             check_bf16(bits[rows, h::group], ref, B, f"sequence {b}")
             assert (np.abs(lse[rows, h::group] - ref_lse) <= 2.0 ** -20 * np.abs(ref_lse)).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dim,group,t", [(64, 2, 5), (128, 1, 1), (128, 4, 7), (64, 40, 2), (128, 12, 6), (128, 12, 20),
+                                         (256, 8, 6)])
+def test_a_row_that_sees_one_key_is_its_value(fmt, dim, group, t):
+    """The one weight and the sum that divides are the same power of two, so the
+    value comes back bit for bit (codes times scales are bf16 numbers here)."""
+    P = U.Paged(86, fmt, dim, 16, 2, [0, 0], [t, t])
+    masks = own_only(P.counts)
+    x = O.round_bf16(np.random.default_rng(87).standard_normal((P.total, 2 * group, dim)))
+    _, bits, _ = attend(P, x, masks)
+    for b in range(2):
+        v = P.stored(1, b, 0, t)
+        assert np.array_equal(O.round_bf16(v), v)
+        rows = slice(int(P.start[b]), int(P.start[b]) + t)
+        assert np.array_equal(O.bf16_array(bits[rows]), np.repeat(v, group, axis=1))
