@@ -63,10 +63,12 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi)
 
 // x / d to nearest, for eight x: with r = 1 / d to nearest and q = x r, one
 // residual x - q d (exact in an fma) corrects q to the nearest quotient
-// (Markstein, IBM J. Res. Dev. 34, 1990). That holds while nothing leaves the
-// normal range: the largest |x|, `top`, and d lie within 2^+-60, and
-// an x so much smaller that its residual is not exact is a zero code whatever
-// its last bit. Else the division itself.
+// (Markstein, IBM J. Res. Dev. 34, 1990). The residual is taken as q d - x and
+// given its sign in the correction: for a zero x that adds a zero of x's sign,
+// so that -0 stays -0. That holds while nothing leaves the normal range: the
+// largest |x|, `top`, and d lie within 2^+-60, and an x so much smaller that its
+// residual is not exact is a zero code whatever its last bit. Else the division
+// itself.
 __device__ __forceinline__ void divide8(float (&x)[8], float d, float top)
 {
     const uint32_t e = __float_as_uint(top) >> 23, ed = __float_as_uint(d) >> 23;
@@ -75,7 +77,7 @@ __device__ __forceinline__ void divide8(float (&x)[8], float d, float top)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float q = x[i] * r;
-            x[i] = fmaf(fmaf(-q, d, x[i]), r, q);
+            x[i] = fmaf(-fmaf(q, d, -x[i]), r, q);
         }
     } else {
 #pragma unroll 1
