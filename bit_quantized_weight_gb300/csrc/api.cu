@@ -612,6 +612,7 @@ qg_status tree_attention(const qg_kv_cache* cache, const qg_kv_batch* batch, con
     s = check_tree(q_heads, a.heads, max_tree, group);
     if (s != QG_OK) return s;
     if (!std::isfinite(scale) || static_cast<int64_t>(a.n_tokens) * q_heads > 0x7FFFFFFF) return QG_ERR_INVALID_ARG;
+    if (!tree_attention_serves(a, group, max_tree)) return QG_ERR_UNSUPPORTED;
     if (empty_batch(a)) return QG_OK;
     if (!q || !out || q_stride < static_cast<int64_t>(q_heads) * a.dim) return QG_ERR_INVALID_ARG;
     if (!aligned16(q) || q_stride % 8 || !aligned16(out) || !aligned16(lse) || !aligned16(tree_mask))

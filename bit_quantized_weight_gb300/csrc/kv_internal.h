@@ -36,6 +36,7 @@ qg_status launch_kv_append(const KvArgs& a, const void* k, int64_t k_stride, con
 qg_status launch_kv_read(const KvArgs& a, void* k_out, void* v_out, int f32, cudaStream_t stream);
 qg_status launch_kv_accept(const KvArgs& a, const int32_t* path, const int32_t* n_accept, int32_t* new_lens,
                            cudaStream_t stream);
+bool tree_attention_serves(const KvArgs& a, int group, int max_tree);
 size_t tree_attention_workspace_bytes(int head_dim, int group, int max_tree);
 qg_status launch_tree_attention(const KvArgs& a, const uint16_t* q, int64_t q_stride, int q_heads, int max_tree,
                                 const uint64_t* mask, float scale, uint16_t* out, float* lse, void* workspace,

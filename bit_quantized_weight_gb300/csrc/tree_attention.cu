@@ -928,6 +928,14 @@ cudaError_t launch_tree_join(const TreeArgs& t, cudaStream_t stream)
     return t.a.dim == 64 ? run(Int<64>{}) : t.a.dim == 128 ? run(Int<128>{}) : run(Int<256>{});
 }
 
+// A TMA coordinate has 31 bits, and the tensor-core kernel copies bf16 rows by one
+// that counts all the cache's rows (2^31 of them are 256 GB or more).
+bool tree_attention_serves(const KvArgs& a, int group, int max_tree)
+{
+    const bool tc = group * max_tree > 32 && a.dim != 256;
+    return !tc || a.fmt != QG_KV_BF16 || static_cast<int64_t>(a.num_pages) * a.heads * a.page_size <= 0x7FFFFFFF;
+}
+
 size_t tree_attention_workspace_bytes(int head_dim, int group, int max_tree)
 {
     const TreePlan p = plan_tree(head_dim, group, max_tree);

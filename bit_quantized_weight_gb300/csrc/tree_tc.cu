@@ -1219,8 +1219,8 @@ cudaError_t run_tc(TreeArgs t, cudaStream_t stream)
     const uint64_t rows = static_cast<uint64_t>(t.a.num_pages) * t.a.heads * t.a.page_size;
     if (FMT == QG_KV_BF16)
         for (int kv = 0; kv < 2; ++kv)
-            if (rows > 0x7FFFFFFFu ||                // a coordinate has 31 bits; 2^31 rows would be 256 GB or more
-                !encode_tmap_2d(&maps[kv], t.a.codes[kv], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, rows, 64, t.run,
+            // (rows fit a coordinate: tree_attention_serves)
+            if (!encode_tmap_2d(&maps[kv], t.a.codes[kv], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, rows, 64, t.run,
                                 true))
                 return cudaErrorInvalidValue;
     e = launch_pdl(kern, dim3(static_cast<unsigned>(sms)), dim3(kTcThreads), P::kSmem, stream, t, maps[0], maps[1]);

@@ -473,7 +473,10 @@ QG_API qg_status kv_cache_accept(const qg_kv_cache* cache, const qg_kv_batch* ba
  *              n_tokens * q_heads below 2^31
  *   max_tree   1..64, the largest number of tokens of a sequence of this
  *              call; a sequence that has more is left out, with
- *              QG_ERR_INVALID_ARG in the device status word
+ *              QG_ERR_INVALID_ARG in the device status word. A bf16 cache of
+ *              head_dim 64 or 128 with num_pages * kv_heads * page_size of
+ *              2^31 or more is served up to max_tree * q_heads / kv_heads = 32
+ *              (beyond: QG_ERR_UNSUPPORTED)
  *   tree_mask  uint64 [n_tokens], bit j: sees its sequence's token j (its own
  *              bit included: nothing is implied); NULL: token j sees the
  *              tokens 0..j, a chain
