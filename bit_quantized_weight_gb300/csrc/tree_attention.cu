@@ -24,9 +24,11 @@
 // rate) from one context length to the next; before that about 12 us of launch,
 // first loads, join of the warps and join of the parts. Measured on a GB300 (48
 // query, 4 key/value heads of 128, one token per lane): 8 x 16,384 tokens in bf16
-// 64 us, FP8 43, NVFP4 35; 8 x 65,536 FP8 119 us; one lane of 1,000 tokens 8 us
+// 63 us, FP8 42, NVFP4 34; 8 x 65,536 FP8 119 us; one lane of 1,000 tokens 8 us
 // on the device. Three CTAs of four warps per SM at 168 registers; two at 255
-// took 3 % longer.
+// took 3 % longer. A unit of more rows than a tile has its cache read once per
+// tile: at head_dim 256, where every tile has 16 rows, trees of 7 on 12 query heads
+// per key/value head read it 6 times (8 x 16,384 in bf16 301 us, one token 65).
 #include <atomic>
 #include <type_traits>
 
@@ -890,13 +892,15 @@ cudaError_t run_format(const TreeArgs& t, cudaStream_t stream)
 // Rows per unit R, which also says which kernel runs, and the workspace's two
 // parts, for the most CTAs (slots: two per CTA) that a format's kernel takes.
 // Up to 16 rows one row tile of the warp-MMA kernel, up to 32 two; more go to
-// the tensor-core kernel, in one or two tiles of 128, but for head_dim 256,
-// whose accumulators do not fit it. Measured at 24 rows, 8 lanes of 2,048 /
-// 16,384 / 65,536 tokens, warp-MMA against tensor-core kernel (us): FP8 19 / 58 /
-// 163 against 25 / 69 / 209, NVFP4 18 / 49 / 138 against 25 / 59 / 177, bf16 22 /
-// 69 against 27 / 65 (at one token and 65,536 bf16 218 against 174: the lengths
-// that would decide are device data). At 84 rows three passes of 32 over NVFP4
-// took 107 us, the tensor-core kernel takes 64.
+// the tensor-core kernel, in one or two tiles of 128, but for head_dim 256: that
+// kernel runs two streams, whose accumulators (256 columns each) leave no tensor
+// memory for scores; it has no form with one. Measured at 24 rows, 8 lanes of 2,048 /
+// 16,384 / 65,536 tokens, warp-MMA against tensor-core kernel (us): FP8 19 / 57 /
+// 162 against 28 / 73 / 213, NVFP4 18 / 49 / 137 against 28 / 68 / 185, bf16 21 / 68 /
+// 217 against 29 / 67 / 178. So long bf16 contexts lose up to 22 % by the rule: the
+// lengths are device data, and max_pages * page_size, which bounds them, may lie far
+// above them. At 84 rows (8 x 16,384, NVFP4) three passes of 32 took 107 us, the
+// tensor-core kernel takes 74.
 struct TreePlan {
     int rows;
     size_t o_bytes, ml_bytes;

@@ -21,13 +21,13 @@
 //
 // Bound: at 256 rows the tensor core, by how fast it is fed: an MMA of 128 x 64 x
 // 16 with both operands in shared memory takes about 85 cycles for 32 of
-// arithmetic, P V 71 for 64, so that a tile of 64 keys takes about 2,060 cycles
+// arithmetic, P V 71 for 64, so that a tile of 64 keys takes about 2,230 cycles
 // for both streams where the arithmetic alone is 1,020. Measured on a GB300: 8
-// lanes of up to 16,384 tokens, trees of 64, 32 query and 4 key/value heads of
-// 128, bf16: 120 us (730 TFLOP/s of 1,946 measured); one lane of 260,096 tokens,
-// 16 drafts, 48 heads, FP8: 140 us (730 TFLOP/s). At up to 128 rows the bytes
+// lanes of 16,384 tokens, trees of 64, 32 query and 4 key/value heads of 128,
+// bf16: 141 us (975 TFLOP/s of 1,946 measured); one lane of 260,096 tokens, 16
+// drafts, 48 heads, FP8: 139 us (735 TFLOP/s). At up to 128 rows the bytes
 // (bf16, 8 x 65,536 tokens, trees of 7: 188 us, 5.7 TB/s) or the conversion (FP8,
-// NVFP4: 8 x 16,384 tokens, trees of 7: 82 and 73 us). S for 128 keys at a time
+// NVFP4: 8 x 16,384 tokens, trees of 7: 81 and 74 us). S for 128 keys at a time
 // halves the tensor core's work on S, but waits for both halves of P: no faster.
 #include <atomic>
 #include <type_traits>
@@ -820,7 +820,7 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_
 // tile overwrites the weights that the P V two tiles before reads, and waits for
 // its end: products with different accumulators are not promised to run in the
 // order in which they were issued. (Without the wait nothing was ever seen to go
-// wrong; it costs 133 -> 141 us over 260,096 keys in FP8 with 16 drafts, 156 ->
+// wrong; when it came it cost 133 -> 141 us over 260,096 keys in FP8 with 16 drafts, 156 ->
 // 162 us for 8 x 16,384 with trees of 64, and 1 us in most others.) The whole
 // warp walks the tiles, so that what addresses them stays in uniform registers;
 // one lane issues.
