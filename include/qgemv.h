@@ -399,10 +399,10 @@ typedef struct {
  * hold there does not matter. A sequence whose entries do not fit (a negative
  * length, rows outside n_tokens, positions beyond max_pages * page_size or
  * 2^30) is left out, and so is a token whose page lies outside the cache; each
- * records QG_ERR_INVALID_ARG in the device status word. (Where token_start does not ascend, rows that two
- * sequences claim may be left out with the one that does not fit.) Sequences
- * may share pages that a call only reads; a position that a call writes
- * belongs to one sequence.
+ * records QG_ERR_INVALID_ARG in the device status word. (Where token_start does
+ * not ascend, rows that two sequences claim may be left out with the one that
+ * does not fit.) Sequences may share pages that a call only reads; a position
+ * that a call writes belongs to one sequence.
  */
 typedef struct {
     const int32_t* page_table;
@@ -465,8 +465,8 @@ QG_API qg_status kv_cache_accept(const qg_kv_cache* cache, const qg_kv_batch* ba
  *   out[i][h] = bf16_rne( sum_p softmax_p(scale * q[i][h] . K[p][h/G]) V[p][h/G] )
  *   lse[i][h] = ln sum_p exp(scale * q[i][h] . K[p][h/G]),   G = q_heads / kv_heads
  * over the positions p it sees; a token that sees nothing, or whose scores are
- * all -infinity, gets zeros and -infinity. What stands in places that a token does not see never reaches
- * it, infinities and NaN included.
+ * all -infinity, gets zeros and -infinity. What stands in places that a token
+ * does not see never reaches it, infinities and NaN included.
  *   q          bf16, row i at q + i * q_stride: q_heads * head_dim values;
  *              q_stride in elements, a multiple of 8
  *   q_heads    a multiple of kv_heads, at most 128 * kv_heads;
@@ -487,12 +487,12 @@ QG_API qg_status kv_cache_accept(const qg_kv_cache* cache, const qg_kv_batch* ba
  *              bytes, 256-byte aligned; needs no initialisation, is scratch
  *              after the call, and may be shared by calls that do not overlap
  *              on the GPU
- * Products of q and K and of the softmax weights and V accumulate in fp32;
- * the weights enter the second product as f16 (bf16 for QG_KV_BF16), the sum
- * that divides has them before that rounding. Over QG_KV_FP8 and QG_KV_NVFP4 a
- * row of q enters as f16 times a power of two: exact but for values below 2^-31
- * of the row's largest. Keys in a page outside the cache are not seen. The result does not depend on the
- * stream's other work (fixed order, no atomics).
+ * Products of q and K and of the softmax weights and V accumulate in fp32; the
+ * weights enter the second product as f16 (bf16 for QG_KV_BF16), the sum that
+ * divides has them before that rounding. Over QG_KV_FP8 and QG_KV_NVFP4 a row
+ * of q enters as f16 times a power of two: exact but for values below 2^-31 of
+ * the row's largest. Keys in a page outside the cache are not seen. The result
+ * does not depend on the stream's other work (fixed order, no atomics).
  */
 QG_API qg_status tree_attention(const qg_kv_cache* cache, const qg_kv_batch* batch, const void* q, int64_t q_stride,
                                 int q_heads, int max_tree, const uint64_t* tree_mask, float scale, void* out,
