@@ -311,3 +311,30 @@ def test_a_row_that_sees_one_key_is_its_value(fmt, dim, group, t):
         assert np.array_equal(O.round_bf16(v), v)
         rows = slice(int(P.start[b]), int(P.start[b]) + t)
         assert np.array_equal(O.bf16_array(bits[rows]), np.repeat(v, group, axis=1))
+
+
+@pytest.mark.parametrize("n", [9, 1300])
+@pytest.mark.parametrize("left", [0, 1])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group,t,lanes,heads", ROUTES)
+def test_scores_of_minus_infinity(n, left, dim, group, t, lanes, heads):
+    """Keys whose scores are -infinity have no weight: rows that see no others
+    get zeros and -infinity, rows that see one other key get its value."""
+    lanes = min(lanes, 9 if dim == 256 else lanes)
+    P = U.Paged(88, "bf16", dim, 64, heads, [n] * lanes, [t] * lanes)
+    for b in range(lanes):
+        pg, off = P.at(b, 0, n + t)
+        keep = P.parts[0][0][pg[1], :, off[1], 3].copy()
+        P.parts[0][0][pg, :, off, 3] = 0xFF80
+        if left:
+            P.parts[0][0][pg[1], :, off[1], 3] = keep
+    x = O.round_bf16(np.random.default_rng(89).standard_normal((P.total, group * heads, dim)))
+    x[:, :, 3] = 2.0
+    got, _, lse = attend(P, x, chains(P.counts))
+    for b in range(lanes):
+        rows = slice(int(P.start[b]), int(P.start[b]) + t)
+        if not left:
+            assert not got[rows].any() and (lse[rows] == -np.inf).all()
+            continue
+        v = np.repeat(P.stored(1, b, 1, 1), group, axis=1)
+        assert np.array_equal(got[rows], np.repeat(v, t, axis=0)) and np.isfinite(lse[rows]).all()
