@@ -14,4 +14,6 @@ from .qgemv import (  # noqa: F401
     QG_FMT_NVFP4, QG_FMT_Q4, QG_FMT_Q5, QG_EPI_NONE, QG_EPI_RESIDUAL, QG_EPI_SWIGLU,
     KVCache, KVBatch, kv_cache_append, kv_cache_read, kv_cache_accept, tree_attention,
     tree_attention_workspace_size, QgKvCache, QgKvBatch, QG_KV_BF16, QG_KV_FP8, QG_KV_NVFP4,
+    KVPages, KVMoves, kv_pages_fork, kv_pages_reserve, kv_pages_compact, kv_pages_copy, beam_select,
+    beam_select_workspace_size, QgKvPages, QgKvMoves,
 )

@@ -304,10 +304,10 @@ qg_status run_op(const qg_gemv_op& g, int M, cudaStream_t stream)
     return run_op_simple(g, M, stream);
 }
 
-// A cache and a batch of its sequences, checked and packed for the kernels.
-qg_status check_kv(const qg_kv_cache* c, const qg_kv_batch* b, KvArgs& a)
+// A cache, checked and packed for the kernels.
+qg_status check_cache(const qg_kv_cache* c, KvArgs& a)
 {
-    if (!c || !b) return QG_ERR_INVALID_ARG;
+    if (!c) return QG_ERR_INVALID_ARG;
     if (c->format != QG_KV_BF16 && c->format != QG_KV_FP8 && c->format != QG_KV_NVFP4) return QG_ERR_INVALID_ARG;
     if (c->num_pages < 1 || c->kv_heads < 1 || c->kv_heads > 1024 || c->head_dim < 1 || c->page_size < 16 ||
         c->page_size > 1024 || c->page_size % 16)
@@ -319,13 +319,6 @@ qg_status check_kv(const qg_kv_cache* c, const qg_kv_batch* b, KvArgs& a)
     if (scaled && !(std::isfinite(c->k_gscale) && c->k_gscale > 0.f && std::isfinite(c->v_gscale) &&
                     c->v_gscale > 0.f))
         return QG_ERR_INVALID_ARG;
-    if (b->n_seqs < 0 || b->n_seqs > kKvMaxSeqs || b->max_pages < 1 || b->n_tokens < 0 ||
-        b->n_tokens > kKvMaxTokens)
-        return QG_ERR_INVALID_ARG;
-    if (b->n_seqs && (!b->page_table || !b->seq_lens || !b->token_start)) return QG_ERR_INVALID_ARG;
-    const void* ptrs[] = {c->k, c->v, c->k_scales, c->v_scales, b->page_table, b->seq_lens, b->token_start};
-    for (const void* p : ptrs)
-        if (!aligned16(p)) return QG_ERR_MISALIGNED;
     a.fmt = c->format;
     a.num_pages = c->num_pages;
     a.page_size = c->page_size;
@@ -337,15 +330,59 @@ qg_status check_kv(const qg_kv_cache* c, const qg_kv_batch* b, KvArgs& a)
     a.scales[1] = c->v_scales;
     a.g[0] = scaled ? c->k_gscale : 1.f;
     a.g[1] = scaled ? c->v_gscale : 1.f;
+    const uint64_t groups = static_cast<uint64_t>(c->page_size / 16);
+    a.page_magic = ((1ull << 36) + groups - 1) / groups;
+    a.status = nullptr;
+    return QG_OK;
+}
+
+bool cache_aligned(const KvArgs& a)
+{
+    return aligned16(a.codes[0]) && aligned16(a.codes[1]) && aligned16(a.scales[0]) && aligned16(a.scales[1]);
+}
+
+// A cache and a batch of its sequences, checked and packed for the kernels.
+qg_status check_kv(const qg_kv_cache* c, const qg_kv_batch* b, KvArgs& a)
+{
+    if (!b) return QG_ERR_INVALID_ARG;
+    const qg_status s = check_cache(c, a);
+    if (s != QG_OK) return s;
+    if (b->n_seqs < 0 || b->n_seqs > kKvMaxSeqs || b->max_pages < 1 || b->n_tokens < 0 ||
+        b->n_tokens > kKvMaxTokens)
+        return QG_ERR_INVALID_ARG;
+    if (b->n_seqs && (!b->page_table || !b->seq_lens || !b->token_start)) return QG_ERR_INVALID_ARG;
+    if (!cache_aligned(a) || !aligned16(b->page_table) || !aligned16(b->seq_lens) || !aligned16(b->token_start))
+        return QG_ERR_MISALIGNED;
     a.table = b->page_table;
     a.lens = b->seq_lens;
     a.start = b->token_start;
     a.n_seqs = b->n_seqs;
     a.max_pages = b->max_pages;
     a.n_tokens = b->n_tokens;
-    const uint64_t groups = static_cast<uint64_t>(c->page_size / 16);
-    a.page_magic = ((1ull << 36) + groups - 1) / groups;
-    a.status = nullptr;
+    return QG_OK;
+}
+
+// A page record, checked and packed for the kernels.
+qg_status check_pages(const qg_kv_pages* p, PageArgs& a)
+{
+    if (!p) return QG_ERR_INVALID_ARG;
+    if (p->n_seqs < 0 || p->n_seqs > kKvMaxSeqs || p->max_pages < 1 || p->num_pages < 1 || p->page_size < 16 ||
+        p->page_size > 1024 || p->page_size % 16)
+        return QG_ERR_INVALID_ARG;
+    if (p->num_pages > kKvMaxPoolPages) return QG_ERR_UNSUPPORTED;
+    if (!p->refs || (p->n_seqs && (!p->page_table || !p->seq_lens || !p->n_pages))) return QG_ERR_INVALID_ARG;
+    if (!aligned16(p->page_table) || !aligned16(p->seq_lens) || !aligned16(p->n_pages) || !aligned16(p->refs))
+        return QG_ERR_MISALIGNED;
+    a = PageArgs{p->page_table, p->seq_lens, p->n_pages, p->refs, p->n_seqs, p->max_pages, p->num_pages,
+                 p->page_size, nullptr};
+    return QG_OK;
+}
+
+qg_status check_moves(const qg_kv_moves* m, MoveArgs& a)
+{
+    if (!m || !m->list || !m->count || m->capacity < 1 || m->capacity > kKvMaxPoolPages) return QG_ERR_INVALID_ARG;
+    if (!aligned16(m->list) || !aligned16(m->count)) return QG_ERR_MISALIGNED;
+    a = MoveArgs{reinterpret_cast<int4*>(m->list), m->count, m->capacity};
     return QG_OK;
 }
 
@@ -360,6 +397,12 @@ qg_status check_tree(int q_heads, int kv_heads, int max_tree, int& group)
         return QG_ERR_INVALID_ARG;
     group = q_heads / kv_heads;
     return QG_OK;
+}
+
+bool beam_sizes(int lanes, int beams, int vocab, int n_out)
+{
+    return lanes >= 0 && beams >= 1 && beams <= 64 && lanes <= 65536 / beams && vocab >= 1 && vocab <= (1 << 24) &&
+           n_out >= 1 && n_out <= 64;
 }
 
 }  // namespace
@@ -622,6 +665,84 @@ qg_status tree_attention(const qg_kv_cache* cache, const qg_kv_batch* batch, con
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return QG_ERR_MISALIGNED;
     return launch_tree_attention(a, static_cast<const uint16_t*>(q), q_stride, q_heads, max_tree, tree_mask, scale,
                                  static_cast<uint16_t*>(out), lse, workspace, stream);
+}
+
+qg_status kv_pages_fork(const qg_kv_pages* pages, const int32_t* parent, cudaStream_t stream)
+{
+    PageArgs a;
+    const qg_status s = check_pages(pages, a);
+    if (s != QG_OK) return s;
+    if (a.n_seqs == 0) return QG_OK;
+    if (!parent) return QG_ERR_INVALID_ARG;
+    if (!aligned16(parent)) return QG_ERR_MISALIGNED;
+    return launch_pages_fork(a, parent, stream);
+}
+
+qg_status kv_pages_reserve(const qg_kv_pages* pages, const int32_t* n_new, const qg_kv_moves* moves, int32_t* n_free,
+                           cudaStream_t stream)
+{
+    PageArgs a;
+    MoveArgs m;
+    qg_status s = check_pages(pages, a);
+    if (s == QG_OK) s = check_moves(moves, m);
+    if (s != QG_OK) return s;
+    if (m.capacity < a.n_seqs || (a.n_seqs && !n_new)) return QG_ERR_INVALID_ARG;
+    if (!aligned16(n_new) || !aligned16(n_free)) return QG_ERR_MISALIGNED;
+    return launch_pages_reserve(a, n_new, m, n_free, stream);
+}
+
+qg_status kv_pages_compact(const qg_kv_pages* pages, const qg_kv_moves* moves, int32_t* page_map, int32_t* n_live,
+                           cudaStream_t stream)
+{
+    PageArgs a;
+    MoveArgs m;
+    qg_status s = check_pages(pages, a);
+    if (s == QG_OK) s = check_moves(moves, m);
+    if (s != QG_OK) return s;
+    if (!page_map) return QG_ERR_INVALID_ARG;
+    if (!aligned16(page_map) || !aligned16(n_live)) return QG_ERR_MISALIGNED;
+    return launch_pages_compact(a, m, page_map, n_live, stream);
+}
+
+qg_status kv_pages_copy(const qg_kv_cache* cache, const qg_kv_moves* moves, cudaStream_t stream)
+{
+    KvArgs a{};
+    MoveArgs m;
+    qg_status s = check_cache(cache, a);
+    if (s == QG_OK && !cache_aligned(a)) s = QG_ERR_MISALIGNED;
+    if (s == QG_OK) s = check_moves(moves, m);
+    if (s != QG_OK) return s;
+    return launch_pages_copy(a, m, stream);
+}
+
+qg_status beam_select_workspace_size(int lanes, int beams, int vocab, int n_out, size_t* bytes)
+{
+    if (!bytes || !beam_sizes(lanes, beams, vocab, n_out)) return QG_ERR_INVALID_ARG;
+    *bytes = beam_select_workspace_bytes(lanes, beams, vocab, n_out);
+    return QG_OK;
+}
+
+qg_status beam_select(const void* logits, qg_out logits_dtype, int64_t row_stride, int lanes, int beams, int vocab,
+                      const float* scores, const uint8_t* finished, int eos, int pad, int n_out, float* out_scores,
+                      int32_t* out_tokens, int32_t* out_parents, uint8_t* out_finished, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream)
+{
+    if (!beam_sizes(lanes, beams, vocab, n_out) || (logits_dtype != QG_OUT_BF16 && logits_dtype != QG_OUT_F32) ||
+        row_stride < vocab || row_stride > (int64_t{1} << 40) || eos < -1 || eos >= vocab || pad < 0 || pad >= vocab)
+        return QG_ERR_INVALID_ARG;
+    if (lanes == 0) return QG_OK;
+    if (!logits || !scores || !out_scores || !out_tokens || !out_parents) return QG_ERR_INVALID_ARG;
+    const bool in_place = out_scores == scores || (out_finished && out_finished == finished);
+    if (in_place && n_out != beams) return QG_ERR_INVALID_ARG;
+    const void* ptrs[] = {logits, scores, finished, out_scores, out_tokens, out_parents, out_finished};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return QG_ERR_MISALIGNED;
+    if (!workspace || workspace_bytes < beam_select_workspace_bytes(lanes, beams, vocab, n_out))
+        return QG_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return QG_ERR_MISALIGNED;
+    const BeamArgs a{logits, logits_dtype == QG_OUT_F32, row_stride, lanes, beams, vocab, scores, finished, eos, pad,
+                     n_out, out_scores, out_tokens, out_parents, out_finished, nullptr};
+    return launch_beam_select(a, workspace, stream);
 }
 
 qg_status qg_last_device_status(cudaStream_t stream)

@@ -1,5 +1,6 @@
 // kv_internal.h -- types shared by the host launchers and the kernels of the
-// paged cache and the attention over it.
+// paged cache, the attention over it, the pages that sequences share and the
+// selection of beam search.
 #pragma once
 
 #include "qgemv_internal.h"
@@ -30,6 +31,58 @@ struct KvArgs {
     uint64_t page_magic;        // ceil(2^36 / (page_size / 16)), see kv_page_index
     int* status;
 };
+
+constexpr int kKvMaxPoolPages = 1 << 22;              // of a page record
+
+// A page record as the kernels read and change it (qg_kv_pages after
+// validation), and a list of moves.
+struct PageArgs {
+    int32_t* table;
+    int32_t* lens;
+    int32_t* held;
+    int32_t* refs;
+    int n_seqs;
+    int max_pages;
+    int num_pages;
+    int page_size;
+    int* status;
+};
+
+struct MoveArgs {
+    int4* list;
+    int32_t* count;
+    int capacity;
+};
+
+qg_status launch_pages_fork(const PageArgs& a, const int32_t* parent, cudaStream_t stream);
+qg_status launch_pages_reserve(const PageArgs& a, const int32_t* n_new, const MoveArgs& m, int32_t* n_free,
+                               cudaStream_t stream);
+qg_status launch_pages_compact(const PageArgs& a, const MoveArgs& m, int32_t* page_map, int32_t* n_live,
+                               cudaStream_t stream);
+qg_status launch_pages_copy(const KvArgs& a, const MoveArgs& m, cudaStream_t stream);
+
+// Beam search's selection (beam_select after validation).
+struct BeamArgs {
+    const void* logits;
+    int f32;
+    int64_t stride;
+    int lanes;
+    int beams;
+    int vocab;
+    const float* scores;
+    const uint8_t* finished;
+    int eos;
+    int pad;
+    int n_out;
+    float* out_scores;
+    int32_t* out_tokens;
+    int32_t* out_parents;
+    uint8_t* out_finished;
+    int* status;
+};
+
+size_t beam_select_workspace_bytes(int lanes, int beams, int vocab, int n_out);
+qg_status launch_beam_select(const BeamArgs& a, void* workspace, cudaStream_t stream);
 
 qg_status launch_kv_append(const KvArgs& a, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                            cudaStream_t stream);

@@ -62,6 +62,18 @@ class QgKvBatch(ctypes.Structure):
                 ("n_seqs", ctypes.c_int), ("max_pages", ctypes.c_int), ("n_tokens", ctypes.c_int)]
 
 
+class QgKvPages(ctypes.Structure):
+    """qg_kv_pages of include/qgemv.h."""
+    _fields_ = [("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("n_pages", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("n_seqs", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int)]
+
+
+class QgKvMoves(ctypes.Structure):
+    """qg_kv_moves of include/qgemv.h."""
+    _fields_ = [("list", ctypes.c_void_p), ("count", ctypes.c_void_p), ("capacity", ctypes.c_int)]
+
+
 class QGemvError(RuntimeError):
     def __init__(self, name, status):
         super().__init__(f"{name} failed: {qg_status_string(status)} ({status})")
@@ -101,6 +113,13 @@ def lib():
         L.kv_cache_accept.argtypes = [pc, pb, _P, _P, _P, _P]
         L.tree_attention.argtypes = [pc, pb, _P, i64, _I, _I, _P, _F, _P, _P, _P, ctypes.c_size_t, _P]
         L.tree_attention_workspace_size.argtypes = [pc, _I, _I, ctypes.POINTER(ctypes.c_size_t)]
+        pp, pm = ctypes.POINTER(QgKvPages), ctypes.POINTER(QgKvMoves)
+        L.kv_pages_fork.argtypes = [pp, _P, _P]
+        L.kv_pages_reserve.argtypes = [pp, _P, pm, _P, _P]
+        L.kv_pages_compact.argtypes = [pp, pm, _P, _P, _P]
+        L.kv_pages_copy.argtypes = [pc, pm, _P]
+        L.beam_select.argtypes = [_P, _I, i64, _I, _I, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
+        L.beam_select_workspace_size.argtypes = [_I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]
         L.qg_last_device_status.argtypes = [_P]
         L.qg_read_probe.argtypes = [_P, ctypes.c_size_t, _P, _P]
         L.qg_status_string.argtypes = [_I]
@@ -110,7 +129,8 @@ def lib():
                      "moe_qgemv_nvfp4_workspace_size", "moe_qgemv_nvfp4", "moe_qgemv_nvfp4_noalloc",
                      "qgemv_chain", "qgemv_chain_ws", "qgemv_chain_workspace_size", "qgemv_swiglu_q45",
                      "kv_cache_append", "kv_cache_read", "kv_cache_accept", "tree_attention",
-                     "tree_attention_workspace_size", "qdequant_nvfp4",
+                     "tree_attention_workspace_size", "kv_pages_fork", "kv_pages_reserve", "kv_pages_compact",
+                     "kv_pages_copy", "beam_select", "beam_select_workspace_size", "qdequant_nvfp4",
                      "qdequant_q45", "qg_last_device_status", "qg_debug_set_wait"):
             getattr(L, name).restype = _I
         _lib = L
@@ -546,6 +566,162 @@ def tree_attention(cache, batch, q, out, max_tree, tree_mask=None, scale=None, l
             dim ** -0.5 if scale is None else float(scale), out.data_ptr(), _ptr(lse), _ptr(workspace), nbytes,
             _stream(stream, cache.k)))
     return out
+
+
+class KVPages:
+    """The pages that sequences hold and may share (qg_kv_pages), over the
+    caller's int32 tensors: page_table [n][max_pages], seq_lens [n], n_pages
+    [n], refs [num_pages] (0: a free page). The calls change them in place;
+    they must stay in place while the record is used. page_table and seq_lens
+    are a KVBatch's too. KVPages.empty allocates them, with no page held."""
+
+    def __init__(self, page_table, seq_lens, n_pages, refs, page_size):
+        import torch
+        self.index = page_table.get_device()
+        if self.index < 0:
+            raise ValueError("a page record's tensors must be CUDA tensors")
+        _kv_tensors(self.index, page_table, seq_lens, n_pages, refs)
+        _kv_check("page_table, seq_lens, n_pages and refs", torch.int32, page_table, seq_lens, n_pages, refs)
+        if seq_lens.dim() != 1 or refs.dim() != 1 or page_table.dim() != 2 or (
+                page_table.shape[0] != seq_lens.shape[0] or n_pages.shape != seq_lens.shape):
+            raise ValueError("page_table [n][max_pages], seq_lens [n], n_pages [n] and refs [num_pages] must agree")
+        self.page_table, self.seq_lens, self.n_pages, self.refs = page_table, seq_lens, n_pages, refs
+        self.n_seqs, self.num_pages, self.page_size = seq_lens.shape[0], refs.shape[0], int(page_size)
+        self.rec = QgKvPages(_ptr(page_table), _ptr(seq_lens), _ptr(n_pages), _ptr(refs), self.n_seqs,
+                             page_table.shape[1], self.num_pages, self.page_size)
+        self.ref = ctypes.byref(self.rec)
+
+    @classmethod
+    def empty(cls, n_seqs, max_pages, num_pages, page_size, device="cuda"):
+        """Sequences without tokens over a pool of free pages."""
+        import torch
+        table, lens, held, refs = (torch.zeros(shape, dtype=torch.int32, device=device)
+                                   for shape in ((n_seqs, max_pages), (n_seqs,), (n_seqs,), (num_pages,)))
+        return cls(table, lens, held, refs, page_size)
+
+
+class KVMoves:
+    """A list of page moves (qg_kv_moves): list int32 [capacity][4] of {source,
+    destination, tokens, 0} and count int32 [1], which kv_pages_reserve and
+    kv_pages_compact write and kv_pages_copy carries out. KVMoves.empty
+    allocates one."""
+
+    def __init__(self, moves, count):
+        import torch
+        self.index = moves.get_device()
+        if self.index < 0:
+            raise ValueError("a list of moves must be CUDA tensors")
+        _kv_tensors(self.index, moves, count)
+        _kv_check("list and count", torch.int32, moves, count)
+        if moves.dim() != 2 or moves.shape[1] != 4 or tuple(count.shape) != (1,):
+            raise ValueError("a list of moves must have shapes [capacity][4] and [1]")
+        self.list, self.count, self.capacity = moves, count, moves.shape[0]
+        self.rec = QgKvMoves(_ptr(moves), _ptr(count), self.capacity)
+        self.ref = ctypes.byref(self.rec)
+
+    @classmethod
+    def empty(cls, capacity, device="cuda"):
+        import torch
+        return cls(torch.zeros((capacity, 4), dtype=torch.int32, device=device),
+                   torch.zeros(1, dtype=torch.int32, device=device))
+
+
+def _kv_int32(name, t, index, shape):
+    import torch
+    if t is not None and (t.dtype is not torch.int32 or t.get_device() != index or t.shape != shape or
+                          not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on the pages' device")
+
+
+def kv_pages_fork(pages, parent, stream=None):
+    """Row i of the pages goes on from row parent[i] (int32 [n]; -1: from
+    nothing, which frees its pages), sharing that row's pages."""
+    _kv_int32("parent", parent, pages.index, (pages.n_seqs,))
+    with _OnDevice(pages.index):
+        _check("kv_pages_fork", lib().kv_pages_fork(pages.ref, _ptr(parent), _stream(stream, pages.refs)))
+
+
+def kv_pages_reserve(pages, n_new, moves, n_free=None, stream=None):
+    """Pages of its own for each sequence's next n_new tokens (int32 [n]); the
+    part-filled pages that are replaced join `moves`. n_free int32 [1]: the free
+    pages left, negative (and nothing changed) where they do not suffice."""
+    _kv_int32("n_new", n_new, pages.index, (pages.n_seqs,))
+    _kv_int32("n_free", n_free, pages.index, (1,))
+    if moves.index != pages.index:
+        raise ValueError("pages and moves must be on one device")
+    with _OnDevice(pages.index):
+        _check("kv_pages_reserve", lib().kv_pages_reserve(pages.ref, _ptr(n_new), moves.ref, _ptr(n_free),
+                                                          _stream(stream, pages.refs)))
+
+
+def kv_pages_compact(pages, moves, page_map, n_live=None, stream=None):
+    """Give the highest pages in use the lowest free numbers, moves.capacity of
+    them at most; page_map int32 [num_pages] receives each page's number, n_live
+    int32 [1] the pages in use."""
+    _kv_int32("page_map", page_map, pages.index, (pages.num_pages,))
+    _kv_int32("n_live", n_live, pages.index, (1,))
+    if moves.index != pages.index:
+        raise ValueError("pages and moves must be on one device")
+    with _OnDevice(pages.index):
+        _check("kv_pages_compact", lib().kv_pages_compact(pages.ref, moves.ref, _ptr(page_map), _ptr(n_live),
+                                                          _stream(stream, pages.refs)))
+    return page_map
+
+
+def kv_pages_copy(cache, moves, stream=None):
+    """Carry out a list of moves in one cache."""
+    if moves.index != cache.index:
+        raise ValueError("cache and moves must be on one device")
+    with _OnDevice(cache.index):
+        _check("kv_pages_copy", lib().kv_pages_copy(cache.ref, moves.ref, _stream(stream, cache.k)))
+
+
+def beam_select_workspace_size(lanes, beams, vocab, n_out) -> int:
+    """Bytes of beam_select's workspace on the current device."""
+    b = ctypes.c_size_t(0)
+    _check("beam_select_workspace_size", lib().beam_select_workspace_size(int(lanes), int(beams), int(vocab), int(n_out),
+                                                                          ctypes.byref(b)))
+    return b.value
+
+
+def beam_select(logits, scores, out_scores, out_tokens, out_parents, out_finished=None, finished=None, eos=-1, pad=0,
+                workspace=None, stream=None):
+    """The out_scores.shape[1] best continuations of each lane over its beams
+    and the vocabulary. logits bf16 or fp32 [lanes * beams][vocab] (rows may lie
+    apart), scores fp32 [lanes][beams], finished bool or uint8 [lanes][beams]
+    or None; outputs [lanes][n_out]: scores fp32, tokens and parents (rows of
+    logits) int32, finished bool or uint8 or None. workspace: a uint8 tensor of
+    beam_select_workspace_size bytes, not shared by calls that may overlap on
+    the GPU."""
+    import torch
+    dev = logits.get_device()
+    if dev < 0:
+        raise ValueError("logits must be a CUDA tensor")
+    if scores.dim() != 2 or out_scores.dim() != 2 or logits.dim() != 2:
+        raise ValueError("logits must be [lanes * beams][vocab], scores [lanes][beams] and outputs [lanes][n_out]")
+    (lanes, beams), n_out, (rows, vocab) = scores.shape, out_scores.shape[1], logits.shape
+    if rows != lanes * beams or (vocab > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must have a row for each of the scores, with its values next to each other")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("logits must be bfloat16 or float32")
+    _kv_tensors(dev, scores, out_scores, out_tokens, out_parents, out_finished, finished, workspace)
+    out = (lanes, n_out)
+    for name, t, shape, types in (("scores", scores, (lanes, beams), (torch.float32,)),
+                                  ("finished", finished, (lanes, beams), (torch.bool, torch.uint8)),
+                                  ("out_scores", out_scores, out, (torch.float32,)),
+                                  ("out_tokens", out_tokens, out, (torch.int32,)),
+                                  ("out_parents", out_parents, out, (torch.int32,)),
+                                  ("out_finished", out_finished, out, (torch.bool, torch.uint8))):
+        if t is not None and (t.shape != shape or t.dtype not in types):
+            raise ValueError(f"{name} must be {' or '.join(map(str, types))} {list(shape)}")
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    dt = QG_OUT_F32 if logits.dtype is torch.float32 else QG_OUT_BF16
+    with _OnDevice(dev):
+        _check("beam_select", lib().beam_select(
+            _ptr(logits), dt, logits.stride(0) if rows > 1 else vocab, lanes, beams, vocab, _ptr(scores), _ptr(finished),
+            int(eos), int(pad), n_out, _ptr(out_scores), _ptr(out_tokens), _ptr(out_parents), _ptr(out_finished),
+            _ptr(workspace), nbytes, _stream(stream, logits)))
+    return out_scores, out_tokens, out_parents, out_finished
 
 
 def read_probe(buf, sink, stream=None):

@@ -502,12 +502,161 @@ QG_API qg_status tree_attention(const qg_kv_cache* cache, const qg_kv_batch* bat
  * this cache, these heads and max_tree. */
 QG_API qg_status tree_attention_workspace_size(const qg_kv_cache* cache, int q_heads, int max_tree, size_t* bytes);
 
+/* ------------------------------------------------------------------ pages of sequences that share them */
+
+/*
+ * The pages that the sequences of a cache hold, in caller-owned DEVICE data
+ * which the calls below change in place (a captured step replays on it). One
+ * such record serves every layer's qg_kv_cache: page p is page p of each.
+ *   page_table  int32 [n_seqs][max_pages], as qg_kv_batch's
+ *   seq_lens    int32 [n_seqs], tokens of each sequence
+ *   n_pages     int32 [n_seqs], entries of its table row that the sequence
+ *               holds, at least ceil(seq_lens / page_size); entries behind
+ *               them are neither read nor changed
+ *   refs        int32 [num_pages], how often a page is held: once for each
+ *               table entry that names it, and once more for each holder
+ *               outside the table (a prefix store). 0 is a free page
+ *   n_seqs      0..1024      max_pages >= 1
+ *   num_pages   1..2^22 (else QG_ERR_UNSUPPORTED)
+ *   page_size   a multiple of 16, 16..1024
+ * Every result is a function of these alone: pages are handed out lowest
+ * number first, sequences in order. A sequence whose entries do not fit (a
+ * length or n_pages out of range, fewer pages than its length needs, more than
+ * 2^30 positions) is taken as one without tokens and pages; this, and an entry
+ * in use that names a page outside the pool, records QG_ERR_INVALID_ARG in the
+ * device status word.
+ */
+typedef struct {
+    int32_t* page_table;
+    int32_t* seq_lens;
+    int32_t* n_pages;
+    int32_t* refs;
+    int n_seqs;
+    int max_pages;
+    int num_pages;
+    int page_size;
+} qg_kv_pages;
+
+/*
+ * A list of moves of pages in device data: entry i of list = {source page,
+ * destination page, tokens, 0}, the first `tokens` of the page's tokens; count
+ * = the entries in use.
+ *   list      int32 [capacity][4]     count  int32 [1]     capacity 1..2^22
+ */
+typedef struct {
+    int32_t* list;
+    int32_t* count;
+    int capacity;
+} qg_kv_moves;
+
+/*
+ * Let sequences go on from others, as beams do from their parents: row i of
+ * the table, its length and its pages become those that row parent[i] had
+ * before the call, or none for parent[i] = -1. Nothing is copied: the pages
+ * are shared from then on (refs counts them), pages that no row goes on from
+ * lose their counts and are free at 0, and so are pages behind the one that
+ * holds a sequence's last token (n_pages = ceil(seq_lens / page_size)). So
+ * parent[i] = i drops what was held ahead, and -1 frees a sequence.
+ *   parent  int32 [n_seqs]. One outside -1..n_seqs-1 records
+ *           QG_ERR_INVALID_ARG and its row goes on from itself.
+ * An entry that names a page outside the pool is handed on but not counted.
+ */
+QG_API qg_status kv_pages_fork(const qg_kv_pages* pages, const int32_t* parent, cudaStream_t stream);
+
+/*
+ * Pages for what is written next: afterwards every sequence b with n_new[b] > 0
+ * holds the pages of its positions below seq_lens[b] + n_new[b], and those from
+ * seq_lens[b] on are its own (kv_cache_append may write them). A part-filled
+ * last page that others hold too is replaced by a new one, and its tokens join
+ * `moves` (kv_pages_copy in every layer before the append); where all who hold
+ * it are sequences of this call that write, the lowest of them keeps it.
+ * Either every sequence gets its pages or, where the free ones do not suffice,
+ * the call changes nothing but moves->count = 0 and n_free.
+ *   n_new   int32 [n_seqs], 0: the row is left as it is
+ *   moves   capacity of at least n_seqs, entries in the order of the rows;
+ *           entries behind count are not written
+ *   n_free  int32 [1] or NULL: the free pages left, or minus the missing ones
+ * A row with a negative n_new, more positions than max_pages * page_size or
+ * 2^30, or a page to be written that is outside the pool or, behind the last
+ * token's page, shared (kv_pages_fork drops such pages) is left as it is and
+ * records QG_ERR_INVALID_ARG in the device status word.
+ */
+QG_API qg_status kv_pages_reserve(const qg_kv_pages* pages, const int32_t* n_new, const qg_kv_moves* moves,
+                                  int32_t* n_free, cudaStream_t stream);
+
+/*
+ * Move pages in use into the lowest free places: with L pages in use, the
+ * highest page at L or above goes into the lowest free place below L, the next
+ * highest into the next lowest, moves->capacity of them at most. The table's
+ * entries and refs follow; kv_pages_copy in every layer moves the pages' data
+ * (whole pages). Once all fit, the pool's first L pages are the ones in use.
+ *   page_map  int32 [num_pages] out: the new number of each page in use (its
+ *             old one where it stays), -1 for a free one: for holders outside
+ *             the table
+ *   n_live    int32 [1] or NULL: L
+ */
+QG_API qg_status kv_pages_compact(const qg_kv_pages* pages, const qg_kv_moves* moves, int32_t* page_map,
+                                  int32_t* n_live, cudaStream_t stream);
+
+/*
+ * Carry out a list of moves in one cache (one layer): codes and scales of the
+ * first `tokens` tokens, all heads, keys and values; the destination's other
+ * tokens stay as they are. Moves run side by side: no page may be a
+ * destination twice, nor both a source and a destination. An entry with a page
+ * outside the cache or tokens outside 0..page_size is left out and records
+ * QG_ERR_INVALID_ARG in the device status word, as does a count outside
+ * 0..capacity (nothing is moved then).
+ */
+QG_API qg_status kv_pages_copy(const qg_kv_cache* cache, const qg_kv_moves* moves, cudaStream_t stream);
+
+/*
+ * Beam search's selection. Row r = lane * beams + beam has the logits
+ * logits[r][0 .. vocab) and the score scores[r] so far; with
+ * z_r = ln sum_t exp(logits[r][t]), its candidates are the tokens t with
+ * score scores[r] + logits[r][t] - z_r. Of a lane's candidates the n_out best
+ * are given in order, ties to the lower row and then the lower token:
+ *   out_scores   fp32 [lanes][n_out]
+ *   out_tokens   int32 [lanes][n_out]
+ *   out_parents  int32 [lanes][n_out], the row r it continues (as
+ *                kv_pages_fork's parent where n_out = beams)
+ *   out_finished u8 [lanes][n_out] or NULL: 1 if the row had finished or the
+ *                token is eos, else 0
+ * A finished row has one candidate, the token pad with its score unchanged. A
+ * row with the score -infinity has none and its logits are not read; a logit
+ * of -infinity is no candidate. Places for which there is no candidate get the
+ * score -infinity, the token pad, the lane's first row and finished = 0. A row
+ * whose logits hold a NaN or +infinity, or whose score is one, has no
+ * candidates and records QG_ERR_INVALID_ARG in the device status word.
+ *   logits      bf16 or fp32 per logits_dtype, row r at logits + r *
+ *               row_stride; row_stride in elements, any number >= vocab
+ *   lanes       >= 0; lanes * beams at most 65536      beams, n_out  1..64
+ *   vocab       1..2^24     eos, pad  token numbers (eos -1: none)
+ *   scores      fp32 [lanes][beams]     finished  u8 [lanes][beams] or NULL
+ *   out_scores and out_finished may be scores and finished where n_out = beams
+ *   workspace   device memory of at least beam_select_workspace_size() bytes,
+ *               256-byte aligned; needs no initialisation, is scratch after
+ *               the call, and may be shared by calls that do not overlap on
+ *               the GPU
+ * Sums of exponentials are held in fp32 within a part of a row and in 64 bits
+ * across parts; scores are compared in 64 bits and rounded once (one below
+ * fp32's range becomes -infinity). Rows with
+ * equal logits get equal sums whatever their alignment, and the result does
+ * not depend on the stream's other work (fixed order).
+ */
+QG_API qg_status beam_select(const void* logits, qg_out logits_dtype, int64_t row_stride, int lanes, int beams,
+                             int vocab, const float* scores, const uint8_t* finished, int eos, int pad, int n_out,
+                             float* out_scores, int32_t* out_tokens, int32_t* out_parents, uint8_t* out_finished,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of beam_select's workspace on the current device for these sizes. */
+QG_API qg_status beam_select_workspace_size(int lanes, int beams, int vocab, int n_out, size_t* bytes);
+
 /*
  * Synchronise `stream`, then return and clear the device status word:
  * QG_OK, QG_ERR_DEVICE_TIMEOUT when a bounded device-side wait gave up (the
  * kernel stopped early; its outputs are undefined), or QG_ERR_INVALID_ARG for
  * out-of-range device data (MoE expert ids, a cache batch's lengths, pages and
- * paths).
+ * paths, page records and moves) or logits that have no sum.
  */
 QG_API qg_status qg_last_device_status(cudaStream_t stream);
 
