@@ -13,11 +13,11 @@ namespace {
 
 constexpr int kScanWarps = 8, kScanThreads = 32 * kScanWarps;
 constexpr int kVec = 8;                              // values a thread takes at a time
-constexpr int kUnroll = 4;
-constexpr int kTile = 32 * kVec * kUnroll;           // values a warp takes at a time
-constexpr int kList = 128;                           // keys a warp holds
-constexpr int kMaxOut = 64;
-constexpr int kJoinThreads = 256;
+constexpr int kList = 1024;                          // tokens a block can hold
+constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
+constexpr int kGroups = kJoinThreads / 4;            // candidates' groups, by whose best one is bounded
+constexpr int kPairs = 1024;                         // parts of a lane's rows, at most
+constexpr int kPicked = 512;                         // candidates of a lane that are looked at in 64 bits
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -111,131 +111,208 @@ __device__ __forceinline__ void load8(const uint8_t* row, int vocab, int e, floa
     }
 }
 
-// A warp's best tokens so far: up to kList keys, and a bound below which none
-// is among its n best.
-struct Best {
-    uint64_t* keys;
-    int count;
-    int n;
-    uint64_t bound;
-};
-
-// Keep the n best, in order: each key's place is the number of greater ones.
-__device__ __forceinline__ void keep_best(Best& b, int lane)
+// The n-th largest of the warp's values, n <= 32: all sorted, greatest first.
+__device__ __forceinline__ float nth_of_warp(float v, int n)
 {
-    uint64_t mine[kList / 32];
-    int place[kList / 32];
-    __syncwarp();
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < kList / 32; ++i) {
-        mine[i] = lane + 32 * i < b.count ? b.keys[lane + 32 * i] : 0;
-        place[i] = 0;
-    }
-    for (int j = 0; j < b.count; ++j) {
-        const uint64_t k = b.keys[j];
+    for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
-        for (int i = 0; i < kList / 32; ++i) place[i] += k > mine[i];
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kList / 32; ++i)
-        if (mine[i] && place[i] < b.n) b.keys[place[i]] = mine[i];
-    __syncwarp();
-    b.count = min(b.count, b.n);
-    if (b.count == b.n) b.bound = b.keys[b.n - 1];
+        for (int step = size / 2; step; step >>= 1) {
+            const float o = __shfl_xor_sync(0xffffffffu, v, step);
+            const bool greater_first = (lane & size) == 0 || size == 32;
+            v = ((lane & step) == 0) == greater_first ? fmaxf(v, o) : fminf(v, o);
+        }
+    return __shfl_sync(0xffffffffu, v, n - 1);
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_constant__ BeamArgs a, int parts, int span,
-                                                                 float2* sums, uint64_t* out)
+// A part of a row: the maximum and the scaled sum of its exponentials, and how
+// many of its tokens are handed on.
+struct PartSum {
+    float top;
+    float sum;
+    int count;
+    int pad;
+};
+
+// A block's tokens that may be among its n best: those above `bound`, a key
+// that n of the block's tokens reach.
+struct ScanSmem {
+    uint64_t list[kList];
+    uint64_t bound;
+    int count;
+    float tops[kScanWarps];
+    float2 sums[kScanWarps];
+};
+
+// Keep the n best of the first k keys, in order: a key's place is the number
+// of greater ones.
+__device__ __forceinline__ void keep_best(ScanSmem& s, int k, int n)
 {
-    __shared__ uint64_t lists[kScanWarps][kList];
-    __shared__ uint64_t merged[kScanWarps * kMaxOut];
-    __shared__ int counts[kScanWarps];
-    __shared__ float2 warp_sums[kScanWarps];
+    constexpr int kMine = kList / kScanThreads;
+    uint64_t mine[kMine];
+    int place[kMine];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int at = threadIdx.x + i * kScanThreads;
+        mine[i] = at < k ? s.list[at] : 0;
+        place[i] = 0;
+    }
+    if (k <= kScanThreads) {
+        for (int j = 0; j < k; ++j) place[0] += s.list[j] > mine[0];
+    } else {
+        for (int j = 0; j < k; ++j) {
+            const uint64_t x = s.list[j];
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) place[i] += x > mine[i];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+        if (mine[i] && place[i] < n) {
+            s.list[place[i]] = mine[i];
+            if (place[i] == n - 1) s.bound = mine[i];
+        }
+    if (threadIdx.x == 0) s.count = min(k, n);
+    __syncthreads();
+}
+
+// A block takes a part of a row, U * 8 values per thread at a time. Its bound
+// starts from the first of these: the m-th largest of a warp's threads'
+// maxima, the least over w warps, with m w >= n, is reached by n tokens. Few
+// tokens reach it (about n H(w) of independent ones for m = 1), and the list
+// that these fill is cut to its n best when it is long, which raises the bound.
+template <bool F32, int U>
+__global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_constant__ BeamArgs a, int parts, int span, int slots,
+                                                                 PartSum* sums, uint64_t* out)
+{
+    __shared__ ScanSmem s;
+    constexpr int kTile = kScanThreads * kVec * U;
     pdl_enter();
     const int row_i = blockIdx.x / parts, part = blockIdx.x % parts;
     if (!row_live(a, row_i)) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.n_out;
     const uint8_t* row = static_cast<const uint8_t*>(a.logits) + row_i * a.stride * (F32 ? 4 : 2);
     const int begin = part * span, end = min(begin + span, a.vocab);
-    Best best{lists[warp], 0, a.n_out, make_key(-INFINITY, 0)};
+    if (tid == 0) {
+        s.count = 0;
+        s.bound = make_key(-INFINITY, 0);
+    }
+    uint64_t bound = make_key(-INFINITY, 0);
     float top = kLowest, sum = 0.f;
-    for (int base = begin + warp * kTile; base < end; base += kScanWarps * kTile) {
-        float v[kUnroll][kVec];
+    for (int base = begin; base < end; base += kTile) {
+        float v[U][kVec];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) load8<F32>(row, a.vocab, base + u * 32 * kVec + lane * kVec, v[u]);
+        for (int u = 0; u < U; ++u) load8<F32>(row, a.vocab, base + (u * kScanThreads + tid) * kVec, v[u]);
+        float most = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            float m = v[u][0];
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 1; i < kVec; ++i) m = fmaxf(m, v[u][i]);
-            if (m > top) {
-                sum *= ex2((top - m) * kLog2e);
-                top = m;
-            }
+            for (int i = 0; i < kVec; ++i) most = fmaxf(most, v[u][i]);
+        if (most > top) {
+            sum *= ex2((top - most) * kLog2e);
+            top = most;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < kVec; ++i) sum += ex2((v[u][i] - top) * kLog2e);
-            if (!__any_sync(0xffffffffu, m >= key_value(best.bound))) continue;
-#pragma unroll 1
-            for (int i = 0; i < kVec; ++i) {
-                float x = v[u][0];
-#pragma unroll
-                for (int j = 1; j < kVec; ++j) x = i == j ? v[u][j] : x;
-                const uint64_t key = make_key(x, static_cast<uint32_t>(base + u * 32 * kVec + lane * kVec + i));
-                uint32_t with = __ballot_sync(0xffffffffu, x == x && key > best.bound);
-                if (!with) continue;
-                if (best.count + __popc(with) > kList) {
-                    keep_best(best, lane);
-                    with = __ballot_sync(0xffffffffu, x == x && key > best.bound);
-                }
-                if (with >> lane & 1u) best.keys[best.count + __popc(with & ((1u << lane) - 1u))] = key;
-                best.count += __popc(with);
+        if (base == begin) {
+            const int warps = max(1, min(kScanWarps, (end - begin) / (32 * kVec)));    // whose threads all have values
+            const int m = (n + warps - 1) / warps;
+            if (m <= 32) {
+                const float t = nth_of_warp(most, m);
+                if (lane == 0) s.tops[warp] = t;
+                __syncthreads();
+                float least = s.tops[0];
+                for (int w = 1; w < warps; ++w) least = fminf(least, s.tops[w]);
+                if (least > -INFINITY) bound = make_key(least, 0xFFFFFFFFu) - 1;
+            } else {
+                __syncthreads();
             }
         }
+        for (;;) {
+            const float least = key_value(bound);
+            int seen = 0;
+            if (__any_sync(0xffffffffu, most >= least)) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    uint32_t hits = 0;
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) hits |= static_cast<uint32_t>(v[u][i] >= least) << i;
+                    while (__any_sync(0xffffffffu, hits != 0)) {
+                        const int at = __ffs(hits) - 1;
+                        float x = v[u][0];
+#pragma unroll
+                        for (int i = 1; i < kVec; ++i) x = i == at ? v[u][i] : x;
+                        const uint64_t key = make_key(x, static_cast<uint32_t>(base + (u * kScanThreads + tid) * kVec + at));
+                        const uint32_t with = __ballot_sync(0xffffffffu, hits && key > bound);
+                        int place = 0;
+                        if (lane == 0 && with) place = atomicAdd(&s.count, __popc(with));
+                        place = __shfl_sync(0xffffffffu, place, 0);
+                        seen = max(seen, place + __popc(with));
+                        place += __popc(with & ((1u << lane) - 1u));
+                        if ((with >> lane & 1u) && place < kList) s.list[place] = key;
+                        hits &= hits - 1;
+                    }
+                }
+            }
+            if (!__syncthreads_or(seen > 2 * slots)) break;
+            // a long list: cut, which raises the bound
+            const int k = s.count;
+            keep_best(s, min(k, kList), n);
+            bound = s.bound;
+            if (k <= kList) break;
+            // some found no place: those of this tile are taken again, above the new bound (each turn at least
+            // kList - n fewer)
+            __syncthreads();
+            if (warp == 0) {
+                const uint64_t k0 = lane < n ? s.list[lane] : 0, k1 = lane + 32 < n ? s.list[lane + 32] : 0;
+                const bool old0 = k0 && key_token(k0) < static_cast<uint32_t>(base);
+                const bool old1 = k1 && key_token(k1) < static_cast<uint32_t>(base);
+                const uint32_t b0 = __ballot_sync(0xffffffffu, old0), b1 = __ballot_sync(0xffffffffu, old1);
+                __syncwarp();
+                if (old0) s.list[__popc(b0 & ((1u << lane) - 1u))] = k0;
+                if (old1) s.list[__popc(b0) + __popc(b1 & ((1u << lane) - 1u))] = k1;
+                if (lane == 0) s.count = __popc(b0) + __popc(b1);
+            }
+            bound -= 1;
+            __syncthreads();
+        }
     }
-    if (best.count > best.n) keep_best(best, lane);
     // the warp's sum, then the block's, in a fixed order
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-        const float t = __shfl_xor_sync(0xffffffffu, top, o), s = __shfl_xor_sync(0xffffffffu, sum, o);
+        const float t = __shfl_xor_sync(0xffffffffu, top, o), x = __shfl_xor_sync(0xffffffffu, sum, o);
         const float m = fmaxf(top, t);
-        // lanes that swap have to round alike: the two products are added, whichever is whose
-        sum = __fadd_rn(__fmul_rn(sum, ex2((top - m) * kLog2e)), __fmul_rn(s, ex2((t - m) * kLog2e)));
+        // rounded products, so that two lanes that swap get the same
+        sum = __fadd_rn(__fmul_rn(sum, ex2((top - m) * kLog2e)), __fmul_rn(x, ex2((t - m) * kLog2e)));
         top = m;
     }
-    if (lane == 0) {
-        warp_sums[warp] = make_float2(top, sum);
-        counts[warp] = best.count;
-    }
+    if (lane == 0) s.sums[warp] = make_float2(top, sum);
     __syncthreads();
-    if (threadIdx.x == 0) {
-        float m = kLowest, s = 0.f;
-        for (int w = 0; w < kScanWarps; ++w) m = fmaxf(m, warp_sums[w].x);
-        for (int w = 0; w < kScanWarps; ++w) s += warp_sums[w].y * ex2((warp_sums[w].x - m) * kLog2e);
-        sums[blockIdx.x] = make_float2(m, s);
+    int k = s.count;
+    if (k > slots) {
+        keep_best(s, k, n);
+        k = n;
     }
-    int total = 0, before = 0;
-    for (int w = 0; w < kScanWarps; ++w) {
-        if (w < warp) before += counts[w];
-        total += counts[w];
+    if (tid == 0) {
+        float m = kLowest, x = 0.f;
+#pragma unroll
+        for (int w = 0; w < kScanWarps; ++w) m = fmaxf(m, s.sums[w].x);
+#pragma unroll
+        for (int w = 0; w < kScanWarps; ++w) x += s.sums[w].y * ex2((s.sums[w].x - m) * kLog2e);
+        sums[blockIdx.x] = PartSum{m, x, k, 0};
     }
-    for (int i = lane; i < best.count; i += 32) merged[before + i] = best.keys[i];
-    __syncthreads();
-    uint64_t* to = out + static_cast<int64_t>(blockIdx.x) * a.n_out;
-    for (int i = threadIdx.x; i < total; i += kScanThreads) {
-        const uint64_t k = merged[i];
-        int place = 0;
-        for (int j = 0; j < total; ++j) place += merged[j] > k;
-        if (place < a.n_out) to[place] = k;
-    }
-    for (int i = total + threadIdx.x; i < a.n_out; i += kScanThreads) to[i] = 0;
+    for (int i = tid; i < k; i += kScanThreads) out[static_cast<int64_t>(blockIdx.x) * slots + i] = s.list[i];
 }
 
-// A candidate of a lane: its score, and its row and token in one number, the
-// lower the better.
+// A candidate of a lane: its score as a whole number of the same order, and
+// its row and token in one number, the lower the better. {0, ~0}: none.
 struct Candidate {
-    double score;
+    uint64_t score;
     uint64_t id;
 };
 
@@ -244,118 +321,242 @@ __device__ __forceinline__ bool better(const Candidate& x, const Candidate& y)
     return x.score > y.score || (x.score == y.score && x.id < y.id);
 }
 
-// A block per lane.
-__global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_constant__ BeamArgs a, int parts, const float2* sums,
-                                                                 const uint64_t* keys)
+__device__ __forceinline__ uint64_t ordered64(double v)
 {
-    enum { kNone, kGoesOn, kFinished };
-    __shared__ double scores[64], z[64];
-    __shared__ int state[64];
-    __shared__ Candidate warps[kJoinThreads / 32];
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+    return b ^ (b >> 63 ? ~0ull : 1ull << 63);
+}
+
+__device__ __forceinline__ double value64(uint64_t o)
+{
+    return __longlong_as_double(static_cast<long long>(o ^ (o >> 63 ? 1ull << 63 : ~0ull)));
+}
+
+enum RowState { kNone, kGoesOn, kFinished };
+
+struct JoinSmem {
+    double score[64];
+    double z[64];                // ln of the row's sum
+    float base[64];              // score - z, rounded
+    int state[64];
+    int parts[kPairs];           // handed-on tokens of a part, and its beam from bit 16 on
+    float best[kGroups];
+    Candidate picked[kPicked];
+    Candidate warps[kJoinWarps];
+    float bound;
+    int count;
+};
+
+// Candidate `i` of a beam's part from its key, in 64 bits.
+__device__ __forceinline__ Candidate candidate(const JoinSmem& s, int row0, int beam, uint64_t key)
+{
+    return Candidate{ordered64(s.score[beam] + (static_cast<double>(key_value(key)) - s.z[beam])),
+                     static_cast<uint64_t>(row0 + beam) << 24 | key_token(key)};
+}
+
+__device__ __forceinline__ Candidate finished_candidate(const BeamArgs& a, const JoinSmem& s, int row0, int beam)
+{
+    return Candidate{ordered64(s.score[beam]), static_cast<uint64_t>(row0 + beam) << 24 | static_cast<uint32_t>(a.pad)};
+}
+
+__device__ __forceinline__ void write_out(const BeamArgs& a, const JoinSmem& s, int row0, int place, const Candidate& c)
+{
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * a.n_out + place;
+    const bool some = c.id != ~0ull;
+    const int row = some ? static_cast<int>(c.id >> 24) : row0;
+    const int token = some ? static_cast<int>(c.id & 0xFFFFFFu) : a.pad;
+    a.out_scores[at] = some ? static_cast<float>(value64(c.score)) : -INFINITY;
+    a.out_tokens[at] = token;
+    a.out_parents[at] = row;
+    if (a.out_finished) a.out_finished[at] = some && (s.state[row - row0] == kFinished || token == a.eos);
+}
+
+// A block per lane. A candidate's score in 32 bits, f, is off by less than e =
+// 2^-21 (|score - z| + |logit|): score - z is rounded once and the sum with the
+// logit once, 2^-24 of each. The n-th largest of the groups' best f - e is
+// reached by n candidates, so only those with f + e at or above it are looked
+// at in 64 bits (which this GPU adds and compares slowly).
+__global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_constant__ BeamArgs a, int parts, int slots_log2,
+                                                                 const PartSum* sums, const uint64_t* keys)
+{
+    __shared__ JoinSmem s;
     pdl_enter();
-    const int lane = blockIdx.x, tid = threadIdx.x, row0 = lane * a.beams;
-    if (tid < a.beams) {
-        const int row = row0 + tid;
-        const float s = a.scores[row];
-        int st = kNone;
-        double zr = 0.0;
-        if (s != s || s == INFINITY) {
-            set_device_status(a.status, QG_ERR_INVALID_ARG);
-        } else if (s > -INFINITY) {
-            if (a.finished && a.finished[row]) {
-                st = kFinished;
-            } else {
-                float top = kLowest;
-                for (int p = 0; p < parts; ++p) top = fmaxf(top, sums[static_cast<int64_t>(row) * parts + p].x);
-                double sum = 0.0;
-                for (int p = 0; p < parts; ++p) {
-                    const float2 x = sums[static_cast<int64_t>(row) * parts + p];
-                    sum += x.y * exp(static_cast<double>(x.x) - top);
-                }
-                if (!(sum >= 0.0 && sum < INFINITY))
-                    set_device_status(a.status, QG_ERR_INVALID_ARG);
-                else if (sum > 0.0) {
-                    st = kGoesOn;
-                    zr = top + log(sum);
-                }
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.n_out;
+    const int row0 = static_cast<int>(blockIdx.x) * a.beams;
+    for (int beam = warp; beam < a.beams; beam += kJoinWarps) {
+        const int row = row0 + beam;
+        const float score = a.scores[row];
+        const bool number = score > -INFINITY && score < INFINITY;
+        const bool done = a.finished && a.finished[row];
+        int state = kNone;
+        double z = 0.0;
+        if (!number) {
+            if (lane == 0 && score != -INFINITY) set_device_status(a.status, QG_ERR_INVALID_ARG);
+        } else if (done) {
+            state = kFinished;
+        } else {
+            const PartSum* p = sums + static_cast<int64_t>(row) * parts;
+            float top = kLowest;
+            for (int i = lane; i < parts; i += 32) top = fmaxf(top, p[i].top);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            double sum = 0.0;
+            for (int i = lane; i < parts; i += 32) {
+                const PartSum x = p[i];
+                sum += static_cast<double>(x.sum) * expf(x.top - top);
+                s.parts[beam * parts + i] = x.count | beam << 16;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (!(sum >= 0.0 && sum < INFINITY)) {
+                if (lane == 0) set_device_status(a.status, QG_ERR_INVALID_ARG);
+            } else if (sum > 0.0) {
+                state = kGoesOn;
+                z = top + log(sum);
             }
         }
-        scores[tid] = s;
-        z[tid] = zr;
-        state[tid] = st;
+        if (state != kGoesOn)
+            for (int i = lane; i < parts; i += 32) s.parts[beam * parts + i] = beam << 16;
+        if (lane == 0) {
+            s.score[beam] = score;
+            s.z[beam] = z;
+            s.base[beam] = static_cast<float>(score - z);
+            s.state[beam] = state;
+        }
+    }
+    if (tid == 0) {
+        s.bound = -INFINITY;
+        s.count = 0;
     }
     __syncthreads();
-    const int per_row = parts * a.n_out, all = a.beams * per_row;
-    const Candidate none{-INFINITY, ~0ull};
-    Candidate last{INFINITY, 0};
-    for (int o = 0; o < a.n_out; ++o) {
-        Candidate best = none;
-        for (int i = tid; i < all; i += kJoinThreads) {
-            const int beam = i / per_row, place = i % per_row;
-            const int row = row0 + beam;
-            Candidate c = none;
-            if (state[beam] == kFinished) {
-                if (place == 0) c = Candidate{scores[beam], static_cast<uint64_t>(row) << 24 | static_cast<uint32_t>(a.pad)};
-            } else if (state[beam] == kGoesOn) {
-                const uint64_t key = keys[static_cast<int64_t>(row) * per_row + place];
-                if (key)
-                    c = Candidate{scores[beam] + (static_cast<double>(key_value(key)) - z[beam]),
-                                  static_cast<uint64_t>(row) << 24 | key_token(key)};
+
+    const int all = a.beams * parts << slots_log2, mask = (1 << slots_log2) - 1;
+    const uint64_t* mine = keys + (static_cast<int64_t>(row0) * parts << slots_log2);
+    const float kOff = 4.76837158e-7f;                  // 2^-21
+    float best = -INFINITY;
+    for (int i = tid; i < all; i += kJoinThreads) {
+        const int p = s.parts[i >> slots_log2];
+        if ((i & mask) >= (p & 0xFFFF)) continue;
+        const float x = key_value(mine[i]), base = s.base[p >> 16];
+        best = fmaxf(best, base + x - kOff * (fabsf(base) + fabsf(x)));
+    }
+    if (tid < a.beams && s.state[tid] == kFinished) best = fmaxf(best, static_cast<float>(s.score[tid]));
+    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
+    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
+    if ((lane & 3) == 0) s.best[tid / 4] = best;
+    __syncthreads();
+    if (tid < kGroups) {
+        const float x = s.best[tid];
+        int place = 0;
+#pragma unroll 8
+        for (int j = 0; j < kGroups; ++j) {
+            const float y = s.best[j];
+            place += y > x || (y == x && j < tid);
+        }
+        if (place == n - 1) s.bound = x;
+    }
+    __syncthreads();
+    const float bound = s.bound;
+    for (int i0 = 0; i0 < all; i0 += kJoinThreads) {
+        const int i = i0 + tid;
+        bool take = false;
+        uint64_t key = 0;
+        int beam = 0;
+        if (i < all) {
+            const int p = s.parts[i >> slots_log2];
+            beam = p >> 16;
+            if ((i & mask) < (p & 0xFFFF)) {
+                key = mine[i];
+                const float x = key_value(key), base = s.base[beam];
+                take = !(base + x + kOff * (fabsf(base) + fabsf(x)) < bound);
             }
-            if (better(last, c) && better(c, best)) best = c;
+        }
+        if (take) {
+            const int at = atomicAdd(&s.count, 1);
+            if (at < kPicked) s.picked[at] = candidate(s, row0, beam, key);
+        }
+    }
+    if (tid < a.beams && s.state[tid] == kFinished && s.score[tid] >= bound) {
+        const int at = atomicAdd(&s.count, 1);
+        if (at < kPicked) s.picked[at] = finished_candidate(a, s, row0, tid);
+    }
+    __syncthreads();
+    const int count = s.count;
+    if (count <= kPicked) {
+        // a candidate's place is the number of better ones
+        if (tid < count) {
+            const Candidate c = s.picked[tid];
+            int place = 0;
+            for (int j = 0; j < count; ++j) place += better(s.picked[j], c);
+            if (place < n) write_out(a, s, row0, place, c);
+        }
+        for (int o = count + tid; o < n; o += kJoinThreads) write_out(a, s, row0, o, Candidate{0, ~0ull});
+        return;
+    }
+    // more candidates within the rounding of each other than are held: the best of what is left, one after another
+    Candidate last{~0ull, 0};
+    for (int o = 0; o < n; ++o) {
+        Candidate c{0, ~0ull};
+        for (int i = tid; i < all; i += kJoinThreads) {
+            const int p = s.parts[i >> slots_log2];
+            if ((i & mask) >= (p & 0xFFFF)) continue;
+            const Candidate x = candidate(s, row0, p >> 16, mine[i]);
+            if (better(last, x) && better(x, c)) c = x;
+        }
+        if (tid < a.beams && s.state[tid] == kFinished) {
+            const Candidate x = finished_candidate(a, s, row0, tid);
+            if (better(last, x) && better(x, c)) c = x;
         }
 #pragma unroll
-        for (int s = 16; s; s >>= 1) {
-            const Candidate c{__shfl_xor_sync(0xffffffffu, best.score, s), __shfl_xor_sync(0xffffffffu, best.id, s)};
-            if (better(c, best)) best = c;
+        for (int h = 16; h; h >>= 1) {
+            const Candidate x{__shfl_xor_sync(0xffffffffu, c.score, h), __shfl_xor_sync(0xffffffffu, c.id, h)};
+            if (better(x, c)) c = x;
         }
-        if ((tid & 31) == 0) warps[tid >> 5] = best;
+        if (lane == 0) s.warps[warp] = c;
         __syncthreads();
-        best = warps[0];
-        for (int w = 1; w < kJoinThreads / 32; ++w)
-            if (better(warps[w], best)) best = warps[w];
+        c = s.warps[0];
+        for (int w = 1; w < kJoinWarps; ++w)
+            if (better(s.warps[w], c)) c = s.warps[w];
         __syncthreads();
-        last = best;
-        if (tid == 0) {
-            const int64_t at = static_cast<int64_t>(lane) * a.n_out + o;
-            const bool some = best.id != ~0ull;
-            const int row = some ? static_cast<int>(best.id >> 24) : row0;
-            const int token = some ? static_cast<int>(best.id & 0xFFFFFFu) : a.pad;
-            a.out_scores[at] = static_cast<float>(best.score);
-            a.out_tokens[at] = token;
-            a.out_parents[at] = row;
-            if (a.out_finished) a.out_finished[at] = some && (state[row - row0] == kFinished || token == a.eos);
-        }
+        last = c;
+        if (tid == 0) write_out(a, s, row0, o, c);
     }
 }
 
-// How a call's rows are cut: parts of whole block tiles.
+// How a call's rows are cut: parts of whole tiles, and the tokens that each may
+// hand on.
 struct Cut {
+    int unroll;
     int parts;
     int span;
+    int slots_log2;
 };
 
-Cut cut_rows(int lanes, int beams, int vocab)
+Cut cut_rows(int lanes, int beams, int vocab, int n_out)
 {
-    const int tile = kScanWarps * kTile, rows = lanes * beams > 0 ? lanes * beams : 1;
-    const int most = (vocab + tile - 1) / tile, want = (4 * sm_count(-1) + rows - 1) / rows;
+    const int rows = lanes * beams > 0 ? lanes * beams : 1, sms = sm_count(-1);
+    const int64_t values = static_cast<int64_t>(rows) * vocab;
     Cut c;
+    c.unroll = values <= static_cast<int64_t>(sms) * 2 * 4096 ? 1 : values <= static_cast<int64_t>(sms) * 4 * 8192 ? 2 : 4;
+    const int tile = kScanThreads * kVec * c.unroll;
+    const int most = (vocab + tile - 1) / tile, want = min((4 * sms + rows - 1) / rows, kPairs / beams);
     c.span = ((most + min(most, want) - 1) / min(most, want)) * tile;
     c.parts = (vocab + c.span - 1) / c.span;
+    c.slots_log2 = n_out <= 8 ? 5 : n_out <= 24 ? 6 : n_out <= 48 ? 7 : 8;
     return c;
 }
 
 size_t sums_bytes(int lanes, int beams, int parts)
 {
-    return (static_cast<size_t>(lanes) * beams * parts * sizeof(float2) + 255) / 256 * 256;
+    return (static_cast<size_t>(lanes) * beams * parts * sizeof(PartSum) + 255) / 256 * 256;
 }
 
 }  // namespace
 
 size_t beam_select_workspace_bytes(int lanes, int beams, int vocab, int n_out)
 {
-    const Cut c = cut_rows(lanes, beams, vocab);
-    return sums_bytes(lanes, beams, c.parts) + static_cast<size_t>(lanes) * beams * c.parts * n_out * sizeof(uint64_t) + 256;
+    const Cut c = cut_rows(lanes, beams, vocab, n_out);
+    return sums_bytes(lanes, beams, c.parts) + (static_cast<size_t>(lanes) * beams * c.parts << c.slots_log2) * sizeof(uint64_t) + 256;
 }
 
 qg_status launch_beam_select(const BeamArgs& in, void* workspace, cudaStream_t stream)
@@ -363,15 +564,17 @@ qg_status launch_beam_select(const BeamArgs& in, void* workspace, cudaStream_t s
     BeamArgs a = in;
     a.status = device_status_ptr();
     if (!a.status) return QG_ERR_CUDA;
-    const Cut c = cut_rows(a.lanes, a.beams, a.vocab);
-    float2* sums = static_cast<float2*>(workspace);
+    const Cut c = cut_rows(a.lanes, a.beams, a.vocab, a.n_out);
+    PartSum* sums = static_cast<PartSum*>(workspace);
     uint64_t* keys = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(workspace) + sums_bytes(a.lanes, a.beams, c.parts));
-    auto scan = a.f32 ? beam_scan_kernel<true> : beam_scan_kernel<false>;
+    auto pick = [&](auto u1, auto u2, auto u4) { return c.unroll == 1 ? u1 : c.unroll == 2 ? u2 : u4; };
+    auto scan = a.f32 ? pick(beam_scan_kernel<true, 1>, beam_scan_kernel<true, 2>, beam_scan_kernel<true, 4>)
+                      : pick(beam_scan_kernel<false, 1>, beam_scan_kernel<false, 2>, beam_scan_kernel<false, 4>);
     cudaError_t e = launch_pdl(scan, dim3(static_cast<unsigned>(a.lanes * a.beams * c.parts)), dim3(kScanThreads), 0, stream,
-                               a, c.parts, c.span, sums, keys);
+                               a, c.parts, c.span, 1 << c.slots_log2, sums, keys);
     if (e == cudaSuccess)
         e = launch_pdl(beam_join_kernel, dim3(static_cast<unsigned>(a.lanes)), dim3(kJoinThreads), 0, stream, a, c.parts,
-                       static_cast<const float2*>(sums), static_cast<const uint64_t*>(keys));
+                       c.slots_log2, static_cast<const PartSum*>(sums), static_cast<const uint64_t*>(keys));
     return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 
