@@ -14,8 +14,9 @@ namespace {
 constexpr int kScanWarps = 8, kScanThreads = 32 * kScanWarps;
 constexpr int kVec = 8;                              // values a thread takes at a time
 constexpr int kList = 1024;                          // tokens a block can hold
-constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
-constexpr int kGroups = kJoinThreads / 4;            // candidates' groups, by whose best one is bounded
+constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinKeys = 8;                         // candidates a thread of the join takes at a time
+constexpr int kGroups = 128;                         // candidates' groups, by whose best one is bounded
 constexpr int kPairs = 1024;                         // parts of a lane's rows, at most
 constexpr int kPicked = 512;                         // candidates of a lane that are looked at in 64 bits
 constexpr float kLowest = -3.402823466e38f;
@@ -111,19 +112,21 @@ __device__ __forceinline__ void load8(const uint8_t* row, int vocab, int e, floa
     }
 }
 
-// The n-th largest of the warp's values, n <= 32: all sorted, greatest first.
+__device__ __forceinline__ float warp_max(float v)
+{
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// The n-th largest of the warp's values, n <= 32.
 __device__ __forceinline__ float nth_of_warp(float v, int n)
 {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-        for (int step = size / 2; step; step >>= 1) {
-            const float o = __shfl_xor_sync(0xffffffffu, v, step);
-            const bool greater_first = (lane & size) == 0 || size == 32;
-            v = ((lane & step) == 0) == greater_first ? fmaxf(v, o) : fminf(v, o);
-        }
-    return __shfl_sync(0xffffffffu, v, n - 1);
+    for (;;) {
+        const float most = warp_max(v);
+        if (--n == 0) return most;
+        if (__ffs(__ballot_sync(0xffffffffu, v == most)) - 1 == static_cast<int>(threadIdx.x & 31)) v = -INFINITY;
+    }
 }
 
 // A part of a row: the maximum and the scaled sum of its exponentials, and how
@@ -185,7 +188,7 @@ __device__ __forceinline__ void keep_best(ScanSmem& s, int k, int n)
 // tokens reach it (about n H(w) of independent ones for m = 1), and the list
 // that these fill is cut to its n best when it is long, which raises the bound.
 template <bool F32, int U>
-__global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_constant__ BeamArgs a, int parts, int span, int slots,
+__global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const __grid_constant__ BeamArgs a, int parts, int span, int slots,
                                                                  PartSum* sums, uint64_t* out)
 {
     __shared__ ScanSmem s;
@@ -206,11 +209,14 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
         float v[U][kVec];
 #pragma unroll
         for (int u = 0; u < U; ++u) load8<F32>(row, a.vocab, base + (u * kScanThreads + tid) * kVec, v[u]);
-        float most = -INFINITY;
+        float tops[U], most = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            tops[u] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) most = fmaxf(most, v[u][i]);
+            for (int i = 0; i < kVec; ++i) tops[u] = fmaxf(tops[u], v[u][i]);
+            most = fmaxf(most, tops[u]);
+        }
         if (most > top) {
             sum *= ex2((top - most) * kLog2e);
             top = most;
@@ -239,6 +245,7 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
             if (__any_sync(0xffffffffu, most >= least)) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
+                    if (U > 1 && !__any_sync(0xffffffffu, tops[u] >= least)) continue;
                     uint32_t hits = 0;
 #pragma unroll
                     for (int i = 0; i < kVec; ++i) hits |= static_cast<uint32_t>(v[u][i] >= least) << i;
@@ -283,14 +290,11 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
         }
     }
     // the warp's sum, then the block's, in a fixed order
+    const float warp_top = warp_max(top);
+    sum *= ex2((top - warp_top) * kLog2e);
+    top = warp_top;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const float t = __shfl_xor_sync(0xffffffffu, top, o), x = __shfl_xor_sync(0xffffffffu, sum, o);
-        const float m = fmaxf(top, t);
-        // rounded products, so that two lanes that swap get the same
-        sum = __fadd_rn(__fmul_rn(sum, ex2((top - m) * kLog2e)), __fmul_rn(x, ex2((t - m) * kLog2e)));
-        top = m;
-    }
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) s.sums[warp] = make_float2(top, sum);
     __syncthreads();
     int k = s.count;
@@ -335,22 +339,44 @@ __device__ __forceinline__ double value64(uint64_t o)
 enum RowState { kNone, kGoesOn, kFinished };
 
 struct JoinSmem {
-    double score[64];
     double z[64];                // ln of the row's sum
+    float score[64];
     float base[64];              // score - z, rounded
     int state[64];
     int parts[kPairs];           // handed-on tokens of a part, and its beam from bit 16 on
-    float best[kGroups];
+    float4 best[kGroups / 4];
+    uint64_t keys[kPicked];
+    int beams[kPicked];          // of the keys picked; -1 - beam: its finished row's one candidate
     Candidate picked[kPicked];
     Candidate warps[kJoinWarps];
     float bound;
     int count;
 };
 
+// ln x of a normal x >= 1, within 6e-8: with x = 2^k m, m in [sqrt(1/2),
+// sqrt(2)), and t = (m - 1) / (m + 1), ln m = 2 (t + t^3/3 + t^5/5 + ...), |t| <
+// 0.172; six terms leave less than 1e-10, t is off by 2^-23 of it.
+__device__ __forceinline__ float split_log(float x, int& k)
+{
+    const uint32_t b = __float_as_uint(x);
+    k = static_cast<int>((b - 0x3F3504F3u) >> 23);
+    const float m = __uint_as_float(b - (static_cast<uint32_t>(k) << 23));
+    const float d = m + 1.f;
+    float t = __fdividef(m - 1.f, d);
+    t = fmaf(fmaf(-t, d, m - 1.f), 0.5f, t);             // what the quotient misses, over a rough d
+    const float q = t * t;
+    float p = 1.f / 11.f;
+    p = fmaf(p, q, 1.f / 9.f);
+    p = fmaf(p, q, 1.f / 7.f);
+    p = fmaf(p, q, 1.f / 5.f);
+    p = fmaf(p, q, 1.f / 3.f);
+    return fmaf(p * q, 2.f * t, 2.f * t);
+}
+
 // Candidate `i` of a beam's part from its key, in 64 bits.
 __device__ __forceinline__ Candidate candidate(const JoinSmem& s, int row0, int beam, uint64_t key)
 {
-    return Candidate{ordered64(s.score[beam] + (static_cast<double>(key_value(key)) - s.z[beam])),
+    return Candidate{ordered64(static_cast<double>(s.score[beam]) + (static_cast<double>(key_value(key)) - s.z[beam])),
                      static_cast<uint64_t>(row0 + beam) << 24 | key_token(key)};
 }
 
@@ -383,36 +409,46 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
     pdl_enter();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.n_out;
     const int row0 = static_cast<int>(blockIdx.x) * a.beams;
+    const int all = a.beams * parts << slots_log2, mask = (1 << slots_log2) - 1;
+    const uint64_t* mine = keys + (static_cast<int64_t>(row0) * parts << slots_log2);
+    // the first keys are on their way while the sums are joined; whether they are any is known then
+    uint64_t key[kJoinKeys];
+#pragma unroll
+    for (int r = 0; r < kJoinKeys; ++r) {
+        const int i = r * kJoinThreads + tid;
+        key[r] = i < all ? mine[i] : 0;
+    }
     for (int beam = warp; beam < a.beams; beam += kJoinWarps) {
         const int row = row0 + beam;
         const float score = a.scores[row];
-        const bool number = score > -INFINITY && score < INFINITY;
         const bool done = a.finished && a.finished[row];
         int state = kNone;
         double z = 0.0;
-        if (!number) {
+        if (!(score > -INFINITY && score < INFINITY)) {
             if (lane == 0 && score != -INFINITY) set_device_status(a.status, QG_ERR_INVALID_ARG);
         } else if (done) {
             state = kFinished;
         } else {
             const PartSum* p = sums + static_cast<int64_t>(row) * parts;
-            float top = kLowest;
-            for (int i = lane; i < parts; i += 32) top = fmaxf(top, p[i].top);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            double sum = 0.0;
+            float top = kLowest, sum = 0.f;
             for (int i = lane; i < parts; i += 32) {
                 const PartSum x = p[i];
-                sum += static_cast<double>(x.sum) * expf(x.top - top);
                 s.parts[beam * parts + i] = x.count | beam << 16;
+                const float m = fmaxf(top, x.top);
+                sum = sum * ex2((top - m) * kLog2e) + x.sum * ex2((x.top - m) * kLog2e);
+                top = m;
             }
+            const float most = warp_max(top);
+            sum *= ex2((top - most) * kLog2e);
 #pragma unroll
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (!(sum >= 0.0 && sum < INFINITY)) {
+            if (!(sum >= 0.f && sum < INFINITY)) {
                 if (lane == 0) set_device_status(a.status, QG_ERR_INVALID_ARG);
-            } else if (sum > 0.0) {
+            } else if (sum > 0.f) {
+                int k;
+                const float l = split_log(sum, k);
                 state = kGoesOn;
-                z = top + log(sum);
+                z = fma(static_cast<double>(k), 0.69314718055994531, static_cast<double>(most)) + l;
             }
         }
         if (state != kGoesOn)
@@ -430,67 +466,73 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
     }
     __syncthreads();
 
-    const int all = a.beams * parts << slots_log2, mask = (1 << slots_log2) - 1;
-    const uint64_t* mine = keys + (static_cast<int64_t>(row0) * parts << slots_log2);
     const float kOff = 4.76837158e-7f;                  // 2^-21
     float best = -INFINITY;
-    for (int i = tid; i < all; i += kJoinThreads) {
-        const int p = s.parts[i >> slots_log2];
-        if ((i & mask) >= (p & 0xFFFF)) continue;
-        const float x = key_value(mine[i]), base = s.base[p >> 16];
-        best = fmaxf(best, base + x - kOff * (fabsf(base) + fabsf(x)));
+    for (int i0 = 0; i0 < all; i0 += kJoinKeys * kJoinThreads) {
+#pragma unroll
+        for (int r = 0; r < kJoinKeys; ++r) {
+            const int i = i0 + r * kJoinThreads + tid;
+            if (i0 && i < all) key[r] = mine[i];
+            if (i >= all) continue;
+            const int p = s.parts[i >> slots_log2];
+            const float x = key_value(key[r]), base = s.base[p >> 16];
+            if ((i & mask) < (p & 0xFFFF)) best = fmaxf(best, base + x - kOff * (fabsf(base) + fabsf(x)));
+        }
     }
-    if (tid < a.beams && s.state[tid] == kFinished) best = fmaxf(best, static_cast<float>(s.score[tid]));
-    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
-    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
-    if ((lane & 3) == 0) s.best[tid / 4] = best;
+    if (tid < a.beams && s.state[tid] == kFinished) best = fmaxf(best, s.score[tid]);
+#pragma unroll
+    for (int o = 1; o < kJoinThreads / kGroups; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+    float* bests = reinterpret_cast<float*>(s.best);
+    if (tid % (kJoinThreads / kGroups) == 0) bests[tid / (kJoinThreads / kGroups)] = best;
     __syncthreads();
     if (tid < kGroups) {
-        const float x = s.best[tid];
+        const float x = bests[tid];
         int place = 0;
-#pragma unroll 8
-        for (int j = 0; j < kGroups; ++j) {
-            const float y = s.best[j];
-            place += y > x || (y == x && j < tid);
+#pragma unroll 4
+        for (int j = 0; j < kGroups / 4; ++j) {
+            const float4 y = s.best[j];
+            place += (y.x > x || (y.x == x && 4 * j < tid)) + (y.y > x || (y.y == x && 4 * j + 1 < tid)) +
+                     (y.z > x || (y.z == x && 4 * j + 2 < tid)) + (y.w > x || (y.w == x && 4 * j + 3 < tid));
         }
         if (place == n - 1) s.bound = x;
     }
     __syncthreads();
     const float bound = s.bound;
-    for (int i0 = 0; i0 < all; i0 += kJoinThreads) {
-        const int i = i0 + tid;
-        bool take = false;
-        uint64_t key = 0;
-        int beam = 0;
-        if (i < all) {
-            const int p = s.parts[i >> slots_log2];
-            beam = p >> 16;
-            if ((i & mask) < (p & 0xFFFF)) {
-                key = mine[i];
-                const float x = key_value(key), base = s.base[beam];
-                take = !(base + x + kOff * (fabsf(base) + fabsf(x)) < bound);
-            }
-        }
-        if (take) {
-            const int at = atomicAdd(&s.count, 1);
-            if (at < kPicked) s.picked[at] = candidate(s, row0, beam, key);
-        }
-    }
-    if (tid < a.beams && s.state[tid] == kFinished && s.score[tid] >= bound) {
+    auto pick = [&](uint64_t k, int beam) {
         const int at = atomicAdd(&s.count, 1);
-        if (at < kPicked) s.picked[at] = finished_candidate(a, s, row0, tid);
+        if (at < kPicked) {
+            s.keys[at] = k;
+            s.beams[at] = beam;
+        }
+    };
+    for (int i0 = 0; i0 < all; i0 += kJoinKeys * kJoinThreads) {
+#pragma unroll
+        for (int r = 0; r < kJoinKeys; ++r) {
+            const int i = i0 + r * kJoinThreads + tid;
+            if (all > kJoinKeys * kJoinThreads && i < all) key[r] = mine[i];
+            if (i >= all) continue;
+            const int p = s.parts[i >> slots_log2];
+            const float x = key_value(key[r]), base = s.base[p >> 16];
+            if ((i & mask) < (p & 0xFFFF) && !(base + x + kOff * (fabsf(base) + fabsf(x)) < bound)) pick(key[r], p >> 16);
+        }
     }
+    if (tid < a.beams && s.state[tid] == kFinished && s.score[tid] >= bound) pick(0, -1 - tid);
     __syncthreads();
     const int count = s.count;
     if (count <= kPicked) {
         // a candidate's place is the number of better ones
+        Candidate c{0, ~0ull};
         if (tid < count) {
-            const Candidate c = s.picked[tid];
-            int place = 0;
-            for (int j = 0; j < count; ++j) place += better(s.picked[j], c);
-            if (place < n) write_out(a, s, row0, place, c);
+            const int beam = s.beams[tid];
+            c = beam < 0 ? finished_candidate(a, s, row0, -1 - beam) : candidate(s, row0, beam, s.keys[tid]);
+            s.picked[tid] = c;
         }
-        for (int o = count + tid; o < n; o += kJoinThreads) write_out(a, s, row0, o, Candidate{0, ~0ull});
+        __syncthreads();
+        int place = 0;
+        if (tid < count)
+            for (int j = 0; j < count; ++j) place += better(s.picked[j], c);
+        if (tid >= count) place = tid;
+        if (place < n) write_out(a, s, row0, place, c);
         return;
     }
     // more candidates within the rounding of each other than are held: the best of what is left, one after another

@@ -637,11 +637,10 @@ QG_API qg_status kv_pages_copy(const qg_kv_cache* cache, const qg_kv_moves* move
  *               256-byte aligned; needs no initialisation, is scratch after
  *               the call, and may be shared by calls that do not overlap on
  *               the GPU
- * Sums of exponentials are held in fp32 within a part of a row and in 64 bits
- * across parts; scores are compared in 64 bits and rounded once (one below
- * fp32's range becomes -infinity). Rows with
- * equal logits get equal sums whatever their alignment, and the result does
- * not depend on the stream's other work (fixed order).
+ * Sums of exponentials are held in fp32; scores are compared in 64 bits and
+ * rounded once (one below fp32's range becomes -infinity). Rows with equal
+ * logits get equal sums whatever their alignment, and the result does not
+ * depend on the stream's other work (fixed order).
  */
 QG_API qg_status beam_select(const void* logits, qg_out logits_dtype, int64_t row_stride, int lanes, int beams,
                              int vocab, const float* scores, const uint8_t* finished, int eos, int pad, int n_out,
