@@ -1,23 +1,23 @@
 // beam.cu -- beam search's selection: the best continuations of a lane over
 // its beams and the vocabulary (beam_select).
 //
-// score(r, t) = scores[r] + logits[r][t] - ln sum_t' exp(logits[r][t']): the
-// order of a row's tokens is that of its logits, so one pass over a row gives
-// both its sum of exponentials (a running maximum and the sum scaled to it)
-// and its n_out best tokens; a lane's best are among those of its rows. Rows
-// are cut into parts, a block each; a second kernel joins the parts of a lane.
+// score(r, t) = scores[r] + logits[r][t] - ln sum_t' exp(logits[r][t']): a
+// row's sum is needed before its tokens can be compared with another row's, so
+// one kernel reads all logits and leaves, of every piece of 1,024, the maximum
+// and the sum of the exponentials scaled to it; a second joins a lane's sums.
+// The n_out best tokens lie in the n_out pieces whose maxima have the best
+// scores (a token of any other piece is worse than those maxima, or equal and
+// behind them), so it reads just these again.
 #include "kv_common.cuh"
 
 namespace qg {
 namespace {
 
-constexpr int kScanWarps = 8, kScanThreads = 32 * kScanWarps;
-constexpr int kVec = 8;                              // values a thread takes at a time
-constexpr int kList = 1024;                          // tokens a block can hold
-constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinKeys = 8;                         // candidates a thread of the join takes at a time
+constexpr int kPiece = 1024;                         // values, 32 of a lane
+constexpr int kScanWarps = 8;                        // of a block, at most
+constexpr int kUnit = 256;                           // values of a piece that a warp looks at again
 constexpr int kGroups = 128;                         // candidates' groups, by whose best one is bounded
-constexpr int kPairs = 1024;                         // parts of a lane's rows, at most
+constexpr int kPieces = 128;                         // pieces of a lane that are read again, if more than n_out
 constexpr int kPicked = 512;                         // candidates of a lane that are looked at in 64 bits
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -75,41 +75,60 @@ __device__ __forceinline__ void shift_words(uint32_t (&w)[N], int skip)
     }
 }
 
-// Values e .. e + 7 of a row of `vocab`, -infinity behind its end. The same
-// values go to the same thread whatever the row's alignment; a row that does
-// not start at 16 bytes is read in the aligned pieces around it, but for the
-// last values, which are read one by one. (Plain loads: the kernel before may
-// have written them while this one had started already.)
+// 16 bytes of a row of `vocab` values, those from `e` on, -infinity behind its
+// end. The same values go to the same lane whatever the row's alignment; a row
+// that does not start at 16 bytes is read in the aligned pieces around it, but
+// for the last values, which are read one by one. (Plain loads: the kernel
+// before may have written them while this one had started already.)
 template <bool F32>
-__device__ __forceinline__ void load8(const uint8_t* row, int vocab, int e, float (&v)[kVec])
+__device__ __forceinline__ void load16(const uint8_t* row, int skip, int vocab, int e, float* v)
 {
-    constexpr int kSize = F32 ? 4 : 2, kPieces = F32 ? 2 : 1;
-    const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+    constexpr int kSize = F32 ? 4 : 2, kN = 16 / kSize;
     const uint8_t* at = row + static_cast<int64_t>(e) * kSize;
-    if (e + kVec + (skip ? 16 / kSize : 0) <= vocab) {
-        uint32_t w[4 * (kPieces + 1)];
+    if (e + kN + (skip ? kN : 0) <= vocab) {
+        uint32_t w[8];
+        const uint4 x = *reinterpret_cast<const uint4*>(at - skip);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        if (skip) {
+            const uint4 y = *reinterpret_cast<const uint4*>(at - skip + 16);
+            w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+            shift_words(w, skip);
+        }
 #pragma unroll
-        for (int i = 0; i <= kPieces; ++i)
-            if (i < kPieces || skip) {
-                const uint4 x = *reinterpret_cast<const uint4*>(at - skip + 16 * i);
-                w[4 * i] = x.x;
-                w[4 * i + 1] = x.y;
-                w[4 * i + 2] = x.z;
-                w[4 * i + 3] = x.w;
-            }
-        if (skip) shift_words(w, skip);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
+        for (int i = 0; i < kN; ++i)
             v[i] = F32 ? __uint_as_float(w[i]) : __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
     } else {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
+        for (int i = 0; i < kN; ++i) {
             v[i] = -INFINITY;
             if (e + i < vocab)
                 v[i] = F32 ? reinterpret_cast<const float*>(at)[i]
                            : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(at)[i]);
         }
     }
+}
+
+// N values of each lane from `base` on.
+template <bool F32, int N>
+__device__ __forceinline__ void load_values(const uint8_t* row, int vocab, int base, float (&v)[N])
+{
+    constexpr int kN = F32 ? 4 : 8;
+    const int lane = threadIdx.x & 31, skip = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+    if (skip == 0 && base + 32 * N <= vocab) {         // the usual case, without its tests
+#pragma unroll
+        for (int u = 0; u < N / kN; ++u) load16<F32>(row, 0, INT32_MAX, base + (u * 32 + lane) * kN, v + u * kN);
+    } else {
+#pragma unroll
+        for (int u = 0; u < N / kN; ++u) load16<F32>(row, skip, vocab, base + (u * 32 + lane) * kN, v + u * kN);
+    }
+}
+
+// Which token the i-th of these values is.
+template <bool F32>
+__device__ __forceinline__ int token_of(int base, int i)
+{
+    constexpr int kN = F32 ? 4 : 8;
+    return base + (i / kN * 32 + static_cast<int>(threadIdx.x & 31)) * kN + i % kN;
 }
 
 __device__ __forceinline__ float warp_max(float v)
@@ -119,198 +138,76 @@ __device__ __forceinline__ float warp_max(float v)
     return r;
 }
 
-// The n-th largest of the warp's values, n <= 32.
-__device__ __forceinline__ float nth_of_warp(float v, int n)
-{
-    for (;;) {
-        const float most = warp_max(v);
-        if (--n == 0) return most;
-        if (__ffs(__ballot_sync(0xffffffffu, v == most)) - 1 == static_cast<int>(threadIdx.x & 31)) v = -INFINITY;
-    }
-}
-
-// A part of a row: the maximum and the scaled sum of its exponentials, and how
-// many of its tokens are handed on.
-struct PartSum {
+// Of some of a row's logits: the maximum and the sum of the exponentials,
+// scaled to it.
+struct ScaledSum {
     float top;
     float sum;
-    int count;
-    int pad;
 };
 
-// A block's tokens that may be among its n best: those above `bound`, a key
-// that n of the block's tokens reach.
-struct ScanSmem {
-    uint64_t list[kList];
-    uint64_t bound;
-    int count;
-    float tops[kScanWarps];
-    float2 sums[kScanWarps];
-};
-
-// Keep the n best of the first k keys, in order: a key's place is the number
-// of greater ones.
-__device__ __forceinline__ void keep_best(ScanSmem& s, int k, int n)
+__device__ __forceinline__ void join_sums(ScaledSum& x, float top, float sum)
 {
-    constexpr int kMine = kList / kScanThreads;
-    uint64_t mine[kMine];
-    int place[kMine];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-        const int at = threadIdx.x + i * kScanThreads;
-        mine[i] = at < k ? s.list[at] : 0;
-        place[i] = 0;
-    }
-    if (k <= kScanThreads) {
-        for (int j = 0; j < k; ++j) place[0] += s.list[j] > mine[0];
-    } else {
-        for (int j = 0; j < k; ++j) {
-            const uint64_t x = s.list[j];
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) place[i] += x > mine[i];
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMine; ++i)
-        if (mine[i] && place[i] < n) {
-            s.list[place[i]] = mine[i];
-            if (place[i] == n - 1) s.bound = mine[i];
-        }
-    if (threadIdx.x == 0) s.count = min(k, n);
-    __syncthreads();
+    const float m = fmaxf(x.top, top);
+    x.sum = x.sum * ex2((x.top - m) * kLog2e) + sum * ex2((top - m) * kLog2e);
+    x.top = m;
 }
 
-// A block takes a part of a row, U * 8 values per thread at a time. Its bound
-// starts from the first of these: the m-th largest of a warp's threads'
-// maxima, the least over w warps, with m w >= n, is reached by n tokens. Few
-// tokens reach it (about n H(w) of independent ones for m = 1), and the list
-// that these fill is cut to its n best when it is long, which raises the bound.
-template <bool F32, int U>
-__global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const __grid_constant__ BeamArgs a, int parts, int span, int slots,
-                                                                 PartSum* sums, uint64_t* out)
+// Over the warp, in a fixed order.
+__device__ __forceinline__ void warp_sum(ScaledSum& x)
 {
-    __shared__ ScanSmem s;
-    constexpr int kTile = kScanThreads * kVec * U;
+    const float top = warp_max(x.top);
+    x.sum *= ex2((x.top - top) * kLog2e);
+    x.top = top;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x.sum += __shfl_xor_sync(0xffffffffu, x.sum, o);
+}
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+// sum of 2^((v - top) log2 e), two values an instruction but for 2^x.
+template <int N>
+__device__ __forceinline__ float exp_sum(const float (&v)[N], float top)
+{
+    const uint64_t off = pair(-top, -top), scale = pair(kLog2e, kLog2e);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        uint64_t x;
+        float lo, hi;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(pair(v[i], v[i + 1])), "l"(off));
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(x), "l"(scale));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(sum) : "l"(sum), "l"(pair(ex2(lo), ex2(hi))));
+    }
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(sum));
+    return lo + hi;
+}
+
+// A warp per piece. Nothing is kept from one to the next, and blocks need no
+// order: as many loads are on their way as registers hold.
+template <bool F32>
+__global__ void __launch_bounds__(32 * kScanWarps, 4) beam_scan_kernel(const __grid_constant__ BeamArgs a, int pieces, ScaledSum* sums)
+{
     pdl_enter();
-    const int row_i = blockIdx.x / parts, part = blockIdx.x % parts;
-    if (!row_live(a, row_i)) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.n_out;
-    const uint8_t* row = static_cast<const uint8_t*>(a.logits) + row_i * a.stride * (F32 ? 4 : 2);
-    const int begin = part * span, end = min(begin + span, a.vocab);
-    if (tid == 0) {
-        s.count = 0;
-        s.bound = make_key(-INFINITY, 0);
-    }
-    uint64_t bound = make_key(-INFINITY, 0);
-    float top = kLowest, sum = 0.f;
-    for (int base = begin; base < end; base += kTile) {
-        float v[U][kVec];
+    const int at = static_cast<int>(blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32);
+    const int row = at / pieces;
+    if (row >= a.lanes * a.beams || !row_live(a, row)) return;
+    float v[kPiece / 32];
+    load_values<F32>(static_cast<const uint8_t*>(a.logits) + row * a.stride * (F32 ? 4 : 2), a.vocab, at % pieces * kPiece, v);
+    float top = kLowest;
 #pragma unroll
-        for (int u = 0; u < U; ++u) load8<F32>(row, a.vocab, base + (u * kScanThreads + tid) * kVec, v[u]);
-        float tops[U], most = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            tops[u] = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) tops[u] = fmaxf(tops[u], v[u][i]);
-            most = fmaxf(most, tops[u]);
-        }
-        if (most > top) {
-            sum *= ex2((top - most) * kLog2e);
-            top = most;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) sum += ex2((v[u][i] - top) * kLog2e);
-        if (base == begin) {
-            const int warps = max(1, min(kScanWarps, (end - begin) / (32 * kVec)));    // whose threads all have values
-            const int m = (n + warps - 1) / warps;
-            if (m <= 32) {
-                const float t = nth_of_warp(most, m);
-                if (lane == 0) s.tops[warp] = t;
-                __syncthreads();
-                float least = s.tops[0];
-                for (int w = 1; w < warps; ++w) least = fminf(least, s.tops[w]);
-                if (least > -INFINITY) bound = make_key(least, 0xFFFFFFFFu) - 1;
-            } else {
-                __syncthreads();
-            }
-        }
-        for (;;) {
-            const float least = key_value(bound);
-            int seen = 0;
-            if (__any_sync(0xffffffffu, most >= least)) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (U > 1 && !__any_sync(0xffffffffu, tops[u] >= least)) continue;
-                    uint32_t hits = 0;
-#pragma unroll
-                    for (int i = 0; i < kVec; ++i) hits |= static_cast<uint32_t>(v[u][i] >= least) << i;
-                    while (__any_sync(0xffffffffu, hits != 0)) {
-                        const int at = __ffs(hits) - 1;
-                        float x = v[u][0];
-#pragma unroll
-                        for (int i = 1; i < kVec; ++i) x = i == at ? v[u][i] : x;
-                        const uint64_t key = make_key(x, static_cast<uint32_t>(base + (u * kScanThreads + tid) * kVec + at));
-                        const uint32_t with = __ballot_sync(0xffffffffu, hits && key > bound);
-                        int place = 0;
-                        if (lane == 0 && with) place = atomicAdd(&s.count, __popc(with));
-                        place = __shfl_sync(0xffffffffu, place, 0);
-                        seen = max(seen, place + __popc(with));
-                        place += __popc(with & ((1u << lane) - 1u));
-                        if ((with >> lane & 1u) && place < kList) s.list[place] = key;
-                        hits &= hits - 1;
-                    }
-                }
-            }
-            if (!__syncthreads_or(seen > 2 * slots)) break;
-            // a long list: cut, which raises the bound
-            const int k = s.count;
-            keep_best(s, min(k, kList), n);
-            bound = s.bound;
-            if (k <= kList) break;
-            // some found no place: those of this tile are taken again, above the new bound (each turn at least
-            // kList - n fewer)
-            __syncthreads();
-            if (warp == 0) {
-                const uint64_t k0 = lane < n ? s.list[lane] : 0, k1 = lane + 32 < n ? s.list[lane + 32] : 0;
-                const bool old0 = k0 && key_token(k0) < static_cast<uint32_t>(base);
-                const bool old1 = k1 && key_token(k1) < static_cast<uint32_t>(base);
-                const uint32_t b0 = __ballot_sync(0xffffffffu, old0), b1 = __ballot_sync(0xffffffffu, old1);
-                __syncwarp();
-                if (old0) s.list[__popc(b0 & ((1u << lane) - 1u))] = k0;
-                if (old1) s.list[__popc(b0) + __popc(b1 & ((1u << lane) - 1u))] = k1;
-                if (lane == 0) s.count = __popc(b0) + __popc(b1);
-            }
-            bound -= 1;
-            __syncthreads();
-        }
-    }
-    // the warp's sum, then the block's, in a fixed order
-    const float warp_top = warp_max(top);
-    sum *= ex2((top - warp_top) * kLog2e);
-    top = warp_top;
+    for (int i = 0; i < kPiece / 32; ++i) top = fmaxf(top, v[i]);
+    top = warp_max(top);
+    float sum = exp_sum(v, top);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s.sums[warp] = make_float2(top, sum);
-    __syncthreads();
-    int k = s.count;
-    if (k > slots) {
-        keep_best(s, k, n);
-        k = n;
-    }
-    if (tid == 0) {
-        float m = kLowest, x = 0.f;
-#pragma unroll
-        for (int w = 0; w < kScanWarps; ++w) m = fmaxf(m, s.sums[w].x);
-#pragma unroll
-        for (int w = 0; w < kScanWarps; ++w) x += s.sums[w].y * ex2((s.sums[w].x - m) * kLog2e);
-        sums[blockIdx.x] = PartSum{m, x, k, 0};
-    }
-    for (int i = tid; i < k; i += kScanThreads) out[static_cast<int64_t>(blockIdx.x) * slots + i] = s.list[i];
+    if ((threadIdx.x & 31) == 0) sums[at] = ScaledSum{top, sum};
 }
 
 // A candidate of a lane: its score as a whole number of the same order, and
@@ -338,18 +235,21 @@ __device__ __forceinline__ double value64(uint64_t o)
 
 enum RowState { kNone, kGoesOn, kFinished };
 
+template <int kThreads>
 struct JoinSmem {
     double z[64];                // ln of the row's sum
     float score[64];
     float base[64];              // score - z, rounded
     int state[64];
-    int parts[kPairs];           // handed-on tokens of a part, and its beam from bit 16 on
     float4 best[kGroups / 4];
+    float mine[kThreads];
+    int pieces[kPieces];
     uint64_t keys[kPicked];
     int beams[kPicked];          // of the keys picked; -1 - beam: its finished row's one candidate
     Candidate picked[kPicked];
-    Candidate warps[kJoinWarps];
+    Candidate warps[kThreads / 32];
     float bound;
+    int n_pieces;
     int count;
 };
 
@@ -373,55 +273,24 @@ __device__ __forceinline__ float split_log(float x, int& k)
     return fmaf(p * q, 2.f * t, 2.f * t);
 }
 
-// Candidate `i` of a beam's part from its key, in 64 bits.
-__device__ __forceinline__ Candidate candidate(const JoinSmem& s, int row0, int beam, uint64_t key)
-{
-    return Candidate{ordered64(static_cast<double>(s.score[beam]) + (static_cast<double>(key_value(key)) - s.z[beam])),
-                     static_cast<uint64_t>(row0 + beam) << 24 | key_token(key)};
-}
-
-__device__ __forceinline__ Candidate finished_candidate(const BeamArgs& a, const JoinSmem& s, int row0, int beam)
-{
-    return Candidate{ordered64(s.score[beam]), static_cast<uint64_t>(row0 + beam) << 24 | static_cast<uint32_t>(a.pad)};
-}
-
-__device__ __forceinline__ void write_out(const BeamArgs& a, const JoinSmem& s, int row0, int place, const Candidate& c)
-{
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * a.n_out + place;
-    const bool some = c.id != ~0ull;
-    const int row = some ? static_cast<int>(c.id >> 24) : row0;
-    const int token = some ? static_cast<int>(c.id & 0xFFFFFFu) : a.pad;
-    a.out_scores[at] = some ? static_cast<float>(value64(c.score)) : -INFINITY;
-    a.out_tokens[at] = token;
-    a.out_parents[at] = row;
-    if (a.out_finished) a.out_finished[at] = some && (s.state[row - row0] == kFinished || token == a.eos);
-}
-
 // A block per lane. A candidate's score in 32 bits, f, is off by less than e =
 // 2^-21 (|score - z| + |logit|): score - z is rounded once and the sum with the
 // logit once, 2^-24 of each. The n-th largest of the groups' best f - e is
 // reached by n candidates, so only those with f + e at or above it are looked
 // at in 64 bits (which this GPU adds and compares slowly).
-__global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_constant__ BeamArgs a, int parts, int slots_log2,
-                                                                 const PartSum* sums, const uint64_t* keys)
+template <bool F32, int kThreads>
+__global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_constant__ BeamArgs a, int pieces, const ScaledSum* sums)
 {
-    __shared__ JoinSmem s;
+    __shared__ JoinSmem<kThreads> s;
+    constexpr int kWarps = kThreads / 32;
+    constexpr float kOff = 4.76837158e-7f;             // 2^-21
     pdl_enter();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.n_out;
-    const int row0 = static_cast<int>(blockIdx.x) * a.beams;
-    const int all = a.beams * parts << slots_log2, mask = (1 << slots_log2) - 1;
-    const uint64_t* mine = keys + (static_cast<int64_t>(row0) * parts << slots_log2);
-    // the first keys are on their way while the sums are joined; whether they are any is known then
-    uint64_t key[kJoinKeys];
-#pragma unroll
-    for (int r = 0; r < kJoinKeys; ++r) {
-        const int i = r * kJoinThreads + tid;
-        key[r] = i < all ? mine[i] : 0;
-    }
-    for (int beam = warp; beam < a.beams; beam += kJoinWarps) {
-        const int row = row0 + beam;
-        const float score = a.scores[row];
-        const bool done = a.finished && a.finished[row];
+    const int row0 = static_cast<int>(blockIdx.x) * a.beams, all = a.beams * pieces;
+    const ScaledSum* mine = sums + static_cast<int64_t>(row0) * pieces;
+    for (int beam = warp; beam < a.beams; beam += kWarps) {
+        const float score = a.scores[row0 + beam];
+        const bool done = a.finished && a.finished[row0 + beam];
         int state = kNone;
         double z = 0.0;
         if (!(score > -INFINITY && score < INFINITY)) {
@@ -429,30 +298,21 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
         } else if (done) {
             state = kFinished;
         } else {
-            const PartSum* p = sums + static_cast<int64_t>(row) * parts;
-            float top = kLowest, sum = 0.f;
-            for (int i = lane; i < parts; i += 32) {
-                const PartSum x = p[i];
-                s.parts[beam * parts + i] = x.count | beam << 16;
-                const float m = fmaxf(top, x.top);
-                sum = sum * ex2((top - m) * kLog2e) + x.sum * ex2((x.top - m) * kLog2e);
-                top = m;
+            ScaledSum r{kLowest, 0.f};
+            for (int i = lane; i < pieces; i += 32) {
+                const ScaledSum x = mine[beam * pieces + i];
+                join_sums(r, x.top, x.sum);
             }
-            const float most = warp_max(top);
-            sum *= ex2((top - most) * kLog2e);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (!(sum >= 0.f && sum < INFINITY)) {
+            warp_sum(r);
+            if (!(r.sum >= 0.f && r.sum < INFINITY)) {
                 if (lane == 0) set_device_status(a.status, QG_ERR_INVALID_ARG);
-            } else if (sum > 0.f) {
+            } else if (r.sum > 0.f) {
                 int k;
-                const float l = split_log(sum, k);
+                const float l = split_log(r.sum, k);
                 state = kGoesOn;
-                z = fma(static_cast<double>(k), 0.69314718055994531, static_cast<double>(most)) + l;
+                z = fma(static_cast<double>(k), 0.69314718055994531, static_cast<double>(r.top)) + l;
             }
         }
-        if (state != kGoesOn)
-            for (int i = lane; i < parts; i += 32) s.parts[beam * parts + i] = beam << 16;
         if (lane == 0) {
             s.score[beam] = score;
             s.z[beam] = z;
@@ -460,95 +320,46 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
             s.state[beam] = state;
         }
     }
-    if (tid == 0) {
-        s.bound = -INFINITY;
-        s.count = 0;
-    }
+    if (tid == 0) s.n_pieces = s.count = 0;
     __syncthreads();
 
-    const float kOff = 4.76837158e-7f;                  // 2^-21
-    float best = -INFINITY;
-    for (int i0 = 0; i0 < all; i0 += kJoinKeys * kJoinThreads) {
-#pragma unroll
-        for (int r = 0; r < kJoinKeys; ++r) {
-            const int i = i0 + r * kJoinThreads + tid;
-            if (i0 && i < all) key[r] = mine[i];
-            if (i >= all) continue;
-            const int p = s.parts[i >> slots_log2];
-            const float x = key_value(key[r]), base = s.base[p >> 16];
-            if ((i & mask) < (p & 0xFFFF)) best = fmaxf(best, base + x - kOff * (fabsf(base) + fabsf(x)));
-        }
-    }
-    if (tid < a.beams && s.state[tid] == kFinished) best = fmaxf(best, s.score[tid]);
-#pragma unroll
-    for (int o = 1; o < kJoinThreads / kGroups; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-    float* bests = reinterpret_cast<float*>(s.best);
-    if (tid % (kJoinThreads / kGroups) == 0) bests[tid / (kJoinThreads / kGroups)] = best;
-    __syncthreads();
-    if (tid < kGroups) {
-        const float x = bests[tid];
-        int place = 0;
-#pragma unroll 4
-        for (int j = 0; j < kGroups / 4; ++j) {
-            const float4 y = s.best[j];
-            place += (y.x > x || (y.x == x && 4 * j < tid)) + (y.y > x || (y.y == x && 4 * j + 1 < tid)) +
-                     (y.z > x || (y.z == x && 4 * j + 2 < tid)) + (y.w > x || (y.w == x && 4 * j + 3 < tid));
-        }
-        if (place == n - 1) s.bound = x;
-    }
-    __syncthreads();
-    const float bound = s.bound;
-    auto pick = [&](uint64_t k, int beam) {
-        const int at = atomicAdd(&s.count, 1);
-        if (at < kPicked) {
-            s.keys[at] = k;
-            s.beams[at] = beam;
-        }
+    const bool finished = tid < a.beams && s.state[tid] == kFinished;
+    auto lower = [&](int beam, float x) { return s.base[beam] + x - kOff * (fabsf(s.base[beam]) + fabsf(x)); };
+    auto may_be = [&](int beam, float x, float bound) { return !(s.base[beam] + x + kOff * (fabsf(s.base[beam]) + fabsf(x)) < bound); };
+    auto exact = [&](int beam, float x, int which) {
+        return Candidate{ordered64(static_cast<double>(s.score[beam]) + (static_cast<double>(x) - s.z[beam])),
+                         static_cast<uint64_t>(row0 + beam) << 24 | static_cast<uint32_t>(which)};
     };
-    for (int i0 = 0; i0 < all; i0 += kJoinKeys * kJoinThreads) {
+    auto of_finished = [&](int beam) {
+        return Candidate{ordered64(s.score[beam]), static_cast<uint64_t>(row0 + beam) << 24 | static_cast<uint32_t>(a.pad)};
+    };
+    // the n-th largest of the groups' best; -infinity if there are not as many
+    auto nth_best = [&](float best) {
+        if (finished) best = fmaxf(best, s.score[tid]);
+        s.mine[tid] = best;
+        __syncthreads();
+        float* bests = reinterpret_cast<float*>(s.best);
+        if (tid < kGroups) {
 #pragma unroll
-        for (int r = 0; r < kJoinKeys; ++r) {
-            const int i = i0 + r * kJoinThreads + tid;
-            if (all > kJoinKeys * kJoinThreads && i < all) key[r] = mine[i];
-            if (i >= all) continue;
-            const int p = s.parts[i >> slots_log2];
-            const float x = key_value(key[r]), base = s.base[p >> 16];
-            if ((i & mask) < (p & 0xFFFF) && !(base + x + kOff * (fabsf(base) + fabsf(x)) < bound)) pick(key[r], p >> 16);
-        }
-    }
-    if (tid < a.beams && s.state[tid] == kFinished && s.score[tid] >= bound) pick(0, -1 - tid);
-    __syncthreads();
-    const int count = s.count;
-    if (count <= kPicked) {
-        // a candidate's place is the number of better ones
-        Candidate c{0, ~0ull};
-        if (tid < count) {
-            const int beam = s.beams[tid];
-            c = beam < 0 ? finished_candidate(a, s, row0, -1 - beam) : candidate(s, row0, beam, s.keys[tid]);
-            s.picked[tid] = c;
+            for (int k = 1; k < kThreads / kGroups; ++k) best = fmaxf(best, s.mine[tid + k * kGroups]);
+            bests[tid] = best;
         }
         __syncthreads();
-        int place = 0;
-        if (tid < count)
-            for (int j = 0; j < count; ++j) place += better(s.picked[j], c);
-        if (tid >= count) place = tid;
-        if (place < n) write_out(a, s, row0, place, c);
-        return;
-    }
-    // more candidates within the rounding of each other than are held: the best of what is left, one after another
-    Candidate last{~0ull, 0};
-    for (int o = 0; o < n; ++o) {
-        Candidate c{0, ~0ull};
-        for (int i = tid; i < all; i += kJoinThreads) {
-            const int p = s.parts[i >> slots_log2];
-            if ((i & mask) >= (p & 0xFFFF)) continue;
-            const Candidate x = candidate(s, row0, p >> 16, mine[i]);
-            if (better(last, x) && better(x, c)) c = x;
+        if (tid < kGroups) {
+            int place = 0;
+#pragma unroll 4
+            for (int j = 0; j < kGroups / 4; ++j) {
+                const float4 y = s.best[j];
+                place += (y.x > best || (y.x == best && 4 * j < tid)) + (y.y > best || (y.y == best && 4 * j + 1 < tid)) +
+                         (y.z > best || (y.z == best && 4 * j + 2 < tid)) + (y.w > best || (y.w == best && 4 * j + 3 < tid));
+            }
+            if (place == n - 1) s.bound = best;
         }
-        if (tid < a.beams && s.state[tid] == kFinished) {
-            const Candidate x = finished_candidate(a, s, row0, tid);
-            if (better(last, x) && better(x, c)) c = x;
-        }
+        __syncthreads();
+        return s.bound;
+    };
+    // the best of all threads' candidates, known to all
+    auto best_of_block = [&](Candidate c) {
 #pragma unroll
         for (int h = 16; h; h >>= 1) {
             const Candidate x{__shfl_xor_sync(0xffffffffu, c.score, h), __shfl_xor_sync(0xffffffffu, c.id, h)};
@@ -557,48 +368,152 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const __grid_co
         if (lane == 0) s.warps[warp] = c;
         __syncthreads();
         c = s.warps[0];
-        for (int w = 1; w < kJoinWarps; ++w)
+        for (int w = 1; w < kWarps; ++w)
             if (better(s.warps[w], c)) c = s.warps[w];
         __syncthreads();
-        last = c;
-        if (tid == 0) write_out(a, s, row0, o, c);
+        return c;
+    };
+
+    // the pieces whose maxima may be among the n best
+    auto each_piece = [&](auto&& f) {
+        for (int i = tid; i < all; i += kThreads) {
+            const int beam = i / pieces;
+            if (s.state[beam] != kGoesOn) continue;
+            const ScaledSum x = mine[i];
+            if (x.sum > 0.f) f(i, beam, x.top);
+        }
+    };
+    float best = -INFINITY;
+    each_piece([&](int, int beam, float top) { best = fmaxf(best, lower(beam, top)); });
+    float bound = nth_best(best);
+    each_piece([&](int i, int beam, float top) {
+        if (!may_be(beam, top, bound)) return;
+        const int at = atomicAdd(&s.n_pieces, 1);
+        if (at < kPieces) s.pieces[at] = i;
+    });
+    __syncthreads();
+    int chosen = s.n_pieces;
+    if (chosen > kPieces) {
+        // too many within the rounding of each other: the best of what is left, one after another
+        Candidate last{~0ull, 0};
+        for (chosen = 0; chosen < n; ++chosen) {
+            Candidate c{0, ~0ull};
+            each_piece([&](int i, int beam, float top) {
+                const Candidate x = exact(beam, top, i - beam * pieces);
+                if (better(last, x) && better(x, c)) c = x;
+            });
+            c = last = best_of_block(c);
+            if (c.id == ~0ull) break;
+            if (tid == 0) s.pieces[chosen] = (static_cast<int>(c.id >> 24) - row0) * pieces + static_cast<int>(c.id & 0xFFFFFFu);
+        }
+        __syncthreads();
+    }
+
+    // their tokens that may be
+    auto each_token = [&](auto&& f) {
+        constexpr int kEach = kUnit / 32;
+        for (int u = warp; u < chosen * (kPiece / kUnit); u += kWarps) {
+            const int i = s.pieces[u / (kPiece / kUnit)], beam = i / pieces;
+            const int base = (i - beam * pieces) * kPiece + u % (kPiece / kUnit) * kUnit;
+            if (base >= a.vocab) continue;
+            float v[kEach];
+            load_values<F32>(static_cast<const uint8_t*>(a.logits) + (row0 + beam) * a.stride * (F32 ? 4 : 2), a.vocab, base, v);
+#pragma unroll
+            for (int k = 0; k < kEach; ++k)
+                if (v[k] > -INFINITY) f(beam, v[k], token_of<F32>(base, k));
+        }
+    };
+    auto pick = [&](uint64_t key, int beam) {
+        const int at = atomicAdd(&s.count, 1);
+        if (at < kPicked) {
+            s.keys[at] = key;
+            s.beams[at] = beam;
+        }
+    };
+    bool closer = bound == -INFINITY && chosen * kPiece > kPicked;
+    for (;;) {
+        if (closer) {                                  // bounded by the tokens' groups
+            best = -INFINITY;
+            each_token([&](int beam, float x, int) { best = fmaxf(best, lower(beam, x)); });
+            bound = nth_best(best);
+        }
+        each_token([&](int beam, float x, int token) {
+            if (may_be(beam, x, bound)) pick(make_key(x, token), beam);
+        });
+        if (finished && s.score[tid] >= bound) pick(0, -1 - tid);
+        __syncthreads();
+        if (s.count <= kPicked || closer) break;
+        closer = true;
+        __syncthreads();
+        if (tid == 0) s.count = 0;
+    }
+    const int count = s.count;
+    auto write_out = [&](int place, const Candidate& c) {
+        const int64_t at = static_cast<int64_t>(blockIdx.x) * n + place;
+        const bool some = c.id != ~0ull;
+        const int row = some ? static_cast<int>(c.id >> 24) : row0;
+        const int token = some ? static_cast<int>(c.id & 0xFFFFFFu) : a.pad;
+        a.out_scores[at] = some ? static_cast<float>(value64(c.score)) : -INFINITY;
+        a.out_tokens[at] = token;
+        a.out_parents[at] = row;
+        if (a.out_finished) a.out_finished[at] = some && (s.state[row - row0] == kFinished || token == a.eos);
+    };
+    if (count <= kPicked) {
+        // a candidate's place is the number of better ones
+        for (int i = tid; i < count; i += kThreads) {
+            const int beam = s.beams[i];
+            s.picked[i] = beam < 0 ? of_finished(-1 - beam) : exact(beam, key_value(s.keys[i]), key_token(s.keys[i]));
+        }
+        __syncthreads();
+        for (int i = tid; i < max(count, n); i += kThreads) {
+            Candidate c{0, ~0ull};
+            int place = i;
+            if (i < count) {
+                c = s.picked[i];
+                place = 0;
+                for (int j = 0; j < count; ++j) place += better(s.picked[j], c);
+            }
+            if (place < n) write_out(place, c);
+        }
+        return;
+    }
+    // too many within the rounding of each other: the best of what is left, one after another
+    Candidate last{~0ull, 0};
+    for (int o = 0; o < n; ++o) {
+        Candidate c{0, ~0ull};
+        each_token([&](int beam, float x, int token) {
+            if (!may_be(beam, x, bound)) return;
+            const Candidate y = exact(beam, x, token);
+            if (better(last, y) && better(y, c)) c = y;
+        });
+        if (finished) {
+            const Candidate y = of_finished(tid);
+            if (better(last, y) && better(y, c)) c = y;
+        }
+        last = best_of_block(c);
+        if (tid == 0) write_out(o, last);
     }
 }
 
-// How a call's rows are cut: parts of whole tiles, and the tokens that each may
-// hand on.
-struct Cut {
-    int unroll;
-    int parts;
-    int span;
-    int slots_log2;
-};
-
-Cut cut_rows(int lanes, int beams, int vocab, int n_out)
+template <bool F32>
+cudaError_t launch(const BeamArgs& a, ScaledSum* sums, cudaStream_t stream)
 {
-    const int rows = lanes * beams > 0 ? lanes * beams : 1, sms = sm_count(-1);
-    const int64_t values = static_cast<int64_t>(rows) * vocab;
-    Cut c;
-    c.unroll = values <= static_cast<int64_t>(sms) * 2 * 4096 ? 1 : values <= static_cast<int64_t>(sms) * 4 * 8192 ? 2 : 4;
-    const int tile = kScanThreads * kVec * c.unroll;
-    const int most = (vocab + tile - 1) / tile, want = min((4 * sms + rows - 1) / rows, kPairs / beams);
-    c.span = ((most + min(most, want) - 1) / min(most, want)) * tile;
-    c.parts = (vocab + c.span - 1) / c.span;
-    c.slots_log2 = n_out <= 8 ? 5 : n_out <= 24 ? 6 : n_out <= 48 ? 7 : 8;
-    return c;
-}
-
-size_t sums_bytes(int lanes, int beams, int parts)
-{
-    return (static_cast<size_t>(lanes) * beams * parts * sizeof(PartSum) + 255) / 256 * 256;
+    const int pieces = (a.vocab + kPiece - 1) / kPiece, sms = sm_count(-1);
+    const int64_t all = static_cast<int64_t>(a.lanes) * a.beams * pieces;
+    const int warps = static_cast<int>(max(static_cast<int64_t>(1), min(all / sms, static_cast<int64_t>(kScanWarps))));
+    const cudaError_t e = launch_pdl(beam_scan_kernel<F32>, dim3(static_cast<unsigned>((all + warps - 1) / warps)),
+                                     dim3(static_cast<unsigned>(32 * warps)), 0, stream, a, pieces, sums);
+    if (e != cudaSuccess) return e;
+    const bool many = a.lanes > 2 * sms;               // lanes: rather more blocks at a time than fast ones
+    return launch_pdl(many ? beam_join_kernel<F32, 256> : beam_join_kernel<F32, 1024>, dim3(static_cast<unsigned>(a.lanes)),
+                      dim3(many ? 256 : 1024), 0, stream, a, pieces, static_cast<const ScaledSum*>(sums));
 }
 
 }  // namespace
 
-size_t beam_select_workspace_bytes(int lanes, int beams, int vocab, int n_out)
+size_t beam_select_workspace_bytes(int lanes, int beams, int vocab, int)
 {
-    const Cut c = cut_rows(lanes, beams, vocab, n_out);
-    return sums_bytes(lanes, beams, c.parts) + (static_cast<size_t>(lanes) * beams * c.parts << c.slots_log2) * sizeof(uint64_t) + 256;
+    return static_cast<size_t>(lanes) * beams * ((vocab + kPiece - 1) / kPiece) * sizeof(ScaledSum) + 256;
 }
 
 qg_status launch_beam_select(const BeamArgs& in, void* workspace, cudaStream_t stream)
@@ -606,17 +521,8 @@ qg_status launch_beam_select(const BeamArgs& in, void* workspace, cudaStream_t s
     BeamArgs a = in;
     a.status = device_status_ptr();
     if (!a.status) return QG_ERR_CUDA;
-    const Cut c = cut_rows(a.lanes, a.beams, a.vocab, a.n_out);
-    PartSum* sums = static_cast<PartSum*>(workspace);
-    uint64_t* keys = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(workspace) + sums_bytes(a.lanes, a.beams, c.parts));
-    auto pick = [&](auto u1, auto u2, auto u4) { return c.unroll == 1 ? u1 : c.unroll == 2 ? u2 : u4; };
-    auto scan = a.f32 ? pick(beam_scan_kernel<true, 1>, beam_scan_kernel<true, 2>, beam_scan_kernel<true, 4>)
-                      : pick(beam_scan_kernel<false, 1>, beam_scan_kernel<false, 2>, beam_scan_kernel<false, 4>);
-    cudaError_t e = launch_pdl(scan, dim3(static_cast<unsigned>(a.lanes * a.beams * c.parts)), dim3(kScanThreads), 0, stream,
-                               a, c.parts, c.span, 1 << c.slots_log2, sums, keys);
-    if (e == cudaSuccess)
-        e = launch_pdl(beam_join_kernel, dim3(static_cast<unsigned>(a.lanes)), dim3(kJoinThreads), 0, stream, a, c.parts,
-                       c.slots_log2, static_cast<const PartSum*>(sums), static_cast<const uint64_t*>(keys));
+    ScaledSum* sums = static_cast<ScaledSum*>(workspace);
+    const cudaError_t e = a.f32 ? launch<true>(a, sums, stream) : launch<false>(a, sums, stream);
     return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 

@@ -243,3 +243,56 @@ def test_offsets_beyond_32_bits():
     ws = torch.empty(q.beam_select_workspace_size(3, 8, V, 8), dtype=torch.uint8, device="cuda")
     q.beam_select(d, torch.from_numpy(scores.astype(np.float32)).cuda(), *out, workspace=ws)
     PU.check_selection(x, scores.astype(np.float32), None, -1, 0, [o.cpu().numpy() for o in out], 8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lanes,beams,vocab,n_out,apart", [
+    (5, 8, 40001, 8, 0), (700, 2, 4097, 5, 3), (9, 64, 12288, 64, 0), (153, 4, 8199, 33, 1), (3, 5, 400000, 12, 5), (2, 1, 5000011, 16, 0),
+    (1300, 1, 8192, 8, 8),
+])
+def test_selection_over_many_logits(dtype, lanes, beams, vocab, n_out, apart):
+    """Calls whose blocks take parts of rows one after another, some of them skipped."""
+    r = np.random.default_rng(vocab)
+    x = logits(r, lanes * beams, vocab, dtype)
+    scores = -10 * r.random((lanes, beams))
+    scores[r.random((lanes, beams)) < 0.1] = -np.inf
+    check(x, dtype, scores, n_out, finished=r.random((lanes, beams)) < 0.2, apart=apart, eos=vocab // 2, pad=vocab - 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n_out", [1, 33, 64])
+def test_orders_that_fill_every_list_of_many_logits(dtype, n_out):
+    V, copies = 60001, 16
+    t = np.arange(V)
+    rows = [t / 400.0, -t / 400.0, np.zeros(V), np.where(t % 5000 == 17, 1.0, 0.0), (t // 64) / 50.0, np.where(t < V - 3, 0.0, 1.0)]
+    x = np.stack(rows)
+    x = O.round_bf16(x) if dtype == "bf16" else x.astype(np.float32).astype(np.float64)
+    got = check(np.repeat(x, copies, 0), dtype, np.zeros((6, copies)), n_out)
+    # rows of a lane are equal and so are their sums, whatever their alignment: by logit, then row, then token
+    for lane in range(6):
+        best = np.lexsort((t, -x[lane]))[:n_out]
+        order = sorted((-x[lane, k], row, k) for k in best for row in range(copies))[:n_out]
+        assert got[1][lane].tolist() == [k for _, _, k in order]
+        assert got[2][lane].tolist() == [lane * copies + row for _, row, _ in order]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_many_logits_masked_and_without_a_sum(dtype):
+    r = np.random.default_rng(21)
+    V, low = 50003, -float(torch.finfo(torch.bfloat16 if dtype == "bf16" else torch.float32).max)
+    x, scores = logits(r, 128, V, dtype), -r.random((16, 8))
+    x[3] = -np.inf
+    x[4, :40000], x[5, 40000:], x[6] = -np.inf, -np.inf, low
+    x[7, ::2], x[8, 5:] = low, low
+    check(x, dtype, scores, 9)
+    x[60, V - 1], x[61, 0], x[62, 30000], scores[9, 1] = np.nan, np.inf, -np.nan, np.inf
+    got = check(x, dtype, scores, 9, bad=True)
+    assert not np.isin(got[2], [60, 61, 62, 73]).any()
+
+
+def test_many_logits_give_the_same_bits_every_time():
+    r = np.random.default_rng(22)
+    x, scores = logits(r, 160, 40011, "fp32"), -r.random((20, 8))
+    first = call(x, "fp32", scores, 8)
+    for _ in range(5):
+        assert all(np.array_equal(a, b) for a, b in zip(first, call(x, "fp32", scores, 8)))
