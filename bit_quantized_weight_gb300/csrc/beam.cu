@@ -15,7 +15,6 @@ namespace {
 
 constexpr int kPiece = 1024;                         // values, 32 of a lane
 constexpr int kScanWarps = 8;                        // of a block, at most
-constexpr int kUnit = 256;                           // values of a piece that a warp looks at again
 constexpr int kGroups = 128;                         // candidates' groups, by whose best one is bounded
 constexpr int kPieces = 128;                         // pieces of a lane that are read again, if more than n_out
 constexpr int kPicked = 512;                         // candidates of a lane that are looked at in 64 bits
@@ -75,51 +74,48 @@ __device__ __forceinline__ void shift_words(uint32_t (&w)[N], int skip)
     }
 }
 
-// 16 bytes of a row of `vocab` values, those from `e` on, -infinity behind its
-// end. The same values go to the same lane whatever the row's alignment; a row
-// that does not start at 16 bytes is read in the aligned pieces around it, but
-// for the last values, which are read one by one. (Plain loads: the kernel
-// before may have written them while this one had started already.)
-template <bool F32>
-__device__ __forceinline__ void load16(const uint8_t* row, int skip, int vocab, int e, float* v)
-{
-    constexpr int kSize = F32 ? 4 : 2, kN = 16 / kSize;
-    const uint8_t* at = row + static_cast<int64_t>(e) * kSize;
-    if (e + kN + (skip ? kN : 0) <= vocab) {
-        uint32_t w[8];
-        const uint4 x = *reinterpret_cast<const uint4*>(at - skip);
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-        if (skip) {
-            const uint4 y = *reinterpret_cast<const uint4*>(at - skip + 16);
-            w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
-            shift_words(w, skip);
-        }
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-            v[i] = F32 ? __uint_as_float(w[i]) : __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            v[i] = -INFINITY;
-            if (e + i < vocab)
-                v[i] = F32 ? reinterpret_cast<const float*>(at)[i]
-                           : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(at)[i]);
-        }
-    }
-}
-
-// N values of each lane from `base` on.
+// N values of each lane from `base` on of a row of `vocab`, -infinity behind
+// its end: pieces of 16 bytes, one lane's after the other. The same values go
+// to the same lane whatever the row's alignment: fp32 rows that do not start at
+// 16 bytes, and the last values of a row, are read one by one, bf16 rows in the
+// aligned pieces around a lane's. (Plain loads: the kernel before may have
+// written them while this one had started already.)
 template <bool F32, int N>
 __device__ __forceinline__ void load_values(const uint8_t* row, int vocab, int base, float (&v)[N])
 {
-    constexpr int kN = F32 ? 4 : 8;
+    constexpr int kSize = F32 ? 4 : 2, kN = 16 / kSize;
     const int lane = threadIdx.x & 31, skip = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
-    if (skip == 0 && base + 32 * N <= vocab) {         // the usual case, without its tests
+    const uint8_t* at = row + static_cast<int64_t>(base + lane * kN) * kSize - skip;
+    if (base + 32 * N <= vocab && skip == 0) {
 #pragma unroll
-        for (int u = 0; u < N / kN; ++u) load16<F32>(row, 0, INT32_MAX, base + (u * 32 + lane) * kN, v + u * kN);
+        for (int u = 0; u < N / kN; ++u) {
+            const uint4 x = *reinterpret_cast<const uint4*>(at + 512 * u);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                v[u * kN + i] = F32 ? __uint_as_float(w[i]) : __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        }
+    } else if (!F32 && base + 32 * N + kN <= vocab) {
+#pragma unroll
+        for (int u = 0; u < N / kN; ++u) {
+            const uint4 x = *reinterpret_cast<const uint4*>(at + 512 * u), y = *reinterpret_cast<const uint4*>(at + 512 * u + 16);
+            uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            shift_words(w, skip);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) v[u * kN + i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        }
     } else {
+        at += skip;
+        const int left = vocab - base - lane * kN;
 #pragma unroll
-        for (int u = 0; u < N / kN; ++u) load16<F32>(row, skip, vocab, base + (u * 32 + lane) * kN, v + u * kN);
+        for (int u = 0; u < N / kN; ++u)
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                v[u * kN + i] = -INFINITY;
+                if (32 * kN * u + i < left)
+                    v[u * kN + i] = F32 ? reinterpret_cast<const float*>(at + 512 * u)[i]
+                                        : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(at + 512 * u)[i]);
+            }
     }
 }
 
@@ -289,6 +285,11 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
     const int row0 = static_cast<int>(blockIdx.x) * a.beams, all = a.beams * pieces;
     const ScaledSum* mine = sums + static_cast<int64_t>(row0) * pieces;
     for (int beam = warp; beam < a.beams; beam += kWarps) {
+        // the first sums are on their way before it is known whether they are any
+        const ScaledSum* p = mine + beam * pieces;
+        ScaledSum x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = i * 32 + lane < pieces ? p[i * 32 + lane] : ScaledSum{kLowest, 0.f};
         const float score = a.scores[row0 + beam];
         const bool done = a.finished && a.finished[row0 + beam];
         int state = kNone;
@@ -298,11 +299,10 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
         } else if (done) {
             state = kFinished;
         } else {
-            ScaledSum r{kLowest, 0.f};
-            for (int i = lane; i < pieces; i += 32) {
-                const ScaledSum x = mine[beam * pieces + i];
-                join_sums(r, x.top, x.sum);
-            }
+            ScaledSum r{fmaxf(fmaxf(x[0].top, x[1].top), fmaxf(x[2].top, x[3].top)), 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r.sum += x[i].sum * ex2((x[i].top - r.top) * kLog2e);
+            for (int i = 128 + lane; i < pieces; i += 32) join_sums(r, p[i].top, p[i].sum);
             warp_sum(r);
             if (!(r.sum >= 0.f && r.sum < INFINITY)) {
                 if (lane == 0) set_device_status(a.status, QG_ERR_INVALID_ARG);
@@ -345,16 +345,22 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
             bests[tid] = best;
         }
         __syncthreads();
-        if (tid < kGroups) {
-            int place = 0;
-#pragma unroll 4
-            for (int j = 0; j < kGroups / 4; ++j) {
-                const float4 y = s.best[j];
-                place += (y.x > best || (y.x == best && 4 * j < tid)) + (y.y > best || (y.y == best && 4 * j + 1 < tid)) +
-                         (y.z > best || (y.z == best && 4 * j + 2 < tid)) + (y.w > best || (y.w == best && 4 * j + 3 < tid));
-            }
-            if (place == n - 1) s.bound = best;
+        // some threads for each group, each with a share of the others
+        constexpr int kEach = kThreads / kGroups;
+        best = bests[tid / kEach];
+        int above = 0, level = 0;
+#pragma unroll
+        for (int j = 0; j < kGroups / 4 / kEach; ++j) {
+            const float4 y = s.best[j * kEach + tid % kEach];
+            above += (y.x > best) + (y.y > best) + (y.z > best) + (y.w > best);
+            level += (y.x == best) + (y.y == best) + (y.z == best) + (y.w == best);
         }
+#pragma unroll
+        for (int o = 1; o < kEach; o <<= 1) {
+            above += __shfl_xor_sync(0xffffffffu, above, o);
+            level += __shfl_xor_sync(0xffffffffu, level, o);
+        }
+        if (above < n && n <= above + level) s.bound = best;
         __syncthreads();
         return s.bound;
     };
@@ -410,18 +416,31 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
     }
 
     // their tokens that may be
-    auto each_token = [&](auto&& f) {
-        constexpr int kEach = kUnit / 32;
-        for (int u = warp; u < chosen * (kPiece / kUnit); u += kWarps) {
-            const int i = s.pieces[u / (kPiece / kUnit)], beam = i / pieces;
-            const int base = (i - beam * pieces) * kPiece + u % (kPiece / kUnit) * kUnit;
-            if (base >= a.vocab) continue;
+    constexpr int kEach = kPiece / 32;
+    auto logits_of = [&](int beam) { return static_cast<const uint8_t*>(a.logits) + (row0 + beam) * a.stride * (F32 ? 4 : 2); };
+    auto each_chosen = [&](auto&& f) {                 // a warp for each
+        for (int u = warp; u < chosen; u += kWarps) {
+            const int i = s.pieces[u], beam = i / pieces, base = (i - beam * pieces) * kPiece;
             float v[kEach];
-            load_values<F32>(static_cast<const uint8_t*>(a.logits) + (row0 + beam) * a.stride * (F32 ? 4 : 2), a.vocab, base, v);
-#pragma unroll
-            for (int k = 0; k < kEach; ++k)
-                if (v[k] > -INFINITY) f(beam, v[k], token_of<F32>(base, k));
+            load_values<F32>(logits_of(beam), a.vocab, base, v);
+            f(beam, base, v);
         }
+    };
+    // Tokens whose f + e may reach the bound. With |x| <= 2 (|base| + |bound|) e is at most 3 2^-21 of that sum, and 2^-21
+    // more of it is above what is rounded here; a lower x is too low by far.
+    auto each_token = [&](auto&& f) {
+        each_chosen([&](int beam, int base, const float (&v)[kEach]) {
+            const float least = bound - s.base[beam] - 4.f * kOff * (fabsf(s.base[beam]) + fabsf(bound));
+            uint32_t hits = 0;
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) hits |= static_cast<uint32_t>(!(v[k] < least) && v[k] > -INFINITY) << k;
+            const uint8_t* row = logits_of(beam);
+            for (; hits; hits &= hits - 1) {           // few: read again, which spares a copy of this code for each
+                const int token = token_of<F32>(base, __ffs(hits) - 1);
+                f(beam, F32 ? reinterpret_cast<const float*>(row)[token] : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(row)[token]),
+                  token);
+            }
+        });
     };
     auto pick = [&](uint64_t key, int beam) {
         const int at = atomicAdd(&s.count, 1);
@@ -434,12 +453,15 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
     for (;;) {
         if (closer) {                                  // bounded by the tokens' groups
             best = -INFINITY;
-            each_token([&](int beam, float x, int) { best = fmaxf(best, lower(beam, x)); });
+            each_chosen([&](int beam, int, const float (&v)[kEach]) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) top = fmaxf(top, v[k]);
+                if (top > -INFINITY) best = fmaxf(best, lower(beam, top));
+            });
             bound = nth_best(best);
         }
-        each_token([&](int beam, float x, int token) {
-            if (may_be(beam, x, bound)) pick(make_key(x, token), beam);
-        });
+        each_token([&](int beam, float x, int token) { pick(make_key(x, token), beam); });
         if (finished && s.score[tid] >= bound) pick(0, -1 - tid);
         __syncthreads();
         if (s.count <= kPicked || closer) break;
@@ -465,15 +487,16 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
             s.picked[i] = beam < 0 ? of_finished(-1 - beam) : exact(beam, key_value(s.keys[i]), key_token(s.keys[i]));
         }
         __syncthreads();
-        for (int i = tid; i < max(count, n); i += kThreads) {
-            Candidate c{0, ~0ull};
-            int place = i;
-            if (i < count) {
-                c = s.picked[i];
-                place = 0;
-                for (int j = 0; j < count; ++j) place += better(s.picked[j], c);
-            }
-            if (place < n) write_out(place, c);
+        constexpr int kShare = 8;                      // threads for each
+        for (int i0 = 0; i0 < max(count, n); i0 += kThreads / kShare) {
+            const int i = i0 + tid / kShare;
+            const Candidate c = i < count ? s.picked[i] : Candidate{0, ~0ull};
+            int place = 0;
+            for (int j = tid % kShare; j < count; j += kShare) place += better(s.picked[j], c);
+#pragma unroll
+            for (int o = 1; o < kShare; o <<= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+            if (i >= count) place = i;
+            if (tid % kShare == 0 && place < n) write_out(place, c);
         }
         return;
     }
@@ -482,7 +505,6 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
     for (int o = 0; o < n; ++o) {
         Candidate c{0, ~0ull};
         each_token([&](int beam, float x, int token) {
-            if (!may_be(beam, x, bound)) return;
             const Candidate y = exact(beam, x, token);
             if (better(last, y) && better(y, c)) c = y;
         });
