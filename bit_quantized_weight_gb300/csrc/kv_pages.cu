@@ -10,7 +10,7 @@
 namespace qg {
 namespace {
 
-constexpr int kForkThreads = 256, kForkCols = 32;
+constexpr int kForkThreads = 1024, kForkCols = 8, kForkRun = 32, kForkAhead = 8;
 constexpr int kPlanThreads = 1024;
 constexpr int kTableThreads = 256;
 constexpr int kHash = 2048;
@@ -52,21 +52,27 @@ __device__ __forceinline__ int parent_of(const PageArgs& a, const int32_t* paren
 // A block takes kForkCols columns of the whole table: every row's entries go
 // to shared memory first, so that rows may be permuted in place. An entry of
 // old row j is held by kids[j] rows afterwards (by none behind the page of the
-// row's last token) and was held once: refs changes by the difference.
+// row's last token) and was held once: refs changes by the difference. A page
+// that the rows of a prompt share stands in one column of rows next to each
+// other: a thread goes down kForkRun rows and adds up what a run of one page
+// changes by, which for beams that go on from each other is mostly nothing.
+__host__ __device__ __forceinline__ int slab_at(int row, int col) { return (row + row / kForkRun) * kForkCols + col; }
+
 __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const __grid_constant__ PageArgs a, const int32_t* parent)
 {
     extern __shared__ int smem[];
     pdl_enter();
-    const int n = a.n_seqs, tid = threadIdx.x;
+    const int n = a.n_seqs, tid = threadIdx.x, threads = blockDim.x;
+    const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kForkCols;
     int* par = smem;
     int* keep = par + n;
     int* held = keep + n;
     int* kids = held + n;
     int* slab = kids + n;
-    for (int i = tid; i < n; i += kForkThreads) kids[i] = 0;
+    for (int i = tid; i < n; i += threads) kids[i] = 0;
     __syncthreads();
     int most = 0;
-    for (int i = tid; i < n; i += kForkThreads) {
+    for (int i = tid; i < n; i += threads) {
         bool bad;
         const PageRow r = page_row(a, i);
         const int p = parent_of(a, parent, i, bad);
@@ -77,23 +83,43 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const __grid_c
         most = max(most, r.held);
         if (p >= 0) atomicAdd(&kids[p], 1);
     }
-    const int c = static_cast<int>(blockIdx.x) * kForkCols + (tid & 31);
-    if (__syncthreads_or(most > static_cast<int>(blockIdx.x) * kForkCols) == 0) return;
-    for (int j = tid >> 5; j < n; j += kForkThreads / 32) {
-        if (c >= held[j]) continue;
-        const int e = a.table[static_cast<int64_t>(j) * a.max_pages + c];
-        slab[j * kForkCols + (tid & 31)] = e;
-        const int change = (c < keep[j] ? kids[j] : 0) - 1;
-        if (!in_pool(a, e))
-            set_device_status(a.status, QG_ERR_INVALID_ARG);
-        else if (change)
-            atomicAdd(&a.refs[e], change);
+    if (__syncthreads_or(most > col0) == 0) return;
+    const int64_t c = col0 + tid % kForkCols;
+    const int row0 = tid / kForkCols, step = threads / kForkCols;
+    for (int j0 = row0; j0 < n; j0 += kForkAhead * step) {
+        int e[kForkAhead];
+#pragma unroll
+        for (int u = 0; u < kForkAhead; ++u) {
+            const int j = j0 + u * step;
+            if (j < n && c < held[j]) e[u] = a.table[static_cast<int64_t>(j) * a.max_pages + c];
+        }
+#pragma unroll
+        for (int u = 0; u < kForkAhead; ++u) {
+            const int j = j0 + u * step;
+            if (j < n && c < held[j]) slab[slab_at(j, tid % kForkCols)] = e[u];
+        }
     }
     __syncthreads();
-    for (int i = tid >> 5; i < n; i += kForkThreads / 32) {
+    for (int i = row0; i < n; i += step) {
         const int p = par[i];
         if (p < 0 || p == i || c >= keep[p]) continue;
-        a.table[static_cast<int64_t>(i) * a.max_pages + c] = slab[p * kForkCols + (tid & 31)];
+        a.table[static_cast<int64_t>(i) * a.max_pages + c] = slab[slab_at(p, tid % kForkCols)];
+    }
+    for (int j0 = row0 * kForkRun; j0 < n; j0 += step * kForkRun) {
+        int page = -1, change = 0;
+        for (int j = j0; j <= min(j0 + kForkRun, n); ++j) {
+            const bool last = j == min(j0 + kForkRun, n);
+            if (!last && c >= held[j]) continue;
+            const int e = last ? -1 : slab[slab_at(j, tid % kForkCols)];
+            const int now = in_pool(a, e) ? e : -1;
+            if (!last && now < 0) set_device_status(a.status, QG_ERR_INVALID_ARG);
+            if (now != page) {
+                if (change) atomicAdd(&a.refs[page], change);
+                page = now;
+                change = 0;
+            }
+            if (page >= 0) change += (c < keep[j] ? kids[j] : 0) - 1;
+        }
     }
 }
 
@@ -148,7 +174,8 @@ __device__ __forceinline__ int cluster_word(const int* p, uint32_t rank)
     return v;
 }
 
-// Sum over the block of v, and what the threads before this one have.
+// Sum over the block of v, and what the threads before this one have. Each
+// scan of a kernel has its own warp_sums, so that one barrier is enough.
 template <typename T>
 __device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total)
 {
@@ -159,7 +186,6 @@ __device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total)
         const T y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    __syncthreads();
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
     T s = warp_sums[lane];
@@ -236,7 +262,8 @@ struct ReserveSmem {
     int page[kHash];             // part-filled pages that rows of the call write,
     int writers[kHash];          // how many do,
     int lowest[kHash];           // and the lowest of them
-    int64_t sums[32];
+    int64_t row_sums[32];
+    int page_sums[32];
     int count;
 };
 
@@ -252,20 +279,26 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const __gri
     uint32_t* bits = reinterpret_cast<uint32_t*>(smem + (sizeof(ReserveSmem) + 3) / 4);
     pdl_enter();
     const int b = threadIdx.x, rank = static_cast<int>(cluster_rank());
+    // this thread's row, on its way while the free pages are looked for
+    PageRow r{0, 0, true};
+    int add = 0;
+    if (b < a.n_seqs) {
+        r = page_row(a, b);
+        add = n_new[b];
+    }
     for (int i = b; i < kHash; i += kPlanThreads) {
         s.page[i] = -1;
         s.writers[i] = 0;
         s.lowest[i] = kKvMaxSeqs;
     }
-    __syncthreads();
+    const Share sh = share_of(a);
+    scan_refs(a, sh.word0, sh.words, true, bits);
+    int mine = 0;
+    for (int w = sh.from; w < sh.to; ++w) mine += __popc(bits[w]);
 
-    // this thread's row
     bool writes = false, bad = false;
     int first = 0, last = 0, tail = -1, count = 0, slot = -1;
-    PageRow r{0, 0, true};
     if (b < a.n_seqs) {
-        r = page_row(a, b);
-        const int add = n_new[b];
         const int64_t end = static_cast<int64_t>(r.len) + add;
         bad = !r.ok || add < 0 ||
               end > min(static_cast<int64_t>(a.max_pages) * a.page_size, static_cast<int64_t>(kKvMaxPositions));
@@ -301,25 +334,21 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const __gri
     __syncthreads();
     const bool replaced = slot >= 0 && !(s.writers[slot] == count && s.lowest[slot] == b);
     const int fresh = writes ? max(0, last - r.held) : 0;
-    int64_t total, moves;
-    const int64_t before = block_scan<int64_t>(static_cast<int64_t>(fresh) + replaced, s.sums, total);
-    const int64_t at = block_scan<int64_t>(replaced, s.sums, moves);
-    s.off[b] = static_cast<int>(before);               // exact where it is used: total <= the pool's pages
+    // new pages (at most 2^26 + 1 of a row), and in the lower 11 bits replaced ones (at most 2^10)
+    int64_t both;
+    const int64_t before = block_scan<int64_t>((static_cast<int64_t>(fresh) + replaced) << 11 | replaced, s.row_sums, both);
+    const int64_t total = both >> 11;
+    const int moves = static_cast<int>(both & 2047);
+    s.off[b] = static_cast<int>(before >> 11);         // exact where it is used: total <= the pool's pages
     s.first[b] = replaced ? first : -1;
     s.held[b] = r.held;
     s.tail[b] = tail;
     s.tokens[b] = writes ? r.len % a.page_size : 0;
-    s.move[b] = static_cast<int>(at);
+    s.move[b] = static_cast<int>(before & 2047);
     if (b == 0) s.off[kKvMaxSeqs] = static_cast<int>(total);
 
-    // this block's share of the pool
-    const Share sh = share_of(a);
-    scan_refs(a, sh.word0, sh.words, true, bits);
-    int mine = 0;
-    for (int w = sh.from; w < sh.to; ++w) mine += __popc(bits[w]);
-    int64_t block_free;
-    int k = static_cast<int>(block_scan<int64_t>(mine, s.sums, block_free));
-    if (b == 0) s.count = static_cast<int>(block_free);
+    int block_free, k = block_scan<int>(mine, s.page_sums, block_free);
+    if (b == 0) s.count = block_free;
     cluster_sync();
     int64_t free_pages = 0;
     for (int x = 0; x < static_cast<int>(cluster_size()); ++x) {
@@ -330,22 +359,23 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const __gri
     const bool enough = total <= free_pages;
     if (rank == 0) {
         if (b == 0) {
-            *m.count = enough ? static_cast<int>(moves) : 0;
+            *m.count = enough ? moves : 0;
             if (n_free) *n_free = static_cast<int>(max(free_pages - total, static_cast<int64_t>(-0x7FFFFFFF)));
         }
         if (enough && writes) a.held[b] = max(r.held, last);
         if (enough && replaced) atomicSub(&a.refs[tail], 1);
     }
     if (enough) {
+        int lo = 0, hi = kKvMaxSeqs;                   // the last row with off <= k has the thread's first page
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (s.off[mid] <= k) lo = mid;
+            else hi = mid;
+        }
         for (int w = sh.from; w < sh.to && k < total; ++w)
             for (uint32_t x = bits[w]; x && k < total; x &= x - 1, ++k) {
                 const int page = (sh.word0 + w) * 32 + __ffs(x) - 1;
-                int lo = 0, hi = kKvMaxSeqs;           // the last row with off <= k has the page
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) / 2;
-                    if (s.off[mid] <= k) lo = mid;
-                    else hi = mid;
-                }
+                while (s.off[lo + 1] <= k) ++lo;       // off[kKvMaxSeqs] = total
                 const int local = k - s.off[lo], c = s.first[lo];
                 const bool copy = c >= 0 && local == 0;
                 const int col = copy ? c : s.held[lo] + local - (c >= 0);
@@ -359,7 +389,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const __gri
 
 // ------------------------------------------------------------------ compact
 struct CompactSmem {
-    int64_t sums[32];
+    int sums[3][32];
     int live;
     int holes;
     int movers;
@@ -380,9 +410,9 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const __gri
     scan_refs(a, sh.word0, sh.words, false, bits);
     int mine = 0;
     for (int w = sh.from; w < sh.to; ++w) mine += __popc(bits[w]);
-    int64_t all;
-    block_scan<int64_t>(mine, s.sums, all);
-    if (tid == 0) s.live = static_cast<int>(all);
+    int all;
+    block_scan<int>(mine, s.sums[0], all);
+    if (tid == 0) s.live = all;
     cluster_sync();
     int live = 0;
     for (int x = 0; x < size; ++x) live += cluster_word(&s.live, x);
@@ -396,13 +426,13 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const __gri
         holes += __popc(~bits[w] & below(w));
         movers += __popc(bits[w] & ~below(w));
     }
-    int64_t block_holes, block_movers;
-    int hole = static_cast<int>(block_scan<int64_t>(holes, s.sums, block_holes));
-    const int64_t movers_before = block_scan<int64_t>(movers, s.sums, block_movers);
-    int mover = static_cast<int>(block_movers - movers_before) - movers;    // movers of the threads behind
+    int block_holes, block_movers;
+    int hole = block_scan<int>(holes, s.sums[1], block_holes);
+    const int movers_before = block_scan<int>(movers, s.sums[2], block_movers);
+    int mover = block_movers - movers_before - movers;                      // movers of the threads behind
     if (tid == 0) {
-        s.holes = static_cast<int>(block_holes);
-        s.movers = static_cast<int>(block_movers);
+        s.holes = block_holes;
+        s.movers = block_movers;
     }
     cluster_sync();
     int n = 0;
@@ -421,20 +451,38 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const __gri
         const int page = sh.word0 * 32 + i;
         if (page < a.num_pages) page_map[page] = bits[i / 32] >> (i & 31) & 1u ? page : -1;
     }
+    // places and pages of the list, each by the thread that found it
     for (int w = sh.from; w < sh.to && hole < n; ++w)
         for (uint32_t x = ~bits[w] & below(w); x && hole < n; x &= x - 1, ++hole)
             m.list[hole].y = (sh.word0 + w) * 32 + __ffs(x) - 1;
-    cluster_sync();
     for (int w = sh.to - 1; w >= sh.from && mover < n; --w)
         for (uint32_t x = bits[w] & ~below(w); x && mover < n; ++mover) {
             const int bit = 31 - __clz(x);
             x ^= 1u << bit;
-            const int page = (sh.word0 + w) * 32 + bit, to = __ldcg(&m.list[mover].y);
-            m.list[mover] = make_int4(page, to, a.page_size, 0);
-            a.refs[to] = a.refs[page];
-            a.refs[page] = 0;
-            page_map[page] = to;
+            m.list[mover].x = (sh.word0 + w) * 32 + bit;
         }
+    cluster_sync();
+    // then the moves side by side
+    constexpr int kAhead = 4;
+    const int step = kPlanThreads * size;
+    for (int i0 = rank * kPlanThreads + tid; i0 < n; i0 += kAhead * step) {
+        int4 e[kAhead];
+        int held[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i0 + u * step < n) e[u] = __ldcg(&m.list[i0 + u * step]);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i0 + u * step < n) held[u] = __ldcg(&a.refs[e[u].x]);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i0 + u * step < n) {
+                m.list[i0 + u * step] = make_int4(e[u].x, e[u].y, a.page_size, 0);
+                a.refs[e[u].y] = held[u];
+                a.refs[e[u].x] = 0;
+                page_map[e[u].x] = e[u].y;
+            }
+    }
 }
 
 // The entries in use, through the map.
@@ -444,7 +492,7 @@ __global__ void __launch_bounds__(kTableThreads) pages_table_kernel(const __grid
     const int b = blockIdx.y;
     const PageRow r = page_row(a, b);
     if (!r.ok && blockIdx.x == 0 && threadIdx.x == 0) set_device_status(a.status, QG_ERR_INVALID_ARG);
-    for (int c = blockIdx.x * kTableThreads + threadIdx.x; c < r.held; c += gridDim.x * kTableThreads) {
+    for (int64_t c = blockIdx.x * kTableThreads + threadIdx.x; c < r.held; c += gridDim.x * kTableThreads) {
         int32_t* e = a.table + static_cast<int64_t>(b) * a.max_pages + c;
         const int was = *e, to = in_pool(a, was) ? page_map[was] : -1;
         if (to < 0)
@@ -480,7 +528,38 @@ __device__ __forceinline__ void copy_pieces(const uint8_t* src, uint8_t* dst, in
     }
 }
 
-// A warp takes an item: a run of a move's codes, or of its scales, of one side.
+// Entry `move` of the list, checked; without tokens where it does not fit.
+__device__ __forceinline__ int4 move_at(const KvArgs& a, const MoveArgs& m, int64_t move)
+{
+    int4 e = m.list[move];
+    if (static_cast<unsigned>(e.x) >= static_cast<unsigned>(a.num_pages) ||
+        static_cast<unsigned>(e.y) >= static_cast<unsigned>(a.num_pages) || e.z < 0 || e.z > a.page_size) {
+        set_device_status(a.status, QG_ERR_INVALID_ARG);
+        e = make_int4(0, 0, 0, 0);
+    }
+    return e;
+}
+
+// A warp copies chunk `chunk` of the scales of move e, one side.
+__device__ __forceinline__ void copy_scales(const KvArgs& a, const int4& e, int kv, int chunk)
+{
+    const int unit = kv_scale_bytes(a.fmt, a.dim);
+    const int64_t stride = static_cast<int64_t>(a.page_size) * unit, page = stride * a.heads;
+    const int64_t n = static_cast<int64_t>(e.z) * unit, all = n * a.heads;
+    const uint8_t* src = a.scales[kv] + e.x * page;
+    uint8_t* dst = a.scales[kv] + e.y * page;
+    const int64_t first = static_cast<int64_t>(chunk) * kScaleChunk, end = min(first + kScaleChunk, all);
+    if (first >= end) return;
+    if (n % 16 == 0)
+        copy_pieces<uint4, kCopyPieces>(src, dst, stride, n, first / 16, end / 16);
+    else if (n % 4 == 0)
+        copy_pieces<uint32_t, kCopyPieces>(src, dst, stride, n, first / 4, end / 4);
+    else
+        copy_pieces<uint8_t, kCopyPieces>(src, dst, stride, n, first, end);
+}
+
+// Few moves. A warp takes an item: a run of a move's codes, or of its scales,
+// of one side.
 __global__ void __launch_bounds__(32 * kCopyWarps) pages_copy_kernel(const __grid_constant__ KvArgs a, const MoveArgs m,
                                                                      int code_items, int scale_items)
 {
@@ -491,38 +570,135 @@ __global__ void __launch_bounds__(32 * kCopyWarps) pages_copy_kernel(const __gri
         return;
     }
     const int per_side = code_items + scale_items, per_move = 2 * per_side;
-    const int rb = kv_row_bytes(a.fmt, a.dim), sb = kv_scale_bytes(a.fmt, a.dim);
+    const int rb = kv_row_bytes(a.fmt, a.dim);
     const int64_t total = static_cast<int64_t>(count) * per_move;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kCopyWarps;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5); i < total; i += step) {
-        const int move = static_cast<int>(i / per_move);
+        const int64_t move = i / per_move;
         int item = static_cast<int>(i % per_move);
         const int kv = item >= per_side;
         item -= kv * per_side;
-        const int4 e = m.list[move];
-        if (static_cast<unsigned>(e.x) >= static_cast<unsigned>(a.num_pages) ||
-            static_cast<unsigned>(e.y) >= static_cast<unsigned>(a.num_pages) || e.z < 0 || e.z > a.page_size) {
-            set_device_status(a.status, QG_ERR_INVALID_ARG);
+        const int4 e = move_at(a, m, move);
+        if (e.z == 0) continue;
+        if (item >= code_items) {
+            copy_scales(a, e, kv, item - code_items);
             continue;
         }
-        if (e.z == 0) continue;
-        const bool scales = item >= code_items;
-        const int unit = scales ? sb : rb;
-        uint8_t* base = scales ? a.scales[kv] : a.codes[kv];
-        const int64_t stride = static_cast<int64_t>(a.page_size) * unit, page = stride * a.heads;
-        const int64_t n = static_cast<int64_t>(e.z) * unit, all = n * a.heads;
-        const uint8_t* src = base + e.x * page;
-        uint8_t* dst = base + e.y * page;
-        const int64_t chunk = scales ? kScaleChunk : 32 * 16 * kCopyPieces;
-        const int64_t first = (scales ? item - code_items : item) * chunk, end = min(first + chunk, all);
-        if (first >= end) continue;
-        if (n % 16 == 0)
-            copy_pieces<uint4, kCopyPieces>(src, dst, stride, n, first / 16, end / 16);
-        else if (n % 4 == 0)
-            copy_pieces<uint32_t, kCopyPieces>(src, dst, stride, n, first / 4, end / 4);
-        else
-            copy_pieces<uint8_t, kCopyPieces>(src, dst, stride, n, first, end);
+        const int64_t stride = static_cast<int64_t>(a.page_size) * rb, page = stride * a.heads;
+        const int64_t n = static_cast<int64_t>(e.z) * rb, all = n * a.heads;            // multiples of 32
+        const int64_t chunk = 32 * 16 * kCopyPieces, first = item * chunk, end = min(first + chunk, all);
+        if (first < end)
+            copy_pieces<uint4, kCopyPieces>(a.codes[kv] + e.x * page, a.codes[kv] + e.y * page, stride, n, first / 16, end / 16);
     }
+}
+
+// Many moves. One thread of a block keeps kBulkAhead chunks of codes on their
+// way into shared memory and stores them from there, all with bulk copies (rows
+// are multiples of 32 bytes); the other warps copy scales. Whole pages are cut
+// into chunks, others into those of each head's tokens.
+constexpr int kBulkChunk = 16 << 10, kBulkStages = 12, kBulkAhead = 8;
+constexpr uint64_t kBulkWaitNs = 1000000000ull;
+
+struct BulkChunk {
+    const uint8_t* src;
+    uint8_t* dst;
+    uint32_t bytes;
+};
+
+__global__ void __launch_bounds__(32 * kCopyWarps, 1) pages_copy_bulk_kernel(const __grid_constant__ KvArgs a, const MoveArgs m,
+                                                                             int code_chunks, int scale_items)
+{
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint64_t full[kBulkStages];
+    const int tid = threadIdx.x;
+    if (tid == 0) {
+        for (int i = 0; i < kBulkStages; ++i) mbar_init(&full[i], 1);
+        fence_barrier_init();
+    }
+    pdl_enter();
+    const int count = *m.count;
+    if (count < 0 || count > m.capacity) {
+        if (blockIdx.x == 0 && tid == 0) set_device_status(a.status, QG_ERR_INVALID_ARG);
+        return;
+    }
+    if (tid >= 32) {
+        const int64_t total = static_cast<int64_t>(count) * 2 * scale_items, step = static_cast<int64_t>(gridDim.x) * (kCopyWarps - 1);
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kCopyWarps - 1) + (tid >> 5) - 1; i < total; i += step) {
+            const int64_t side = i / scale_items;
+            const int4 e = move_at(a, m, side >> 1);
+            if (e.z) copy_scales(a, e, static_cast<int>(side & 1), static_cast<int>(i % scale_items));
+        }
+        return;
+    }
+    if (tid) return;
+    const int rb = kv_row_bytes(a.fmt, a.dim);
+    const int64_t stride = static_cast<int64_t>(a.page_size) * rb, page = stride * a.heads;
+    const int per_head = code_chunks / a.heads;
+    // chunk `chunk` of side `side` (keys or values of a move), gridDim.x on at a time; its entry is read one ahead
+    const int sides = 2 * count, side_step = gridDim.x / code_chunks, chunk_step = gridDim.x % code_chunks;
+    int side = blockIdx.x / code_chunks, chunk = blockIdx.x % code_chunks;
+    int4 ahead = side < sides ? move_at(a, m, side >> 1) : int4{};
+    auto next_chunk = [&](BulkChunk& c) {              // the next one that is any
+        while (side < sides) {
+            const int4 e = ahead;
+            const int kv = side & 1, of = chunk;
+            side += side_step;
+            chunk += chunk_step;
+            if (chunk >= code_chunks) {
+                chunk -= code_chunks;
+                ++side;
+            }
+            if (side < sides) ahead = move_at(a, m, side >> 1);
+            const bool whole = e.z == a.page_size;
+            const int64_t n = whole ? page : static_cast<int64_t>(e.z) * rb;
+            const int head = whole ? 0 : of / per_head;
+            const int64_t from = static_cast<int64_t>(of - head * per_head) * kBulkChunk;
+            if (from >= n) continue;
+            c.src = a.codes[kv] + e.x * page + head * stride + from;
+            c.dst = a.codes[kv] + e.y * page + head * stride + from;
+            c.bytes = static_cast<uint32_t>(min(n - from, static_cast<int64_t>(kBulkChunk)));
+            return true;
+        }
+        return false;
+    };
+    uint8_t* dst[kBulkAhead];
+    uint32_t bytes[kBulkAhead];
+    int loaded = 0, stored = 0;
+    uint32_t round = 0;
+    bool more = true;
+    for (int put = 0, got = 0;; ++stored) {
+#pragma unroll 1
+        while (more && loaded - stored < kBulkAhead) {
+            BulkChunk c;
+            more = next_chunk(c);
+            if (!more) break;
+            // the stage's last store is at least kBulkStages - kBulkAhead + 1 stores back
+            if (loaded >= kBulkStages) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBulkStages - kBulkAhead) : "memory");
+            mbar_arrive_expect_tx(&full[put], c.bytes);
+            bulk_load(ring + put * kBulkChunk, c.src, c.bytes, &full[put]);
+            dst[loaded % kBulkAhead] = c.dst;
+            bytes[loaded % kBulkAhead] = c.bytes;
+            put = put + 1 == kBulkStages ? 0 : put + 1;
+            ++loaded;
+        }
+        if (stored == loaded) break;
+        if (!mbar_wait_bounded(&full[got], round, kBulkWaitNs, a.status)) {
+            // nothing is left on its way into a block that is gone
+            for (; stored < loaded; ++stored) {
+                mbar_wait_bounded(&full[got], round, kBulkWaitNs, a.status);
+                got = got + 1 == kBulkStages ? 0 : got + 1;
+                round ^= got == 0;
+            }
+            break;
+        }
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\ncp.async.bulk.commit_group;" ::"l"(
+                         reinterpret_cast<uint64_t>(dst[stored % kBulkAhead])),
+                     "r"(smem_u32(ring + got * kBulkChunk)), "r"(bytes[stored % kBulkAhead])
+                     : "memory");
+        got = got + 1 == kBulkStages ? 0 : got + 1;
+        round ^= got == 0;
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ launches
@@ -537,12 +713,12 @@ size_t plan_smem(const PageArgs& a, size_t fixed)
     return (fixed + 3) / 4 * 4 + static_cast<size_t>((words + blocks - 1) / blocks) * 4;
 }
 
-bool allow_smem(const void* kern, bool (&set)[64])
+bool allow_smem(const void* kern, bool (&set)[64], int bytes = kPlanSmemMax)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     if (!set[dev]) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanSmemMax) != cudaSuccess) return false;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
         set[dev] = true;
     }
     return true;
@@ -582,9 +758,10 @@ qg_status launch_pages_fork(const PageArgs& in, const int32_t* parent, cudaStrea
     static bool set[64] = {};
     PageArgs a;
     if (!with_status(in, a) || !allow_smem(reinterpret_cast<const void*>(pages_fork_kernel), set)) return QG_ERR_CUDA;
-    const size_t smem = static_cast<size_t>(a.n_seqs) * (4 + kForkCols) * 4;
+    const size_t smem = (static_cast<size_t>(a.n_seqs) * 4 + slab_at(a.n_seqs - 1, kForkCols)) * 4;
+    const int threads = min(kForkThreads, max(64, (a.n_seqs * kForkCols + 31) / 32 * 32));
     cudaError_t e = launch_pdl(pages_fork_kernel, dim3(static_cast<unsigned>((a.max_pages - 1) / kForkCols + 1)),
-                               dim3(kForkThreads), smem, stream, a, parent);
+                               dim3(static_cast<unsigned>(threads)), smem, stream, a, parent);
     if (e == cudaSuccess) e = launch_pdl(pages_fork_rows_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a, parent);
     return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
@@ -625,6 +802,17 @@ qg_status launch_pages_copy(const KvArgs& in, const MoveArgs& m, cudaStream_t st
     const int64_t code = 32 * 16 * kCopyPieces;
     const int code_items = static_cast<int>((rows * kv_row_bytes(a.fmt, a.dim) + code - 1) / code);
     const int scale_items = static_cast<int>((rows * kv_scale_bytes(a.fmt, a.dim) + kScaleChunk - 1) / kScaleChunk);
+    // The list's length is device data: by its capacity. Below it, a few moves that have to be quick (8 part-filled pages:
+    // 2.4 us); above, 2,048 pages of 2 x 128 KB take COPYA us with the bulk copies, COPYB us without.
+    if (m.capacity * 2 * rows * kv_row_bytes(a.fmt, a.dim) > int64_t{64} << 20) {
+        static bool set[64] = {};
+        constexpr int kSmem = kBulkStages * kBulkChunk;
+        if (!allow_smem(reinterpret_cast<const void*>(pages_copy_bulk_kernel), set, kSmem)) return QG_ERR_CUDA;
+        const int code_chunks = a.heads * static_cast<int>((static_cast<int64_t>(a.page_size) * kv_row_bytes(a.fmt, a.dim) + kBulkChunk - 1) / kBulkChunk);
+        const cudaError_t e = launch_pdl(pages_copy_bulk_kernel, dim3(static_cast<unsigned>(sm_count(-1))), dim3(32 * kCopyWarps),
+                                         kSmem, stream, a, m, code_chunks, scale_items);
+        return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+    }
     const int64_t warps = static_cast<int64_t>(m.capacity) * 2 * (code_items + scale_items);
     const int64_t blocks = min((warps + kCopyWarps - 1) / kCopyWarps, static_cast<int64_t>(sm_count(-1)) * 8);
     const cudaError_t e = launch_pdl(pages_copy_kernel, dim3(static_cast<unsigned>(blocks)), dim3(32 * kCopyWarps), 0,

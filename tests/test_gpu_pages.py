@@ -402,3 +402,65 @@ def test_beams_keep_their_own_history(fmt):
     assert torch.equal(refs.int(), rec.refs)
     q.kv_pages_fork(rec, i32(np.full(n, -1)))
     assert int(rec.refs.sum()) == 0 and int(rec.n_pages.sum()) == 0
+
+
+@pytest.mark.parametrize("fmt,page,heads,dim", [("bf16", 64, 8, 128), ("bf16", 256, 3, 256), ("fp8", 48, 5, 64), ("nvfp4", 16, 4, 128),
+                                                ("fp8", 1024, 2, 256), ("nvfp4", 64, 1, 64)])
+def test_long_lists_of_moves(fmt, page, heads, dim):
+    """Lists whose capacity is many pages: whole pages, part-filled ones, none; short lists in them; entries that do not fit."""
+    r = np.random.default_rng(16)
+    row = {"bf16": 2 * dim, "fp8": dim, "nvfp4": dim // 2}[fmt]
+    n = max(3, 70 * 2 ** 20 // (2 * page * heads * row))
+    pages = min(2 * n + 1, 3000)
+    n_used = (pages - 1) // 2
+    c = random_cache(r, fmt, pages, page, heads, dim)
+    for count, mode in ((n_used, "whole"), (n_used, "mixed"), (1, "whole"), (0, "whole"), (min(n_used, 37), "bad")):
+        ids = r.permutation(pages)
+        tokens = np.full(n_used, page)
+        if mode != "whole":
+            tokens = np.where(r.random(n_used) < 0.5, page, r.integers(0, page + 1, n_used))
+        moves = np.zeros((max(n, n_used), 4), np.int64)
+        moves[:n_used, 0], moves[:n_used, 1], moves[:n_used, 2] = ids[:n_used], ids[n_used:2 * n_used], tokens
+        if mode == "bad":
+            moves[3, 0], moves[5, 1], moves[7, 2], moves[9, 2] = pages, -1, page + 1, -1
+        want = [t.clone() for t in parts_of(c)]
+        src, dst, t = (torch.from_numpy(moves[:count, i]).cuda() for i in range(3))
+        ok = (src >= 0) & (src < pages) & (dst >= 0) & (dst < pages) & (t >= 0) & (t <= page)
+        src, dst, t = src[ok], dst[ok], t[ok]
+        inside = torch.arange(page, device="cuda")[None] < t[:, None]
+        for w in want:
+            keep = inside.view(len(t), 1, page, *[1] * (w.dim() - 3))
+            w[dst] = torch.where(keep, w[src], w[dst])
+        q.kv_pages_copy(c, q.KVMoves(i32(moves), i32([count])))
+        status(mode == "bad")
+        assert all(torch.equal(a, b) for a, b in zip(parts_of(c), want)), mode
+    for count in (-1, max(n, n_used) + 1):
+        q.kv_pages_copy(c, q.KVMoves(i32(moves), i32([count])))
+        status(True)
+        assert all(torch.equal(a, b) for a, b in zip(parts_of(c), want))
+
+
+def test_many_rows_share_and_part():
+    """Prompts of 1 to 40 rows whose beams go on from each other or from another prompt, pages in runs of every length."""
+    r = np.random.default_rng(17)
+    for n, wide, page in ((1000, 21, 16), (97, 70, 48), (33, 9, 64), (1024, 3, 1024)):
+        P = PU.Pages(n, wide, n * wide + 5, page)
+        order, b = list(r.permutation(P.pool)), 0
+        while b < n:
+            rows = min(n - b, int(r.integers(1, 41)))
+            shared = [order.pop() for _ in range(int(r.integers(0, wide)))]
+            for i in range(b, b + rows):
+                own = [order.pop() for _ in range(int(r.integers(0, wide - len(shared) + 1)))] if len(order) > n * 2 else []
+                P.table[i, :len(shared)], P.table[i, len(shared):len(shared) + len(own)] = shared, own
+                P.held[i] = len(shared) + len(own)
+                P.lens[i] = max(0, int(P.held[i]) * page - int(r.integers(0, page)))
+                for e in shared + own:
+                    P.refs[e] += 1
+            b += rows
+        rec = P.device(torch, q)
+        for _ in range(3):
+            near = np.clip(np.arange(n) + r.integers(-3, 4, n), 0, n - 1)
+            do_fork(P, rec, np.where(r.random(n) < 0.1, -1, near).astype(np.int32))
+        assert (P.counts() == P.refs).all()
+        do_reserve(P, rec, r.integers(0, 3, n))
+        do_compact(P, rec, 1 << 20)
