@@ -10,7 +10,7 @@
 namespace qg {
 namespace {
 
-constexpr int kForkThreads = 1024, kForkCols = 8, kForkRun = 32, kForkAhead = 8;
+constexpr int kForkThreads = 1024, kForkCols = 8, kForkRun = 8, kForkAhead = 4, kForkMany = 128;
 constexpr int kPlanThreads = 1024;
 constexpr int kTableThreads = 256;
 constexpr int kHash = 2048;
@@ -54,11 +54,12 @@ __device__ __forceinline__ int parent_of(const PageArgs& a, const int32_t* paren
 // old row j is held by kids[j] rows afterwards (by none behind the page of the
 // row's last token) and was held once: refs changes by the difference. A page
 // that the rows of a prompt share stands in one column of rows next to each
-// other: a thread goes down kForkRun rows and adds up what a run of one page
-// changes by, which for beams that go on from each other is mostly nothing.
+// other: of kForkMany rows and more, a thread goes down kForkRun and adds up
+// what a run of one page changes by, which for beams that go on from each other
+// is often nothing.
 __host__ __device__ __forceinline__ int slab_at(int row, int col) { return (row + row / kForkRun) * kForkCols + col; }
 
-__global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const __grid_constant__ PageArgs a, const int32_t* parent)
+__global__ void __launch_bounds__(kForkThreads, 2) pages_fork_kernel(const __grid_constant__ PageArgs a, const int32_t* parent)
 {
     extern __shared__ int smem[];
     pdl_enter();
@@ -96,7 +97,12 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const __grid_c
 #pragma unroll
         for (int u = 0; u < kForkAhead; ++u) {
             const int j = j0 + u * step;
-            if (j < n && c < held[j]) slab[slab_at(j, tid % kForkCols)] = e[u];
+            if (j >= n || c >= held[j]) continue;
+            slab[slab_at(j, tid % kForkCols)] = e[u];
+            if (n >= kForkMany) continue;
+            const int change = (c < keep[j] ? kids[j] : 0) - 1;
+            if (!in_pool(a, e[u])) set_device_status(a.status, QG_ERR_INVALID_ARG);
+            else if (change) atomicAdd(&a.refs[e[u]], change);
         }
     }
     __syncthreads();
@@ -105,6 +111,7 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const __grid_c
         if (p < 0 || p == i || c >= keep[p]) continue;
         a.table[static_cast<int64_t>(i) * a.max_pages + c] = slab[slab_at(p, tid % kForkCols)];
     }
+    if (n < kForkMany) return;
     for (int j0 = row0 * kForkRun; j0 < n; j0 += step * kForkRun) {
         int page = -1, change = 0;
         for (int j = j0; j <= min(j0 + kForkRun, n); ++j) {
@@ -238,11 +245,15 @@ struct Share {
     int to;
 };
 
+__device__ __forceinline__ int share_words(const PageArgs& a)
+{
+    return ((a.num_pages + 31) / 32 + static_cast<int>(cluster_size()) - 1) / static_cast<int>(cluster_size());
+}
+
 __device__ __forceinline__ Share share_of(const PageArgs& a)
 {
     Share s;
-    const int all = (a.num_pages + 31) / 32, size = static_cast<int>(cluster_size());
-    const int each = (all + size - 1) / size;
+    const int all = (a.num_pages + 31) / 32, each = share_words(a);
     s.word0 = min(static_cast<int>(cluster_rank()) * each, all);
     s.words = min(each, all - s.word0);
     s.per = (s.words + kPlanThreads - 1) / kPlanThreads;
@@ -277,6 +288,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const __gri
     extern __shared__ int smem[];
     ReserveSmem& s = *reinterpret_cast<ReserveSmem*>(smem);
     uint32_t* bits = reinterpret_cast<uint32_t*>(smem + (sizeof(ReserveSmem) + 3) / 4);
+    int* before_word = reinterpret_cast<int*>(bits) + share_words(a);
     pdl_enter();
     const int b = threadIdx.x, rank = static_cast<int>(cluster_rank());
     // this thread's row, on its way while the free pages are looked for
@@ -366,15 +378,26 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const __gri
         if (enough && replaced) atomicSub(&a.refs[tail], 1);
     }
     if (enough) {
-        int lo = 0, hi = kKvMaxSeqs;                   // the last row with off <= k has the thread's first page
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (s.off[mid] <= k) lo = mid;
-            else hi = mid;
+        for (int w = sh.from; w < sh.to; ++w) {
+            before_word[w] = k;
+            k += __popc(bits[w]);
         }
-        for (int w = sh.from; w < sh.to && k < total; ++w)
-            for (uint32_t x = bits[w]; x && k < total; x &= x - 1, ++k) {
-                const int page = (sh.word0 + w) * 32 + __ffs(x) - 1;
+        __syncthreads();
+        // a thread per four pages
+        for (int i = b; i < 8 * sh.words; i += kPlanThreads) {
+            const uint32_t word = bits[i / 8], low = 4 * (i % 8);
+            k = before_word[i / 8] + __popc(word & ((1u << low) - 1u));
+            if (k >= total) break;
+            uint32_t x = word & 15u << low;
+            if (!x) continue;
+            int lo = 0, hi = kKvMaxSeqs;               // the last row with off <= k has the page
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (s.off[mid] <= k) lo = mid;
+                else hi = mid;
+            }
+            for (; x && k < total; x &= x - 1, ++k) {
+                const int page = (sh.word0 + i / 8) * 32 + __ffs(x) - 1;
                 while (s.off[lo + 1] <= k) ++lo;       // off[kKvMaxSeqs] = total
                 const int local = k - s.off[lo], c = s.first[lo];
                 const bool copy = c >= 0 && local == 0;
@@ -383,85 +406,80 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const __gri
                 a.refs[page] = 1;
                 if (copy) m.list[s.move[lo]] = make_int4(s.tail[lo], page, s.tokens[lo], 0);
             }
+        }
     }
     cluster_sync();                                    // no block leaves while another reads its count
 }
 
 // ------------------------------------------------------------------ compact
 struct CompactSmem {
-    int sums[3][32];
+    int sums[32];
     int live;
     int holes;
-    int movers;
 };
 
 // One cluster. Of L pages in use, those at L and above move into the free
-// places below L: as many of one as of the other. A block counts the holes of
-// the blocks before it and the movers of those behind it.
+// places below L: as many of one as of the other. With S(p) pages in use below
+// page p, a free one below L is hole number p - S(p), and one in use from L on
+// is number L - 1 - S(p) of those that move, counted from the highest.
 __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const __grid_constant__ PageArgs a, const MoveArgs m,
                                                                      int32_t* page_map, int32_t* n_live)
 {
     extern __shared__ int smem[];
     CompactSmem& s = *reinterpret_cast<CompactSmem*>(smem);
     uint32_t* bits = reinterpret_cast<uint32_t*>(smem + (sizeof(CompactSmem) + 3) / 4);
+    int* before_word = reinterpret_cast<int*>(bits) + share_words(a);
     pdl_enter();
     const int tid = threadIdx.x, rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
     const Share sh = share_of(a);
     scan_refs(a, sh.word0, sh.words, false, bits);
     int mine = 0;
     for (int w = sh.from; w < sh.to; ++w) mine += __popc(bits[w]);
-    int all;
-    block_scan<int>(mine, s.sums[0], all);
-    if (tid == 0) s.live = all;
+    int all, below = block_scan<int>(mine, s.sums, all);
+    if (tid == 0) {
+        s.live = all;
+        s.holes = 0;
+    }
     cluster_sync();
     int live = 0;
-    for (int x = 0; x < size; ++x) live += cluster_word(&s.live, x);
-    // bits of a word for pages below L
-    auto below = [&](int w) {
-        const int64_t n = live - static_cast<int64_t>(sh.word0 + w) * 32;
-        return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
-    };
-    int holes = 0, movers = 0;
-    for (int w = sh.from; w < sh.to; ++w) {
-        holes += __popc(~bits[w] & below(w));
-        movers += __popc(bits[w] & ~below(w));
+    for (int x = 0; x < size; ++x) {
+        const int v = cluster_word(&s.live, x);
+        if (x < rank) below += v;
+        live += v;
     }
-    int block_holes, block_movers;
-    int hole = block_scan<int>(holes, s.sums[1], block_holes);
-    const int movers_before = block_scan<int>(movers, s.sums[2], block_movers);
-    int mover = block_movers - movers_before - movers;                      // movers of the threads behind
-    if (tid == 0) {
-        s.holes = block_holes;
-        s.movers = block_movers;
+    for (int w = sh.from; w < sh.to; ++w) {
+        before_word[w] = below;
+        below += __popc(bits[w]);
+    }
+    __syncthreads();
+    // a thread per four pages: the map, places and pages of the list
+    for (int i = tid; i < 8 * sh.words; i += kPlanThreads) {
+        const uint32_t word = bits[i / 8], low = 4 * (i % 8);
+        const int page0 = (sh.word0 + i / 8) * 32 + static_cast<int>(low);
+        int under = before_word[i / 8] + __popc(word & ((1u << low) - 1u)), map[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int page = page0 + k;
+            const bool used = word >> (low + k) & 1u;
+            map[k] = used ? page : -1;
+            if (page == live) s.holes = live - under;
+            if (!used && page < live && page - under < m.capacity) m.list[page - under].y = page;
+            if (used && page >= live && live - 1 - under < m.capacity) m.list[live - 1 - under].x = page;
+            under += used;
+        }
+        if (page0 + 4 <= a.num_pages)
+            *reinterpret_cast<int4*>(page_map + page0) = make_int4(map[0], map[1], map[2], map[3]);
+        else
+            for (int k = 0; page0 + k < a.num_pages; ++k) page_map[page0 + k] = map[k];
     }
     cluster_sync();
-    int n = 0;
-    for (int x = 0; x < size; ++x) {
-        const int h = cluster_word(&s.holes, x);
-        if (x < rank) hole += h;
-        if (x > rank) mover += cluster_word(&s.movers, x);
-        n += h;
-    }
+    int n = 0;                                         // known to the block that has page L; none if all pages are in use
+    for (int x = 0; x < size; ++x) n = max(n, cluster_word(&s.holes, x));
     n = min(n, m.capacity);
     if (rank == 0 && tid == 0) {
         *m.count = n;
         if (n_live) *n_live = live;
     }
-    for (int i = tid; i < sh.words * 32; i += kPlanThreads) {
-        const int page = sh.word0 * 32 + i;
-        if (page < a.num_pages) page_map[page] = bits[i / 32] >> (i & 31) & 1u ? page : -1;
-    }
-    // places and pages of the list, each by the thread that found it
-    for (int w = sh.from; w < sh.to && hole < n; ++w)
-        for (uint32_t x = ~bits[w] & below(w); x && hole < n; x &= x - 1, ++hole)
-            m.list[hole].y = (sh.word0 + w) * 32 + __ffs(x) - 1;
-    for (int w = sh.to - 1; w >= sh.from && mover < n; --w)
-        for (uint32_t x = bits[w] & ~below(w); x && mover < n; ++mover) {
-            const int bit = 31 - __clz(x);
-            x ^= 1u << bit;
-            m.list[mover].x = (sh.word0 + w) * 32 + bit;
-        }
-    cluster_sync();
     // then the moves side by side
     constexpr int kAhead = 4;
     const int step = kPlanThreads * size;
@@ -483,6 +501,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const __gri
                 page_map[e[u].x] = e[u].y;
             }
     }
+    cluster_sync();                                    // no block leaves while another reads its count
 }
 
 // The entries in use, through the map.
@@ -596,7 +615,7 @@ __global__ void __launch_bounds__(32 * kCopyWarps) pages_copy_kernel(const __gri
 // way into shared memory and stores them from there, all with bulk copies (rows
 // are multiples of 32 bytes); the other warps copy scales. Whole pages are cut
 // into chunks, others into those of each head's tokens.
-constexpr int kBulkChunk = 16 << 10, kBulkStages = 12, kBulkAhead = 8;
+constexpr int kBulkChunk = 16 << 10, kBulkStages = 6, kBulkAhead = 4, kBulkBlocks = 2;
 constexpr uint64_t kBulkWaitNs = 1000000000ull;
 
 struct BulkChunk {
@@ -605,7 +624,7 @@ struct BulkChunk {
     uint32_t bytes;
 };
 
-__global__ void __launch_bounds__(32 * kCopyWarps, 1) pages_copy_bulk_kernel(const __grid_constant__ KvArgs a, const MoveArgs m,
+__global__ void __launch_bounds__(32 * kCopyWarps, kBulkBlocks) pages_copy_bulk_kernel(const __grid_constant__ KvArgs a, const MoveArgs m,
                                                                              int code_chunks, int scale_items)
 {
     extern __shared__ __align__(128) uint8_t ring[];
@@ -702,7 +721,7 @@ __global__ void __launch_bounds__(32 * kCopyWarps, 1) pages_copy_bulk_kernel(con
 }
 
 // ------------------------------------------------------------------ launches
-constexpr int kPlanSmemMax = 160 << 10;
+constexpr int kPlanSmemMax = 192 << 10;
 
 // One block scans a small pool, a cluster of eight a large one.
 int plan_blocks(const PageArgs& a) { return a.num_pages > 8192 ? 8 : 1; }
@@ -710,7 +729,7 @@ int plan_blocks(const PageArgs& a) { return a.num_pages > 8192 ? 8 : 1; }
 size_t plan_smem(const PageArgs& a, size_t fixed)
 {
     const int words = (a.num_pages + 31) / 32, blocks = plan_blocks(a);
-    return (fixed + 3) / 4 * 4 + static_cast<size_t>((words + blocks - 1) / blocks) * 4;
+    return (fixed + 3) / 4 * 4 + static_cast<size_t>((words + blocks - 1) / blocks) * 8;
 }
 
 bool allow_smem(const void* kern, bool (&set)[64], int bytes = kPlanSmemMax)
@@ -809,8 +828,8 @@ qg_status launch_pages_copy(const KvArgs& in, const MoveArgs& m, cudaStream_t st
         constexpr int kSmem = kBulkStages * kBulkChunk;
         if (!allow_smem(reinterpret_cast<const void*>(pages_copy_bulk_kernel), set, kSmem)) return QG_ERR_CUDA;
         const int code_chunks = a.heads * static_cast<int>((static_cast<int64_t>(a.page_size) * kv_row_bytes(a.fmt, a.dim) + kBulkChunk - 1) / kBulkChunk);
-        const cudaError_t e = launch_pdl(pages_copy_bulk_kernel, dim3(static_cast<unsigned>(sm_count(-1))), dim3(32 * kCopyWarps),
-                                         kSmem, stream, a, m, code_chunks, scale_items);
+        const cudaError_t e = launch_pdl(pages_copy_bulk_kernel, dim3(static_cast<unsigned>(kBulkBlocks * sm_count(-1))),
+                                         dim3(32 * kCopyWarps), kSmem, stream, a, m, code_chunks, scale_items);
         return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;
     }
     const int64_t warps = static_cast<int64_t>(m.capacity) * 2 * (code_items + scale_items);
