@@ -383,28 +383,37 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const __gri
             k += __popc(bits[w]);
         }
         __syncthreads();
-        // a thread per four pages
-        for (int i = b; i < 8 * sh.words; i += kPlanThreads) {
-            const uint32_t word = bits[i / 8], low = 4 * (i % 8);
-            k = before_word[i / 8] + __popc(word & ((1u << low) - 1u));
-            if (k >= total) break;
-            uint32_t x = word & 15u << low;
-            if (!x) continue;
-            int lo = 0, hi = kKvMaxSeqs;               // the last row with off <= k has the page
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (s.off[mid] <= k) lo = mid;
-                else hi = mid;
-            }
-            for (; x && k < total; x &= x - 1, ++k) {
+        // a thread per four pages, a warp per 128: the row of its first one is looked for by all lanes, the lanes' own
+        // follow soon
+        const int lane = b & 31;
+        for (int i0 = b - lane; i0 < 8 * sh.words; i0 += kPlanThreads) {
+            const int i = i0 + lane;
+            const bool in = i < 8 * sh.words;
+            const uint32_t word = in ? bits[i / 8] : 0u, low = 4 * (i % 8);
+            k = in ? before_word[i / 8] + __popc(word & ((1u << low) - 1u)) : INT32_MAX;
+            const int k0 = __shfl_sync(0xffffffffu, k, 0);
+            if (k0 >= total) break;
+            const int part = __popc(__ballot_sync(0xffffffffu, s.off[32 * lane] <= k0)) - 1;
+            int lo = 32 * part + __popc(__ballot_sync(0xffffffffu, s.off[32 * part + lane] <= k0)) - 1;
+            int next = s.off[lo + 1], col = 0;
+            int32_t* row = nullptr;
+            for (uint32_t x = word & 15u << low; x && k < total; x &= x - 1, ++k) {
                 const int page = (sh.word0 + i / 8) * 32 + __ffs(x) - 1;
-                while (s.off[lo + 1] <= k) ++lo;       // off[kKvMaxSeqs] = total
-                const int local = k - s.off[lo], c = s.first[lo];
-                const bool copy = c >= 0 && local == 0;
-                const int col = copy ? c : s.held[lo] + local - (c >= 0);
-                a.table[static_cast<int64_t>(lo) * a.max_pages + col] = page;
+                if (!row || k >= next) {               // the last row with off <= k; off[kKvMaxSeqs] = total
+                    while (k >= next) next = s.off[++lo + 1];
+                    row = a.table + static_cast<int64_t>(lo) * a.max_pages;
+                    const int local = k - s.off[lo], c = s.first[lo];
+                    col = s.held[lo] + local - (c >= 0);
+                    if (c >= 0 && local == 0) {        // the one that is replaced comes before new ones
+                        row[c] = page;
+                        m.list[s.move[lo]] = make_int4(s.tail[lo], page, s.tokens[lo], 0);
+                        a.refs[page] = 1;
+                        ++col;
+                        continue;
+                    }
+                }
+                row[col++] = page;
                 a.refs[page] = 1;
-                if (copy) m.list[s.move[lo]] = make_int4(s.tail[lo], page, s.tokens[lo], 0);
             }
         }
     }

@@ -626,31 +626,31 @@ class KVMoves:
                    torch.zeros(1, dtype=torch.int32, device=device))
 
 
-def _kv_int32(name, t, index, shape):
+def _kv_int32(name, t, index, n):
     import torch
-    if t is not None and (t.dtype is not torch.int32 or t.get_device() != index or t.shape != shape or
-                          not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on the pages' device")
+    if t.dtype is not torch.int32 or t.get_device() != index or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [{n}] on the pages' device")
+    return t.data_ptr()
 
 
 def kv_pages_fork(pages, parent, stream=None):
     """Row i of the pages goes on from row parent[i] (int32 [n]; -1: from
     nothing, which frees its pages), sharing that row's pages."""
-    _kv_int32("parent", parent, pages.index, (pages.n_seqs,))
+    parent = _kv_int32("parent", parent, pages.index, pages.n_seqs)
     with _OnDevice(pages.index):
-        _check("kv_pages_fork", lib().kv_pages_fork(pages.ref, _ptr(parent), _stream(stream, pages.refs)))
+        _check("kv_pages_fork", lib().kv_pages_fork(pages.ref, parent, _stream(stream, pages.refs)))
 
 
 def kv_pages_reserve(pages, n_new, moves, n_free=None, stream=None):
     """Pages of its own for each sequence's next n_new tokens (int32 [n]); the
     part-filled pages that are replaced join `moves`. n_free int32 [1]: the free
     pages left, negative (and nothing changed) where they do not suffice."""
-    _kv_int32("n_new", n_new, pages.index, (pages.n_seqs,))
-    _kv_int32("n_free", n_free, pages.index, (1,))
+    n_new = _kv_int32("n_new", n_new, pages.index, pages.n_seqs)
+    n_free = None if n_free is None else _kv_int32("n_free", n_free, pages.index, 1)
     if moves.index != pages.index:
         raise ValueError("pages and moves must be on one device")
     with _OnDevice(pages.index):
-        _check("kv_pages_reserve", lib().kv_pages_reserve(pages.ref, _ptr(n_new), moves.ref, _ptr(n_free),
+        _check("kv_pages_reserve", lib().kv_pages_reserve(pages.ref, n_new, moves.ref, n_free,
                                                           _stream(stream, pages.refs)))
 
 
@@ -658,12 +658,12 @@ def kv_pages_compact(pages, moves, page_map, n_live=None, stream=None):
     """Give the highest pages in use the lowest free numbers, moves.capacity of
     them at most; page_map int32 [num_pages] receives each page's number, n_live
     int32 [1] the pages in use."""
-    _kv_int32("page_map", page_map, pages.index, (pages.num_pages,))
-    _kv_int32("n_live", n_live, pages.index, (1,))
+    where = _kv_int32("page_map", page_map, pages.index, pages.num_pages)
+    n_live = None if n_live is None else _kv_int32("n_live", n_live, pages.index, 1)
     if moves.index != pages.index:
         raise ValueError("pages and moves must be on one device")
     with _OnDevice(pages.index):
-        _check("kv_pages_compact", lib().kv_pages_compact(pages.ref, moves.ref, _ptr(page_map), _ptr(n_live),
+        _check("kv_pages_compact", lib().kv_pages_compact(pages.ref, moves.ref, where, n_live,
                                                           _stream(stream, pages.refs)))
     return page_map
 
@@ -694,33 +694,34 @@ def beam_select(logits, scores, out_scores, out_tokens, out_parents, out_finishe
     beam_select_workspace_size bytes, not shared by calls that may overlap on
     the GPU."""
     import torch
-    dev = logits.get_device()
-    if dev < 0:
-        raise ValueError("logits must be a CUDA tensor")
-    if scores.dim() != 2 or out_scores.dim() != 2 or logits.dim() != 2:
+    dev, wide, shape, out = logits.get_device(), logits.dtype is torch.float32, scores.shape, out_scores.shape
+    if dev < 0 or not (wide or logits.dtype is torch.bfloat16):
+        raise ValueError("logits must be a bfloat16 or float32 CUDA tensor")
+    if logits.dim() != 2 or len(shape) != 2 or len(out) != 2 or out[0] != shape[0]:
         raise ValueError("logits must be [lanes * beams][vocab], scores [lanes][beams] and outputs [lanes][n_out]")
-    (lanes, beams), n_out, (rows, vocab) = scores.shape, out_scores.shape[1], logits.shape
-    if rows != lanes * beams or (vocab > 1 and logits.stride(1) != 1):
+    (lanes, beams), (rows, vocab), (row_stride, step) = shape, logits.shape, logits.stride()
+    if rows != lanes * beams or (step != 1 and vocab > 1):
         raise ValueError("logits must have a row for each of the scores, with its values next to each other")
-    if logits.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("logits must be bfloat16 or float32")
-    _kv_tensors(dev, scores, out_scores, out_tokens, out_parents, out_finished, finished, workspace)
-    out = (lanes, n_out)
-    for name, t, shape, types in (("scores", scores, (lanes, beams), (torch.float32,)),
-                                  ("finished", finished, (lanes, beams), (torch.bool, torch.uint8)),
-                                  ("out_scores", out_scores, out, (torch.float32,)),
-                                  ("out_tokens", out_tokens, out, (torch.int32,)),
-                                  ("out_parents", out_parents, out, (torch.int32,)),
-                                  ("out_finished", out_finished, out, (torch.bool, torch.uint8))):
-        if t is not None and (t.shape != shape or t.dtype not in types):
-            raise ValueError(f"{name} must be {' or '.join(map(str, types))} {list(shape)}")
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    dt = QG_OUT_F32 if logits.dtype is torch.float32 else QG_OUT_BF16
+    for t, dtype, like in ((scores, torch.float32, shape), (out_scores, torch.float32, out), (out_tokens, torch.int32, out),
+                           (out_parents, torch.int32, out)):
+        if t.dtype is not dtype or t.shape != like or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("scores [lanes][beams] and out_scores (float32), out_tokens and out_parents (int32) "
+                             "[lanes][n_out] must be contiguous CUDA tensors on one device")
+    for t, like in ((finished, shape), (out_finished, out)):
+        if t is not None and (t.shape != like or t.get_device() != dev or not t.is_contiguous() or
+                              not (t.dtype is torch.bool or t.dtype is torch.uint8)):
+            raise ValueError("finished [lanes][beams] and out_finished [lanes][n_out] must be contiguous bool or uint8 CUDA "
+                             "tensors on one device")
+    nbytes = 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor on the logits' device")
+        nbytes = workspace.nbytes
     with _OnDevice(dev):
         _check("beam_select", lib().beam_select(
-            _ptr(logits), dt, logits.stride(0) if rows > 1 else vocab, lanes, beams, vocab, _ptr(scores), _ptr(finished),
-            int(eos), int(pad), n_out, _ptr(out_scores), _ptr(out_tokens), _ptr(out_parents), _ptr(out_finished),
-            _ptr(workspace), nbytes, _stream(stream, logits)))
+            logits.data_ptr(), QG_OUT_F32 if wide else QG_OUT_BF16, row_stride if rows > 1 else vocab, lanes, beams, vocab,
+            scores.data_ptr(), _ptr(finished), eos, pad, out[1], out_scores.data_ptr(), out_tokens.data_ptr(),
+            out_parents.data_ptr(), _ptr(out_finished), _ptr(workspace), nbytes, _stream(stream, logits)))
     return out_scores, out_tokens, out_parents, out_finished
 
 
