@@ -11,6 +11,7 @@ namespace qg {
 namespace {
 
 constexpr int kForkThreads = 1024, kForkCols = 8, kForkRun = 8, kForkAhead = 4, kForkMany = 128;
+constexpr int kFewThreads = 512, kFewRows = 64, kFewCols = 64;
 constexpr int kPlanThreads = 1024;
 constexpr int kTableThreads = 256;
 constexpr int kHash = 2048;
@@ -46,6 +47,28 @@ __device__ __forceinline__ int parent_of(const PageArgs& a, const int32_t* paren
     const int p = parent[i];
     bad = p < -1 || p >= a.n_seqs;
     return bad ? i : p;
+}
+
+// ------------------------------------------------------------------ clusters
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Every thread of the cluster arrives and waits; what was written before, to
+// shared or global memory, is seen after.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ fork
@@ -149,28 +172,58 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_rows_kernel(const __g
     }
 }
 
+// Few rows: one launch, of a cluster whose blocks have all read the lengths
+// before one of them writes any.
+__global__ void __launch_bounds__(kFewThreads) pages_fork_few_kernel(const __grid_constant__ PageArgs a, const int32_t* parent)
+{
+    __shared__ int par[kFewRows], keep[kFewRows], held[kFewRows], kids[kFewRows], lens[kFewRows];
+    __shared__ int slab[kFewRows][kFewCols];
+    __shared__ int most;
+    pdl_enter();
+    const int n = a.n_seqs, tid = threadIdx.x, rank = static_cast<int>(cluster_rank());
+    if (tid < n) kids[tid] = 0;
+    if (tid == 0) most = 0;
+    __syncthreads();
+    if (tid < n) {
+        bool bad;
+        const PageRow r = page_row(a, tid);
+        const int p = parent_of(a, parent, tid, bad);
+        if (rank == 0 && (bad || !r.ok)) set_device_status(a.status, QG_ERR_INVALID_ARG);
+        par[tid] = p;
+        keep[tid] = (r.len + a.page_size - 1) / a.page_size;
+        held[tid] = r.held;
+        lens[tid] = r.len;
+        atomicMax(&most, r.held);
+        if (p >= 0) atomicAdd(&kids[p], 1);
+    }
+    cluster_sync();
+    if (rank == 0 && tid < n) {
+        const int p = par[tid];
+        a.lens[tid] = p < 0 ? 0 : lens[p];
+        a.held[tid] = p < 0 ? 0 : keep[p];
+    }
+    const int col = tid % kFewCols, step = kFewThreads / kFewCols;
+    for (int c = rank * kFewCols + col; c - col < most; c += static_cast<int>(cluster_size()) * kFewCols) {
+#pragma unroll 4
+        for (int j = tid / kFewCols; j < n; j += step) {
+            if (c >= held[j]) continue;
+            const int e = a.table[static_cast<int64_t>(j) * a.max_pages + c];
+            slab[j][col] = e;
+            const int change = (c < keep[j] ? kids[j] : 0) - 1;
+            if (!in_pool(a, e)) set_device_status(a.status, QG_ERR_INVALID_ARG);
+            else if (change) atomicAdd(&a.refs[e], change);
+        }
+        __syncthreads();
+        for (int i = tid / kFewCols; i < n; i += step) {
+            const int p = par[i];
+            if (p < 0 || p == i || c >= keep[p]) continue;
+            a.table[static_cast<int64_t>(i) * a.max_pages + c] = slab[p][col];
+        }
+        __syncthreads();
+    }
+}
+
 // ------------------------------------------------------------------ scans over the pool
-__device__ __forceinline__ uint32_t cluster_size()
-{
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// Every thread of the cluster arrives and waits; what was written before, to
-// shared or global memory, is seen after.
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
 // The word at `p` of this block's shared memory in block `rank` of the cluster.
 __device__ __forceinline__ int cluster_word(const int* p, uint32_t rank)
 {
@@ -753,11 +806,11 @@ bool allow_smem(const void* kern, bool (&set)[64], int bytes = kPlanSmemMax)
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kern)(KArgs...), int blocks, size_t smem, cudaStream_t stream, Args... args)
+cudaError_t launch_cluster(void (*kern)(KArgs...), int blocks, size_t smem, cudaStream_t stream, int threads, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(kPlanThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -785,7 +838,13 @@ qg_status launch_pages_fork(const PageArgs& in, const int32_t* parent, cudaStrea
 {
     static bool set[64] = {};
     PageArgs a;
-    if (!with_status(in, a) || !allow_smem(reinterpret_cast<const void*>(pages_fork_kernel), set)) return QG_ERR_CUDA;
+    if (!with_status(in, a)) return QG_ERR_CUDA;
+    if (a.n_seqs <= kFewRows && a.max_pages <= 64 * kFewCols) {
+        const cudaError_t e = launch_cluster(pages_fork_few_kernel, min((a.max_pages - 1) / kFewCols + 1, 8), 0, stream, kFewThreads,
+                                             a, parent);
+        return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+    }
+    if (!allow_smem(reinterpret_cast<const void*>(pages_fork_kernel), set)) return QG_ERR_CUDA;
     const size_t smem = (static_cast<size_t>(a.n_seqs) * 4 + slab_at(a.n_seqs - 1, kForkCols)) * 4;
     const int threads = min(kForkThreads, max(64, (a.n_seqs * kForkCols + 31) / 32 * 32));
     cudaError_t e = launch_pdl(pages_fork_kernel, dim3(static_cast<unsigned>((a.max_pages - 1) / kForkCols + 1)),
@@ -801,7 +860,7 @@ qg_status launch_pages_reserve(const PageArgs& in, const int32_t* n_new, const M
     PageArgs a;
     if (!with_status(in, a) || !allow_smem(reinterpret_cast<const void*>(pages_reserve_kernel), set)) return QG_ERR_CUDA;
     const cudaError_t e = launch_cluster(pages_reserve_kernel, plan_blocks(a), plan_smem(a, sizeof(ReserveSmem)), stream,
-                                         a, n_new, m, n_free);
+                                         kPlanThreads, a, n_new, m, n_free);
     return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 
@@ -811,7 +870,8 @@ qg_status launch_pages_compact(const PageArgs& in, const MoveArgs& m, int32_t* p
     static bool set[64] = {};
     PageArgs a;
     if (!with_status(in, a) || !allow_smem(reinterpret_cast<const void*>(pages_compact_kernel), set)) return QG_ERR_CUDA;
-    cudaError_t e = launch_cluster(pages_compact_kernel, plan_blocks(a), plan_smem(a, sizeof(CompactSmem)), stream, a, m,
+    cudaError_t e = launch_cluster(pages_compact_kernel, plan_blocks(a), plan_smem(a, sizeof(CompactSmem)), stream,
+                                   kPlanThreads, a, m,
                                    page_map, n_live);
     if (e == cudaSuccess && a.n_seqs) {
         const int blocks = min((a.max_pages - 1) / kTableThreads + 1, 64);

@@ -464,3 +464,16 @@ def test_many_rows_share_and_part():
         assert (P.counts() == P.refs).all()
         do_reserve(P, rec, r.integers(0, 3, n))
         do_compact(P, rec, 1 << 20)
+
+
+@pytest.mark.parametrize("sizes", [(64, 300, 9000, 16), (64, 4096, 200000, 16), (64, 4097, 200000, 16), (65, 300, 9000, 16), (1, 4096, 5000, 16),
+                                   (127, 9, 900, 32), (128, 9, 900, 32), (129, 17, 2000, 32)])
+def test_fork_at_the_borders_of_its_kernels(sizes):
+    r = np.random.default_rng(18)
+    P = PU.random_pages(r, *sizes)
+    rec = P.device(torch, q)
+    for _ in range(3):
+        do_fork(P, rec, r.integers(-1, P.n, P.n).astype(np.int32))
+    P.table[0, :max(1, P.held[0])], P.held[0], P.lens[0] = -1, max(1, P.held[0]), 1        # entries outside the pool
+    rec = P.device(torch, q)
+    do_fork(P, rec, np.zeros(P.n, np.int32))
