@@ -68,7 +68,8 @@ __device__ __forceinline__ uint32_t cluster_rank()
 // shared or global memory, is seen after.
 __device__ __forceinline__ void cluster_sync()
 {
-    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+    if (cluster_size() == 1) __syncthreads();
+    else asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ fork
@@ -234,51 +235,74 @@ __device__ __forceinline__ int cluster_word(const int* p, uint32_t rank)
     return v;
 }
 
-// Sum over the block of v, and what the threads before this one have. Each
-// scan of a kernel has its own warp_sums, so that one barrier is enough.
+// Sum over the block of v, and what the threads before this one have: of two
+// numbers with one barrier. Each scan of a kernel has its own warp_sums.
 template <typename T>
-__device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total)
+__device__ __forceinline__ T warp_scan(T v)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    T x = v;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const T y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const T y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
     }
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    T s = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const T y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
-    }
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ T before_warp(const T* warp_sums, T& total)
+{
+    const int warp = threadIdx.x >> 5;
+    const T s = warp_scan(warp_sums[threadIdx.x & 31]);
     total = __shfl_sync(0xffffffffu, s, 31);
     const T before = __shfl_sync(0xffffffffu, s, warp ? warp - 1 : 0);
-    return x - v + (warp ? before : T(0));
+    return warp ? before : T(0);
+}
+
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total)
+{
+    const int x = warp_scan(v);
+    if ((threadIdx.x & 31) == 31) warp_sums[threadIdx.x >> 5] = x;
+    __syncthreads();
+    return x - v + before_warp(warp_sums, total);
 }
 
 // A block's share of the pool, `words` words of 32 pages from word `word0` on:
 // bit i of a word is set for a page that is held (free_bits: that is free).
 // Pages behind the pool have bit 0.
-__device__ __forceinline__ void scan_refs(const PageArgs& a, int word0, int words, bool free_bits, uint32_t* bits)
+struct RefsLoad {
+    int4 r;
+
+    // the counts of four pages of a thread, 0 behind the pool
+    __device__ __forceinline__ RefsLoad(const PageArgs& a, int word0, int words, int base)
+    {
+        const int at = base + 4 * static_cast<int>(threadIdx.x);
+        const int64_t p = static_cast<int64_t>(word0) * 32 + at;
+        r = int4{};
+        if (at >= words * 32) return;
+        if (p + 4 <= a.num_pages) {
+            r = *reinterpret_cast<const int4*>(a.refs + p);
+        } else {
+            if (p < a.num_pages) r.x = a.refs[p];
+            if (p + 1 < a.num_pages) r.y = a.refs[p + 1];
+            if (p + 2 < a.num_pages) r.z = a.refs[p + 2];
+        }
+    }
+};
+
+// `ahead`: the first ones, loaded before.
+__device__ __forceinline__ void scan_refs(const PageArgs& a, int word0, int words, bool free_bits, uint32_t* bits, RefsLoad ahead)
 {
     const int lane = threadIdx.x & 31;
     const int64_t first = static_cast<int64_t>(word0) * 32;
     for (int base = 0; base < words * 32; base += 4 * kPlanThreads) {
         const int at = base + 4 * static_cast<int>(threadIdx.x);
-        const int64_t p = first + at;
-        uint32_t nib = 0;
-        if (at < words * 32) {
-            if (p + 4 <= a.num_pages) {
-                const int4 r = *reinterpret_cast<const int4*>(a.refs + p);
-                nib = (r.x != 0) | (r.y != 0) << 1 | (r.z != 0) << 2 | (r.w != 0) << 3;
-                if (free_bits) nib ^= 15u;
-            } else {
-                for (int i = 0; i < 4; ++i)
-                    if (p + i < a.num_pages) nib |= static_cast<uint32_t>((a.refs[p + i] != 0) != free_bits) << i;
-            }
+        const int4 r = ahead.r;
+        if (base + 4 * kPlanThreads < words * 32) ahead = RefsLoad(a, word0, words, base + 4 * kPlanThreads);
+        uint32_t nib = (r.x != 0) | (r.y != 0) << 1 | (r.z != 0) << 2 | (r.w != 0) << 3;
+        if (free_bits) {
+            const int64_t left = a.num_pages - first - at;
+            nib = ~nib & (left >= 4 ? 15u : left <= 0 ? 0u : (1u << left) - 1u);
         }
         uint32_t w = nib << (4 * (lane & 7));
         w |= __shfl_xor_sync(0xffffffffu, w, 1);
@@ -344,6 +368,8 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const __gri
     int* before_word = reinterpret_cast<int*>(bits) + share_words(a);
     pdl_enter();
     const int b = threadIdx.x, rank = static_cast<int>(cluster_rank());
+    const Share sh = share_of(a);
+    const RefsLoad ahead(a, sh.word0, sh.words, 0);
     // this thread's row, on its way while the free pages are looked for
     PageRow r{0, 0, true};
     int add = 0;
@@ -356,8 +382,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const __gri
         s.writers[i] = 0;
         s.lowest[i] = kKvMaxSeqs;
     }
-    const Share sh = share_of(a);
-    scan_refs(a, sh.word0, sh.words, true, bits);
+    scan_refs(a, sh.word0, sh.words, true, bits, ahead);
     int mine = 0;
     for (int w = sh.from; w < sh.to; ++w) mine += __popc(bits[w]);
 
@@ -400,8 +425,18 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const __gri
     const bool replaced = slot >= 0 && !(s.writers[slot] == count && s.lowest[slot] == b);
     const int fresh = writes ? max(0, last - r.held) : 0;
     // new pages (at most 2^26 + 1 of a row), and in the lower 11 bits replaced ones (at most 2^10)
+    const int64_t want = (static_cast<int64_t>(fresh) + replaced) << 11 | replaced;
+    const int64_t rows_to = warp_scan(want);
+    const int pages_to = warp_scan(mine);
+    if ((b & 31) == 31) {
+        s.row_sums[b >> 5] = rows_to;
+        s.page_sums[b >> 5] = pages_to;
+    }
+    __syncthreads();
     int64_t both;
-    const int64_t before = block_scan<int64_t>((static_cast<int64_t>(fresh) + replaced) << 11 | replaced, s.row_sums, both);
+    int block_free;
+    const int64_t before = rows_to - want + before_warp(s.row_sums, both);
+    int k = pages_to - mine + before_warp(s.page_sums, block_free);
     const int64_t total = both >> 11;
     const int moves = static_cast<int>(both & 2047);
     s.off[b] = static_cast<int>(before >> 11);         // exact where it is used: total <= the pool's pages
@@ -412,7 +447,6 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const __gri
     s.move[b] = static_cast<int>(before & 2047);
     if (b == 0) s.off[kKvMaxSeqs] = static_cast<int>(total);
 
-    int block_free, k = block_scan<int>(mine, s.page_sums, block_free);
     if (b == 0) s.count = block_free;
     cluster_sync();
     int64_t free_pages = 0;
@@ -494,10 +528,10 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const __gri
     pdl_enter();
     const int tid = threadIdx.x, rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
     const Share sh = share_of(a);
-    scan_refs(a, sh.word0, sh.words, false, bits);
+    scan_refs(a, sh.word0, sh.words, false, bits, RefsLoad(a, sh.word0, sh.words, 0));
     int mine = 0;
     for (int w = sh.from; w < sh.to; ++w) mine += __popc(bits[w]);
-    int all, below = block_scan<int>(mine, s.sums, all);
+    int all, below = block_scan(mine, s.sums, all);
     if (tid == 0) {
         s.live = all;
         s.holes = 0;
