@@ -359,7 +359,7 @@ struct ReserveSmem {
 // share of the pool; with the free pages of the blocks before it, it knows the
 // number that each of its free pages has among all, and so the row and the
 // column that each is for. Nothing is written before every block has read.
-__global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const __grid_constant__ PageArgs a, const int32_t* n_new,
+__global__ void __launch_bounds__(kPlanThreads, 1) pages_reserve_kernel(const __grid_constant__ PageArgs a, const int32_t* n_new,
                                                                      const MoveArgs m, int32_t* n_free)
 {
     extern __shared__ int smem[];
@@ -819,15 +819,6 @@ __global__ void __launch_bounds__(32 * kCopyWarps, kBulkBlocks) pages_copy_bulk_
 // ------------------------------------------------------------------ launches
 constexpr int kPlanSmemMax = 192 << 10;
 
-// One block scans a small pool, a cluster of eight a large one.
-int plan_blocks(const PageArgs& a) { return a.num_pages > 8192 ? 8 : 1; }
-
-size_t plan_smem(const PageArgs& a, size_t fixed)
-{
-    const int words = (a.num_pages + 31) / 32, blocks = plan_blocks(a);
-    return (fixed + 3) / 4 * 4 + static_cast<size_t>((words + blocks - 1) / blocks) * 8;
-}
-
 bool allow_smem(const void* kern, bool (&set)[64], int bytes = kPlanSmemMax)
 {
     int dev = 0;
@@ -837,6 +828,41 @@ bool allow_smem(const void* kern, bool (&set)[64], int bytes = kPlanSmemMax)
         set[dev] = true;
     }
     return true;
+}
+
+// One block scans a small pool (a cluster of eight takes 0.8 us longer for
+// 1,200 pages), a cluster of 16 a large one, or of eight where the device has
+// no room for such (24,000 pages handed out of 140,000: 12.2 us, by eight 14.4);
+// 0 on an error.
+int plan_blocks(const PageArgs& a, const void* kern, int (&most)[64])
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (!most[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanSmemMax) != cudaSuccess) return 0;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 16;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(kPlanThreads);
+        cfg.dynamicSmemBytes = kPlanSmemMax;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int room = 0;
+        const bool asked = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                           cudaOccupancyMaxActiveClusters(&room, kern, &cfg) == cudaSuccess;
+        if (!asked) cudaGetLastError();
+        most[dev] = asked && room > 0 ? 16 : 8;
+    }
+    return a.num_pages > 8192 ? most[dev] : 1;
+}
+
+size_t plan_smem(const PageArgs& a, size_t fixed, int blocks)
+{
+    const int words = (a.num_pages + 31) / 32;
+    return (fixed + 3) / 4 * 4 + static_cast<size_t>((words + blocks - 1) / blocks) * 8;
 }
 
 template <typename... KArgs, typename... Args>
@@ -890,10 +916,11 @@ qg_status launch_pages_fork(const PageArgs& in, const int32_t* parent, cudaStrea
 qg_status launch_pages_reserve(const PageArgs& in, const int32_t* n_new, const MoveArgs& m, int32_t* n_free,
                                cudaStream_t stream)
 {
-    static bool set[64] = {};
+    static int most[64] = {};
     PageArgs a;
-    if (!with_status(in, a) || !allow_smem(reinterpret_cast<const void*>(pages_reserve_kernel), set)) return QG_ERR_CUDA;
-    const cudaError_t e = launch_cluster(pages_reserve_kernel, plan_blocks(a), plan_smem(a, sizeof(ReserveSmem)), stream,
+    const int blocks = plan_blocks(in, reinterpret_cast<const void*>(pages_reserve_kernel), most);
+    if (!blocks || !with_status(in, a)) return QG_ERR_CUDA;
+    const cudaError_t e = launch_cluster(pages_reserve_kernel, blocks, plan_smem(a, sizeof(ReserveSmem), blocks), stream,
                                          kPlanThreads, a, n_new, m, n_free);
     return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
@@ -901,15 +928,15 @@ qg_status launch_pages_reserve(const PageArgs& in, const int32_t* n_new, const M
 qg_status launch_pages_compact(const PageArgs& in, const MoveArgs& m, int32_t* page_map, int32_t* n_live,
                                cudaStream_t stream)
 {
-    static bool set[64] = {};
+    static int most[64] = {};
     PageArgs a;
-    if (!with_status(in, a) || !allow_smem(reinterpret_cast<const void*>(pages_compact_kernel), set)) return QG_ERR_CUDA;
-    cudaError_t e = launch_cluster(pages_compact_kernel, plan_blocks(a), plan_smem(a, sizeof(CompactSmem)), stream,
-                                   kPlanThreads, a, m,
-                                   page_map, n_live);
+    const int blocks = plan_blocks(in, reinterpret_cast<const void*>(pages_compact_kernel), most);
+    if (!blocks || !with_status(in, a)) return QG_ERR_CUDA;
+    cudaError_t e = launch_cluster(pages_compact_kernel, blocks, plan_smem(a, sizeof(CompactSmem), blocks), stream,
+                                   kPlanThreads, a, m, page_map, n_live);
     if (e == cudaSuccess && a.n_seqs) {
-        const int blocks = min((a.max_pages - 1) / kTableThreads + 1, 64);
-        e = launch_pdl(pages_table_kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a.n_seqs)),
+        const int wide = min((a.max_pages - 1) / kTableThreads + 1, 64);
+        e = launch_pdl(pages_table_kernel, dim3(static_cast<unsigned>(wide), static_cast<unsigned>(a.n_seqs)),
                        dim3(kTableThreads), 0, stream, a, static_cast<const int32_t*>(page_map));
     }
     return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;

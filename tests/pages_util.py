@@ -181,19 +181,19 @@ def log_sums(x):
 def sum_bound(x):
     """How far a row's ln sum may be off. A term's argument v - top is rounded,
     multiplied by a rounded log2(e) and rounded: 3 half steps, 3 * 2^-24 |v -
-    top| of the term; the hardware's 2^x is off by 2^-22 of it (its documented
-    bound is below that). A thread adds up to vocab / 256 + 8 terms one after
-    another, half a step each, and rescales at most as often with two roundings
-    and a 2^x; lanes, warps and parts join in fewer than 32 further steps."""
+    top| of the term, and so for the factor that brings a piece to the row's
+    maximum; the hardware's 2^x is off by 2^-22 of it (its documented bound is
+    below that). A lane adds 16 pairs, their two halves and, of the pieces of
+    1,024, every 32nd, each of these with a factor; 10 steps join the lanes. One
+    addition is a half step of the sum, one with a factor 7 at most. The
+    logarithm is off by less than 2^-23, of which a half step is its rounding."""
     with np.errstate(all="ignore"):
         top = x.max(1, keepdims=True)
         w = np.exp(x - top)
         p = w / w.sum(1, keepdims=True)
         far = np.where(p > 0, p * np.where(np.isfinite(x), top - x, 0.0), 0.0).sum(1)
-        n = x.shape[1] / 256 + 40
-        # a rescaled maximum is off by the same relative errors as a term; each rescale counts once per thread's run of
-        # maxima, which for a thread's sum is at most n times (2 + 4) half steps
-        return 3 * 2.0 ** -24 * far + 2.0 ** -22 + 7 * n * 2.0 ** -24
+        n = x.shape[1] / 32768 + 16 + 1 + 10 + 4
+        return 3 * 2.0 ** -24 * far + 2.0 ** -22 + 7 * n * 2.0 ** -24 + 2.0 ** -23
 
 
 def check_selection(x, scores, finished, eos, pad, got, n_out):

@@ -296,3 +296,41 @@ def test_many_logits_give_the_same_bits_every_time():
     first = call(x, "fp32", scores, 8)
     for _ in range(5):
         assert all(np.array_equal(a, b) for a, b in zip(first, call(x, "fp32", scores, 8)))
+
+
+@pytest.mark.parametrize("lanes,beams,vocab,n_out", [(400, 64, 40, 64), (5000, 3, 7, 4), (1, 1, 1 << 24, 4), (1, 64, 70001, 64)])
+def test_sizes_at_the_limits(lanes, beams, vocab, n_out):
+    r = np.random.default_rng(23)
+    x = logits(r, lanes * beams, vocab, "bf16")
+    x[-1, -1] = 40.0                                         # the last token of the last row
+    check(x, "bf16", -3 * r.random((lanes, beams)), n_out, eos=vocab - 1)
+
+
+def test_a_row_of_the_largest_call():
+    """65,536 rows; the first and the last are looked at."""
+    x = torch.zeros((65536, 5), dtype=torch.float32, device="cuda")
+    x[0], x[-1] = torch.tensor([0.0, 3, 1, 2, -1]).cuda(), torch.tensor([5.0, 3, 1, 9, -1]).cuda()
+    s, out = torch.zeros((65536, 1), device="cuda"), [torch.empty((65536, 3), dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]
+    q.beam_select(x, s, *out, workspace=torch.empty(q.beam_select_workspace_size(65536, 1, 5, 3), dtype=torch.uint8, device="cuda"))
+    assert out[1][0].tolist() == [1, 3, 2] and out[1][-1].tolist() == [3, 0, 1] and out[1][7].tolist() == [0, 1, 2]
+    assert bool((out[2] == torch.arange(65536, device="cuda")[:, None]).all())
+
+
+def test_what_the_binding_refuses_and_takes():
+    x, s = torch.zeros((8, 33), device="cuda"), torch.zeros((2, 4), device="cuda")
+    o, t, p = (torch.zeros((2, 4), dtype=d, device="cuda") for d in (torch.float32, torch.int32, torch.int32))
+    f, ws = torch.zeros((2, 4), dtype=torch.bool, device="cuda"), torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    ok = dict(logits=x, scores=s, out_scores=o, out_tokens=t, out_parents=p, out_finished=f, finished=f.clone(), workspace=ws)
+    for bad in (dict(logits=x.cpu()), dict(logits=x.half()), dict(logits=x[:7]), dict(logits=x.view(-1)), dict(logits=x.t().contiguous().t()),
+                dict(scores=s.cpu()), dict(scores=s.double()), dict(scores=s.t().contiguous().t()), dict(scores=s.view(-1)),
+                dict(out_scores=o[:1]), dict(out_scores=o.half()), dict(out_tokens=t.long()), dict(out_tokens=t[:, :3]),
+                dict(out_parents=p.cpu()), dict(out_parents=p.view(4, 2)), dict(out_finished=f.int()), dict(out_finished=f[:1]),
+                dict(finished=f.float()), dict(finished=f.view(-1)), dict(finished=f.cpu()), dict(workspace=ws.cpu())):
+        with pytest.raises(ValueError):
+            q.beam_select(**{**ok, **bad})
+    for bad in (dict(workspace=None), dict(workspace=ws[:8]), dict(eos=33), dict(pad=-1), dict(logits=x.view(-1)[1:].as_strided((8, 32), (32, 1)))):
+        with pytest.raises(q.QGemvError):
+            q.beam_select(**{**ok, **bad})
+    q.beam_select(**{**ok, "out_finished": None, "finished": None})
+    q.beam_select(**{**ok, "out_finished": None, "finished": torch.full((2, 4), 2, dtype=torch.uint8, device="cuda"), "pad": 9})
+    assert bool((t == 9).all()) and p.tolist() == [[0, 1, 2, 3], [4, 5, 6, 7]]

@@ -477,3 +477,60 @@ def test_fork_at_the_borders_of_its_kernels(sizes):
     P.table[0, :max(1, P.held[0])], P.held[0], P.lens[0] = -1, max(1, P.held[0]), 1        # entries outside the pool
     rec = P.device(torch, q)
     do_fork(P, rec, np.zeros(P.n, np.int32))
+
+
+def test_long_lists_beyond_32_bits():
+    """As test_copy_beyond_32_bits, with a list long enough for the bulk copies."""
+    pages, page, heads, dim = 4200, 256, 8, 256
+    if torch.cuda.mem_get_info()[0] < 12 * 2 ** 30:
+        pytest.skip("needs 12 GB of device memory")
+    k = torch.zeros((pages, heads, page, dim), dtype=torch.bfloat16, device="cuda")
+    k[pages - 70:].normal_()
+    c = q.KVCache("bf16", k, torch.zeros_like(k))
+    moves = [(pages - 1 - i, i, page if i % 3 else 9, 0) for i in range(64)]
+    q.kv_pages_copy(c, q.KVMoves(i32(moves), i32([64])))
+    for src, dst, n, _ in moves:
+        assert torch.equal(k[dst, :, :n], k[src, :, :n]) and not k[dst, :, n:].any()
+
+
+def test_page_calls_on_a_stream_of_their_own_and_what_the_binding_refuses():
+    r = np.random.default_rng(19)
+    P = PU.random_pages(r, 9, 40, 400, 16, fill=0.3)
+    rec = P.device(torch, q)
+    parent, new = r.integers(0, 9, 9).astype(np.int32), np.ones(9)
+    dp, dn, moves, where = i32(parent), i32(new), q.KVMoves.empty(9), torch.zeros(400, dtype=torch.int32, device="cuda")
+    big, cache, side = q.KVMoves.empty(400), random_cache(r, "fp8", 400, 16, 1, 64), torch.cuda.Stream()
+    want = [t.clone() for t in parts_of(cache)]
+    torch.cuda.synchronize()
+    q.kv_pages_fork(rec, dp, stream=side)
+    q.kv_pages_reserve(rec, dn, moves, stream=side)
+    q.kv_pages_copy(cache, moves, stream=side)
+    q.kv_pages_compact(rec, big, where, stream=side)
+    q.kv_pages_copy(cache, big, stream=side)
+    side.synchronize()
+    P.fork(parent)
+    made = P.reserve(new)[0]
+    made += P.compact(400)[0]
+    P.same(rec)
+    for src, dst, t, _ in made:
+        for w in want:
+            w[dst, :, :t] = w[src, :, :t]
+    assert all(torch.equal(a, b) for a, b in zip(parts_of(cache), want))
+    for f in (lambda: q.kv_pages_fork(rec, dp[:8]), lambda: q.kv_pages_fork(rec, dp.long()), lambda: q.kv_pages_fork(rec, dp.cpu()),
+              lambda: q.kv_pages_reserve(rec, dn.view(3, 3), moves), lambda: q.kv_pages_reserve(rec, dn, moves, n_free=dn),
+              lambda: q.kv_pages_compact(rec, big, where[:399]), lambda: q.kv_pages_compact(rec, big, where, n_live=where),
+              lambda: q.KVPages(rec.page_table[:8], rec.seq_lens, rec.n_pages, rec.refs, 16),
+              lambda: q.KVPages(rec.page_table, rec.seq_lens.long(), rec.n_pages, rec.refs, 16),
+              lambda: q.KVPages(rec.page_table[:, ::2], rec.seq_lens, rec.n_pages, rec.refs, 16),
+              lambda: q.KVMoves(where, dn[:1]), lambda: q.KVMoves(big.list, dn), lambda: q.KVMoves(big.list[:, :3], dn[:1])):
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: q.kv_pages_reserve(rec, dn, q.KVMoves.empty(8)), lambda: q.kv_pages_fork(q.KVPages(*vars_of(rec), 24), dp),
+              lambda: q.kv_pages_fork(rec, i32(np.zeros(10))[1:])):
+        with pytest.raises(q.QGemvError):
+            f()
+    P.same(rec)
+
+
+def vars_of(rec):
+    return rec.page_table, rec.seq_lens, rec.n_pages, rec.refs
