@@ -17,7 +17,8 @@ constexpr int kPiece = 1024;                         // values, 32 of a lane
 constexpr int kScanWarps = 8;                        // of a block, at most
 constexpr int kGroups = 128;                         // candidates' groups, by whose best one is bounded
 constexpr int kPieces = 128;                         // pieces of a lane that are read again, if more than n_out
-constexpr int kPicked = 512;                         // candidates of a lane that are looked at in 64 bits
+constexpr int kPicked = 512;                         // candidates of a lane that are looked at in 64 bits,
+constexpr int kFew = 96;                             // if their number was not bounded twice
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -186,7 +187,11 @@ __device__ __forceinline__ float exp_sum(const float (&v)[N], float top)
 }
 
 // A warp per piece. Nothing is kept from one to the next, and blocks need no
-// order: as many loads are on their way as registers hold.
+// order: as many loads are on their way as registers hold. Bound by the
+// logits' bytes: 512 rows of 131,072 fp32 logits in 43 us, 6.2 TB/s. (Passes
+// that kept a list of the best tokens as they went, over rings of bulk copies,
+// took 66 us and more: the lists' branches and the registers for them left too
+// few warps to cover each other's waits.)
 template <bool F32>
 __global__ void __launch_bounds__(32 * kScanWarps, 4) beam_scan_kernel(const __grid_constant__ BeamArgs a, int pieces, ScaledSum* sums)
 {
@@ -269,7 +274,9 @@ __device__ __forceinline__ float split_log(float x, int& k)
     return fmaf(p * q, 2.f * t, 2.f * t);
 }
 
-// A block per lane. A candidate's score in 32 bits, f, is off by less than e =
+// A block per lane, bound by its chain of loads and barriers: 8 beams of 65,536
+// tokens in 4.5 us (sums 1.5, pieces 1.4, tokens 1.2, order and outputs 0.4) of
+// 6.9 with the scan. A candidate's score in 32 bits, f, is off by less than e =
 // 2^-21 (|score - z| + |logit|): score - z is rounded once and the sum with the
 // logit once, 2^-24 of each. The n-th largest of the groups' best f - e is
 // reached by n candidates, so only those with f + e at or above it are looked
@@ -426,7 +433,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
             f(beam, base, v);
         }
     };
-    // Tokens whose f + e may reach the bound. With |x| <= 2 (|base| + |bound|) e is at most 3 2^-21 of that sum, and 2^-21
+    // Tokens whose f + e may reach the bound, while f(...) is true. With |x| <= 2 (|base| + |bound|) e is at most 3 2^-21 of that sum, and 2^-21
     // more of it is above what is rounded here; a lower x is too low by far.
     auto each_token = [&](auto&& f) {
         each_chosen([&](int beam, int base, const float (&v)[kEach]) {
@@ -437,8 +444,9 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
             const uint8_t* row = logits_of(beam);
             for (; hits; hits &= hits - 1) {           // few: read again, which spares a copy of this code for each
                 const int token = token_of<F32>(base, __ffs(hits) - 1);
-                f(beam, F32 ? reinterpret_cast<const float*>(row)[token] : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(row)[token]),
-                  token);
+                const float x = F32 ? reinterpret_cast<const float*>(row)[token]
+                                    : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(row)[token]);
+                if (!f(beam, x, token)) break;
             }
         });
     };
@@ -448,8 +456,9 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
             s.keys[at] = key;
             s.beams[at] = beam;
         }
+        return at < kPicked;
     };
-    bool closer = bound == -INFINITY && chosen * kPiece > kPicked;
+    bool closer = bound == -INFINITY && chosen * kPiece > kFew;
     for (;;) {
         if (closer) {                                  // bounded by the tokens' groups
             best = -INFINITY;
@@ -461,10 +470,10 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
             });
             bound = nth_best(best);
         }
-        each_token([&](int beam, float x, int token) { pick(make_key(x, token), beam); });
+        each_token([&](int beam, float x, int token) { return pick(make_key(x, token), beam); });
         if (finished && s.score[tid] >= bound) pick(0, -1 - tid);
         __syncthreads();
-        if (s.count <= kPicked || closer) break;
+        if (s.count <= kFew || closer) break;
         closer = true;
         __syncthreads();
         if (tid == 0) s.count = 0;
@@ -507,6 +516,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
         each_token([&](int beam, float x, int token) {
             const Candidate y = exact(beam, x, token);
             if (better(last, y) && better(y, c)) c = y;
+            return true;
         });
         if (finished) {
             const Candidate y = of_finished(tid);
@@ -526,9 +536,13 @@ cudaError_t launch(const BeamArgs& a, ScaledSum* sums, cudaStream_t stream)
     const cudaError_t e = launch_pdl(beam_scan_kernel<F32>, dim3(static_cast<unsigned>((all + warps - 1) / warps)),
                                      dim3(static_cast<unsigned>(32 * warps)), 0, stream, a, pieces, sums);
     if (e != cudaSuccess) return e;
-    const bool many = a.lanes > 2 * sms;               // lanes: rather more blocks at a time than fast ones
-    return launch_pdl(many ? beam_join_kernel<F32, 256> : beam_join_kernel<F32, 1024>, dim3(static_cast<unsigned>(a.lanes)),
-                      dim3(many ? 256 : 1024), 0, stream, a, pieces, static_cast<const ScaledSum*>(sums));
+    // One block of 1,024 threads, two of 512 or four of 256 are on an SM at a time: the fastest that all lanes find room in
+    // (bf16 rows of 4,096, 8 of them for 1,024 / 512 / 256 threads: 150 lanes 8.7 / 9.0 / 11.2 us, 304 lanes 14.5 / 9.3 /
+    // 11.7, 400 lanes 19.7 / 14.2 / 11.9).
+    const int threads = a.lanes <= sms ? 1024 : a.lanes <= 2 * sms ? 512 : 256;
+    return launch_pdl(threads == 1024 ? beam_join_kernel<F32, 1024> : threads == 512 ? beam_join_kernel<F32, 512> : beam_join_kernel<F32, 256>,
+                      dim3(static_cast<unsigned>(a.lanes)), dim3(static_cast<unsigned>(threads)), 0, stream, a, pieces,
+                      static_cast<const ScaledSum*>(sums));
 }
 
 }  // namespace

@@ -10,13 +10,14 @@
 namespace qg {
 namespace {
 
-constexpr int kForkThreads = 1024, kForkCols = 8, kForkRun = 8, kForkAhead = 4, kForkMany = 128;
-constexpr int kFewThreads = 512, kFewRows = 64, kFewCols = 64;
+constexpr int kForkThreads = 1024, kForkCols = 8, kForkAhead = 4;
+constexpr int kFewThreads = 512, kFewRows = 16, kFewCols = 64;
 constexpr int kPlanThreads = 1024;
 constexpr int kTableThreads = 256;
 constexpr int kHash = 2048;
-constexpr int kCopyWarps = 8, kCopyPieces = 4;
-constexpr int kScaleChunk = 4096;
+constexpr int kCopyWarps = 8, kCopyParts = 16;
+constexpr int kBulkChunk = 16 << 10, kBulkStages = 4, kBulkAhead = 2, kBulkBlocks = 2;
+constexpr uint64_t kBulkWaitNs = 1000000000ull;
 
 // ------------------------------------------------------------------ rows
 // Row b of a page record: its tokens and entries, none if they do not fit.
@@ -78,16 +79,16 @@ __device__ __forceinline__ void cluster_sync()
 // old row j is held by kids[j] rows afterwards (by none behind the page of the
 // row's last token) and was held once: refs changes by the difference. A page
 // that the rows of a prompt share stands in one column of rows next to each
-// other: of kForkMany rows and more, a thread goes down kForkRun and adds up
-// what a run of one page changes by, which for beams that go on from each other
-// is often nothing.
-__host__ __device__ __forceinline__ int slab_at(int row, int col) { return (row + row / kForkRun) * kForkCols + col; }
-
+// other: what it changes by is added up over a warp's four rows first, which
+// for beams that go on from each other is often nothing. Bound by chained
+// loads (lengths, then entries, 32 bytes of a row) and the second launch: 1,024
+// rows of 2,048 entries in 12.6 us (blocks of 32 columns with an atomic for
+// each entry: 50).
 __global__ void __launch_bounds__(kForkThreads, 2) pages_fork_kernel(const __grid_constant__ PageArgs a, const int32_t* parent)
 {
     extern __shared__ int smem[];
     pdl_enter();
-    const int n = a.n_seqs, tid = threadIdx.x, threads = blockDim.x;
+    const int n = a.n_seqs, tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
     const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kForkCols;
     int* par = smem;
     int* keep = par + n;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kForkThreads, 2) pages_fork_kernel(const __gri
     if (__syncthreads_or(most > col0) == 0) return;
     const int64_t c = col0 + tid % kForkCols;
     const int row0 = tid / kForkCols, step = threads / kForkCols;
-    for (int j0 = row0; j0 < n; j0 += kForkAhead * step) {
+    for (int j0 = row0; j0 - lane / 8 < n; j0 += kForkAhead * step) {        // the same for a whole warp
         int e[kForkAhead];
 #pragma unroll
         for (int u = 0; u < kForkAhead; ++u) {
@@ -121,36 +122,30 @@ __global__ void __launch_bounds__(kForkThreads, 2) pages_fork_kernel(const __gri
 #pragma unroll
         for (int u = 0; u < kForkAhead; ++u) {
             const int j = j0 + u * step;
-            if (j >= n || c >= held[j]) continue;
-            slab[slab_at(j, tid % kForkCols)] = e[u];
-            if (n >= kForkMany) continue;
-            const int change = (c < keep[j] ? kids[j] : 0) - 1;
-            if (!in_pool(a, e[u])) set_device_status(a.status, QG_ERR_INVALID_ARG);
-            else if (change) atomicAdd(&a.refs[e[u]], change);
+            int page = -1, change = 0;
+            if (j < n && c < held[j]) {
+                slab[j * kForkCols + tid % kForkCols] = e[u];
+                if (in_pool(a, e[u])) {
+                    page = e[u];
+                    change = (c < keep[j] ? kids[j] : 0) - 1;
+                } else {
+                    set_device_status(a.status, QG_ERR_INVALID_ARG);
+                }
+            }
+            // the sum over a run goes to its first row's lane
+            const int up = __shfl_up_sync(0xffffffffu, page, 8), next = __shfl_down_sync(0xffffffffu, page, 8);
+            const int after = __shfl_down_sync(0xffffffffu, page, 16), more = __shfl_down_sync(0xffffffffu, change, 8);
+            if (lane < 24 && next == page) change += more;
+            const int rest = __shfl_down_sync(0xffffffffu, change, 16);
+            if (lane < 16 && next == page && after == page) change += rest;
+            if (page >= 0 && (lane < 8 || up != page) && change) atomicAdd(&a.refs[page], change);
         }
     }
     __syncthreads();
     for (int i = row0; i < n; i += step) {
         const int p = par[i];
         if (p < 0 || p == i || c >= keep[p]) continue;
-        a.table[static_cast<int64_t>(i) * a.max_pages + c] = slab[slab_at(p, tid % kForkCols)];
-    }
-    if (n < kForkMany) return;
-    for (int j0 = row0 * kForkRun; j0 < n; j0 += step * kForkRun) {
-        int page = -1, change = 0;
-        for (int j = j0; j <= min(j0 + kForkRun, n); ++j) {
-            const bool last = j == min(j0 + kForkRun, n);
-            if (!last && c >= held[j]) continue;
-            const int e = last ? -1 : slab[slab_at(j, tid % kForkCols)];
-            const int now = in_pool(a, e) ? e : -1;
-            if (!last && now < 0) set_device_status(a.status, QG_ERR_INVALID_ARG);
-            if (now != page) {
-                if (change) atomicAdd(&a.refs[page], change);
-                page = now;
-                change = 0;
-            }
-            if (page >= 0) change += (c < keep[j] ? kids[j] : 0) - 1;
-        }
+        a.table[static_cast<int64_t>(i) * a.max_pages + c] = slab[p * kForkCols + tid % kForkCols];
     }
 }
 
@@ -174,7 +169,8 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_rows_kernel(const __g
 }
 
 // Few rows: one launch, of a cluster whose blocks have all read the lengths
-// before one of them writes any.
+// before one of them writes any. 8 rows of 257 entries in 2.3 us, 16 in 2.8 (by
+// the two launches above 3.5 and 3.6); for 32 rows both take 3.7.
 __global__ void __launch_bounds__(kFewThreads) pages_fork_few_kernel(const __grid_constant__ PageArgs a, const int32_t* parent)
 {
     __shared__ int par[kFewRows], keep[kFewRows], held[kFewRows], kids[kFewRows], lens[kFewRows];
@@ -359,6 +355,8 @@ struct ReserveSmem {
 // share of the pool; with the free pages of the blocks before it, it knows the
 // number that each of its free pages has among all, and so the row and the
 // column that each is for. Nothing is written before every block has read.
+// Bound by chained loads and barriers (a row's length, last entry and count of
+// that page; two scans; the cluster's sum): 8 rows of a step in 4.5 us.
 __global__ void __launch_bounds__(kPlanThreads, 1) pages_reserve_kernel(const __grid_constant__ PageArgs a, const int32_t* n_new,
                                                                      const MoveArgs m, int32_t* n_free)
 {
@@ -517,7 +515,9 @@ struct CompactSmem {
 // One cluster. Of L pages in use, those at L and above move into the free
 // places below L: as many of one as of the other. With S(p) pages in use below
 // page p, a free one below L is hole number p - S(p), and one in use from L on
-// is number L - 1 - S(p) of those that move, counted from the highest.
+// is number L - 1 - S(p) of those that move, counted from the highest. Bound by
+// the cluster's few SMs: 46,000 pages in use of 92,000, half of them moved, in 14
+// us with the table.
 __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const __grid_constant__ PageArgs a, const MoveArgs m,
                                                                      int32_t* page_map, int32_t* n_live)
 {
@@ -619,21 +619,19 @@ __global__ void __launch_bounds__(kTableThreads) pages_table_kernel(const __grid
 
 // ------------------------------------------------------------------ copy
 // n consecutive bytes of each head (heads `stride` bytes apart) from one page
-// to another, pieces of sizeof(T); this warp's pieces are first + lane, 32 on
-// at a time, up to `end`.
+// to another in pieces of sizeof(T), those from `first` up to `end` by a warp.
 template <typename T, int U>
-__device__ __forceinline__ void copy_pieces(const uint8_t* src, uint8_t* dst, int64_t stride, int64_t n, int64_t first, int64_t end)
+__device__ __forceinline__ void copy_pieces(const uint8_t* src, uint8_t* dst, int64_t stride, int64_t n, uint32_t first, uint32_t end)
 {
     const uint32_t per = static_cast<uint32_t>(n / static_cast<int64_t>(sizeof(T)));
-    for (int64_t x0 = first + (threadIdx.x & 31); x0 < end; x0 += 32 * U) {
+    for (uint32_t x0 = first + (threadIdx.x & 31); x0 < end; x0 += 32 * U) {
         T v[U];
         int64_t at[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t x = x0 + 32 * u;
+            const uint32_t x = x0 + 32 * u;
             if (x < end) {
-                const uint32_t head = static_cast<uint32_t>(x) / per, off = static_cast<uint32_t>(x) % per;
-                at[u] = head * stride + off * static_cast<int64_t>(sizeof(T));
+                at[u] = x / per * stride + x % per * static_cast<int64_t>(sizeof(T));
                 v[u] = *reinterpret_cast<const T*>(src + at[u]);
             }
         }
@@ -643,8 +641,34 @@ __device__ __forceinline__ void copy_pieces(const uint8_t* src, uint8_t* dst, in
     }
 }
 
+// Share `part` of `parts` of what a move copies of one side's codes or
+// scales, `unit` bytes a token and head.
+__device__ __noinline__ void copy_part(const KvArgs& a, uint8_t* base, int unit, const int4& e, int part, int parts)
+{
+    const int64_t stride = static_cast<int64_t>(a.page_size) * unit, page = stride * a.heads;
+    const int64_t n = static_cast<int64_t>(e.z) * unit;
+    const uint8_t* src = base + e.x * page;
+    uint8_t* dst = base + e.y * page;
+    auto share = [&](uint32_t size, uint32_t& first, uint32_t& end) {          // in whole warps' pieces
+        const uint32_t all = static_cast<uint32_t>(n * a.heads / size), each = (all + 32 * parts - 1) / (32 * parts) * 32;
+        first = min(part * each, all);
+        end = min(first + each, all);
+    };
+    uint32_t first, end;
+    if (n % 16 == 0) {
+        share(16, first, end);
+        copy_pieces<uint4, 4>(src, dst, stride, n, first, end);
+    } else if (n % 4 == 0) {
+        share(4, first, end);
+        copy_pieces<uint32_t, 4>(src, dst, stride, n, first, end);
+    } else {
+        share(1, first, end);
+        copy_pieces<uint8_t, 4>(src, dst, stride, n, first, end);
+    }
+}
+
 // Entry `move` of the list, checked; without tokens where it does not fit.
-__device__ __forceinline__ int4 move_at(const KvArgs& a, const MoveArgs& m, int64_t move)
+__device__ __forceinline__ int4 move_at(const KvArgs& a, const MoveArgs& m, int move)
 {
     int4 e = m.list[move];
     if (static_cast<unsigned>(e.x) >= static_cast<unsigned>(a.num_pages) ||
@@ -655,73 +679,21 @@ __device__ __forceinline__ int4 move_at(const KvArgs& a, const MoveArgs& m, int6
     return e;
 }
 
-// A warp copies chunk `chunk` of the scales of move e, one side.
-__device__ __forceinline__ void copy_scales(const KvArgs& a, const int4& e, int kv, int chunk)
-{
-    const int unit = kv_scale_bytes(a.fmt, a.dim);
-    const int64_t stride = static_cast<int64_t>(a.page_size) * unit, page = stride * a.heads;
-    const int64_t n = static_cast<int64_t>(e.z) * unit, all = n * a.heads;
-    const uint8_t* src = a.scales[kv] + e.x * page;
-    uint8_t* dst = a.scales[kv] + e.y * page;
-    const int64_t first = static_cast<int64_t>(chunk) * kScaleChunk, end = min(first + kScaleChunk, all);
-    if (first >= end) return;
-    if (n % 16 == 0)
-        copy_pieces<uint4, kCopyPieces>(src, dst, stride, n, first / 16, end / 16);
-    else if (n % 4 == 0)
-        copy_pieces<uint32_t, kCopyPieces>(src, dst, stride, n, first / 4, end / 4);
-    else
-        copy_pieces<uint8_t, kCopyPieces>(src, dst, stride, n, first, end);
-}
-
-// Few moves. A warp takes an item: a run of a move's codes, or of its scales,
-// of one side.
-__global__ void __launch_bounds__(32 * kCopyWarps) pages_copy_kernel(const __grid_constant__ KvArgs a, const MoveArgs m,
-                                                                     int code_items, int scale_items)
-{
-    pdl_enter();
-    const int count = *m.count;
-    if (count < 0 || count > m.capacity) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) set_device_status(a.status, QG_ERR_INVALID_ARG);
-        return;
-    }
-    const int per_side = code_items + scale_items, per_move = 2 * per_side;
-    const int rb = kv_row_bytes(a.fmt, a.dim);
-    const int64_t total = static_cast<int64_t>(count) * per_move;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kCopyWarps;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5); i < total; i += step) {
-        const int64_t move = i / per_move;
-        int item = static_cast<int>(i % per_move);
-        const int kv = item >= per_side;
-        item -= kv * per_side;
-        const int4 e = move_at(a, m, move);
-        if (e.z == 0) continue;
-        if (item >= code_items) {
-            copy_scales(a, e, kv, item - code_items);
-            continue;
-        }
-        const int64_t stride = static_cast<int64_t>(a.page_size) * rb, page = stride * a.heads;
-        const int64_t n = static_cast<int64_t>(e.z) * rb, all = n * a.heads;            // multiples of 32
-        const int64_t chunk = 32 * 16 * kCopyPieces, first = item * chunk, end = min(first + chunk, all);
-        if (first < end)
-            copy_pieces<uint4, kCopyPieces>(a.codes[kv] + e.x * page, a.codes[kv] + e.y * page, stride, n, first / 16, end / 16);
-    }
-}
-
-// Many moves. One thread of a block keeps kBulkAhead chunks of codes on their
-// way into shared memory and stores them from there, all with bulk copies (rows
-// are multiples of 32 bytes); the other warps copy scales. Whole pages are cut
-// into chunks, others into those of each head's tokens.
-constexpr int kBulkChunk = 16 << 10, kBulkStages = 6, kBulkAhead = 4, kBulkBlocks = 2;
-constexpr uint64_t kBulkWaitNs = 1000000000ull;
-
+// Codes of whole pages, which lie next to each other: one warp of a block keeps
+// kBulkAhead chunks on their way into shared memory and stores them from
+// there, all with bulk copies. Codes of other moves, and scales: the other
+// warps, several to a side of a move where there are more warps than sides.
+// Bound by bytes: 2,048 pages of 2 x 128 KB in 165 us, 6.5 TB/s read and
+// written (with 16-byte loads and stores of all warps 192); 8 part-filled pages
+// in 2.3 us, 2,048 moves of 13 fp8 tokens of 8 heads in 18 (bulk copies of each
+// head's tokens: 68).
 struct BulkChunk {
     const uint8_t* src;
     uint8_t* dst;
     uint32_t bytes;
 };
 
-__global__ void __launch_bounds__(32 * kCopyWarps, kBulkBlocks) pages_copy_bulk_kernel(const __grid_constant__ KvArgs a, const MoveArgs m,
-                                                                             int code_chunks, int scale_items)
+__global__ void __launch_bounds__(32 * kCopyWarps, kBulkBlocks) pages_copy_kernel(const __grid_constant__ KvArgs a, const MoveArgs m)
 {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[kBulkStages];
@@ -736,84 +708,85 @@ __global__ void __launch_bounds__(32 * kCopyWarps, kBulkBlocks) pages_copy_bulk_
         if (blockIdx.x == 0 && tid == 0) set_device_status(a.status, QG_ERR_INVALID_ARG);
         return;
     }
+    const int rb = kv_row_bytes(a.fmt, a.dim), sb = kv_scale_bytes(a.fmt, a.dim), sides = 2 * count;
     if (tid >= 32) {
-        const int64_t total = static_cast<int64_t>(count) * 2 * scale_items, step = static_cast<int64_t>(gridDim.x) * (kCopyWarps - 1);
-        for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kCopyWarps - 1) + (tid >> 5) - 1; i < total; i += step) {
-            const int64_t side = i / scale_items;
+        const int warps = gridDim.x * (kCopyWarps - 1), kinds = sb ? 2 : 1;
+        const int parts = max(1, min(kCopyParts, warps / max(1, sides * kinds)));
+        const int64_t items = static_cast<int64_t>(sides) * kinds * parts;
+        for (int64_t i = blockIdx.x * (kCopyWarps - 1) + (tid >> 5) - 1; i < items; i += warps) {
+            const int part = static_cast<int>(i % parts), x = static_cast<int>(i / parts), side = x / kinds;
             const int4 e = move_at(a, m, side >> 1);
-            if (e.z) copy_scales(a, e, static_cast<int>(side & 1), static_cast<int>(i % scale_items));
+            if (x % kinds) {
+                if (e.z) copy_part(a, a.scales[side & 1], sb, e, part, parts);
+            } else if (e.z && e.z < a.page_size) {
+                copy_part(a, a.codes[side & 1], rb, e, part, parts);
+            }
         }
         return;
     }
-    if (tid) return;
-    const int rb = kv_row_bytes(a.fmt, a.dim);
-    const int64_t stride = static_cast<int64_t>(a.page_size) * rb, page = stride * a.heads;
-    const int per_head = code_chunks / a.heads;
-    // chunk `chunk` of side `side` (keys or values of a move), gridDim.x on at a time; its entry is read one ahead
-    const int sides = 2 * count, side_step = gridDim.x / code_chunks, chunk_step = gridDim.x % code_chunks;
-    int side = blockIdx.x / code_chunks, chunk = blockIdx.x % code_chunks;
-    int4 ahead = side < sides ? move_at(a, m, side >> 1) : int4{};
-    auto next_chunk = [&](BulkChunk& c) {              // the next one that is any
-        while (side < sides) {
-            const int4 e = ahead;
-            const int kv = side & 1, of = chunk;
-            side += side_step;
-            chunk += chunk_step;
-            if (chunk >= code_chunks) {
-                chunk -= code_chunks;
-                ++side;
-            }
-            if (side < sides) ahead = move_at(a, m, side >> 1);
-            const bool whole = e.z == a.page_size;
-            const int64_t n = whole ? page : static_cast<int64_t>(e.z) * rb;
-            const int head = whole ? 0 : of / per_head;
-            const int64_t from = static_cast<int64_t>(of - head * per_head) * kBulkChunk;
-            if (from >= n) continue;
-            c.src = a.codes[kv] + e.x * page + head * stride + from;
-            c.dst = a.codes[kv] + e.y * page + head * stride + from;
-            c.bytes = static_cast<uint32_t>(min(n - from, static_cast<int64_t>(kBulkChunk)));
-            return true;
-        }
-        return false;
-    };
-    uint8_t* dst[kBulkAhead];
-    uint32_t bytes[kBulkAhead];
+    const int64_t page = static_cast<int64_t>(a.page_size) * rb * a.heads;
+    const int chunks = static_cast<int>((page + kBulkChunk - 1) / kBulkChunk);
+    // Of the block's chunks, gridDim.x from each other, each lane looks at one: `whole` has those of whole pages that are
+    // still to be copied. Lane i also has the chunk on its way that is i-th of kBulkAhead.
+    const int64_t total = static_cast<int64_t>(sides) * chunks;
+    int64_t batch = blockIdx.x;
+    uint32_t whole = 0;
+    BulkChunk mine{}, waiting{};
     int loaded = 0, stored = 0;
     uint32_t round = 0;
-    bool more = true;
     for (int put = 0, got = 0;; ++stored) {
-#pragma unroll 1
-        while (more && loaded - stored < kBulkAhead) {
-            BulkChunk c;
-            more = next_chunk(c);
-            if (!more) break;
-            // the stage's last store is at least kBulkStages - kBulkAhead + 1 stores back
-            if (loaded >= kBulkStages) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBulkStages - kBulkAhead) : "memory");
-            mbar_arrive_expect_tx(&full[put], c.bytes);
-            bulk_load(ring + put * kBulkChunk, c.src, c.bytes, &full[put]);
-            dst[loaded % kBulkAhead] = c.dst;
-            bytes[loaded % kBulkAhead] = c.bytes;
+        while (loaded - stored < kBulkAhead) {
+            while (!whole && batch < total) {
+                const int64_t at = batch + static_cast<int64_t>(tid) * gridDim.x;
+                bool mine_is = false;
+                if (at < total) {
+                    const int side = static_cast<int>(at / chunks), kv = side & 1;
+                    const int4 e = move_at(a, m, side >> 1);
+                    const int64_t from = (at - static_cast<int64_t>(side) * chunks) * kBulkChunk;
+                    mine_is = e.z == a.page_size;
+                    mine = BulkChunk{a.codes[kv] + e.x * page + from, a.codes[kv] + e.y * page + from,
+                                     static_cast<uint32_t>(min(page - from, static_cast<int64_t>(kBulkChunk)))};
+                }
+                whole = __ballot_sync(0xffffffffu, mine_is);
+                batch += 32 * static_cast<int64_t>(gridDim.x);
+            }
+            if (!whole) break;
+            const int from_lane = __ffs(whole) - 1;
+            whole &= whole - 1;
+            const BulkChunk c{reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine.src), from_lane)),
+                              reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine.dst), from_lane)),
+                              __shfl_sync(0xffffffffu, mine.bytes, from_lane)};
+            if (tid == 0) {
+                // the stage's last store is at least kBulkStages - kBulkAhead + 1 stores back
+                if (loaded >= kBulkStages) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBulkStages - kBulkAhead) : "memory");
+                mbar_arrive_expect_tx(&full[put], c.bytes);
+                bulk_load(ring + put * kBulkChunk, c.src, c.bytes, &full[put]);
+            }
+            if (tid == loaded % kBulkAhead) waiting = c;
             put = put + 1 == kBulkStages ? 0 : put + 1;
             ++loaded;
         }
         if (stored == loaded) break;
-        if (!mbar_wait_bounded(&full[got], round, kBulkWaitNs, a.status)) {
+        const int of = stored % kBulkAhead;
+        const uint64_t dst = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(waiting.dst), of);
+        const uint32_t bytes = __shfl_sync(0xffffffffu, waiting.bytes, of);
+        if (!__all_sync(0xffffffffu, tid || mbar_wait_bounded(&full[got], round, kBulkWaitNs, a.status))) {
             // nothing is left on its way into a block that is gone
-            for (; stored < loaded; ++stored) {
+            for (; tid == 0 && stored < loaded; ++stored) {
                 mbar_wait_bounded(&full[got], round, kBulkWaitNs, a.status);
                 got = got + 1 == kBulkStages ? 0 : got + 1;
                 round ^= got == 0;
             }
             break;
         }
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\ncp.async.bulk.commit_group;" ::"l"(
-                         reinterpret_cast<uint64_t>(dst[stored % kBulkAhead])),
-                     "r"(smem_u32(ring + got * kBulkChunk)), "r"(bytes[stored % kBulkAhead])
-                     : "memory");
+        if (tid == 0)
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\ncp.async.bulk.commit_group;" ::"l"(dst),
+                         "r"(smem_u32(ring + got * kBulkChunk)), "r"(bytes)
+                         : "memory");
         got = got + 1 == kBulkStages ? 0 : got + 1;
         round ^= got == 0;
     }
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ launches
@@ -830,10 +803,12 @@ bool allow_smem(const void* kern, bool (&set)[64], int bytes = kPlanSmemMax)
     return true;
 }
 
-// One block scans a small pool (a cluster of eight takes 0.8 us longer for
-// 1,200 pages), a cluster of 16 a large one, or of eight where the device has
-// no room for such (24,000 pages handed out of 140,000: 12.2 us, by eight 14.4);
-// 0 on an error.
+// One block scans a small pool, a cluster of 16 a large one, or of eight where
+// the device has no room for such; 0 on an error. One block and a cluster of 16
+// take, with the copy that restores the record, 8.2 and 8.9 us to reserve from
+// 13,000 pages, 9.3 and 9.3 from 24,500 and 11.9 and 9.5 from 49,000; to
+// compact these 10.5 and 11.1, 13.4 and 12.0, 20.4 and 12.6. 21,000 pages of
+// 100,000 are handed out in 12.2 us by 16 blocks and in 14.4 by eight.
 int plan_blocks(const PageArgs& a, const void* kern, int (&most)[64])
 {
     int dev = 0;
@@ -856,7 +831,7 @@ int plan_blocks(const PageArgs& a, const void* kern, int (&most)[64])
         if (!asked) cudaGetLastError();
         most[dev] = asked && room > 0 ? 16 : 8;
     }
-    return a.num_pages > 8192 ? most[dev] : 1;
+    return a.num_pages > 16384 ? most[dev] : 1;
 }
 
 size_t plan_smem(const PageArgs& a, size_t fixed, int blocks)
@@ -899,13 +874,13 @@ qg_status launch_pages_fork(const PageArgs& in, const int32_t* parent, cudaStrea
     static bool set[64] = {};
     PageArgs a;
     if (!with_status(in, a)) return QG_ERR_CUDA;
-    if (a.n_seqs <= kFewRows && a.max_pages <= 64 * kFewCols) {
+    if (a.n_seqs <= kFewRows && a.max_pages <= 8 * kFewCols) {
         const cudaError_t e = launch_cluster(pages_fork_few_kernel, min((a.max_pages - 1) / kFewCols + 1, 8), 0, stream, kFewThreads,
                                              a, parent);
         return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;
     }
     if (!allow_smem(reinterpret_cast<const void*>(pages_fork_kernel), set)) return QG_ERR_CUDA;
-    const size_t smem = (static_cast<size_t>(a.n_seqs) * 4 + slab_at(a.n_seqs - 1, kForkCols)) * 4;
+    const size_t smem = static_cast<size_t>(a.n_seqs) * (4 + kForkCols) * 4;
     const int threads = min(kForkThreads, max(64, (a.n_seqs * kForkCols + 31) / 32 * 32));
     cudaError_t e = launch_pdl(pages_fork_kernel, dim3(static_cast<unsigned>((a.max_pages - 1) / kForkCols + 1)),
                                dim3(static_cast<unsigned>(threads)), smem, stream, a, parent);
@@ -944,28 +919,13 @@ qg_status launch_pages_compact(const PageArgs& in, const MoveArgs& m, int32_t* p
 
 qg_status launch_pages_copy(const KvArgs& in, const MoveArgs& m, cudaStream_t stream)
 {
+    static bool set[64] = {};
+    constexpr int kSmem = kBulkStages * kBulkChunk;
     KvArgs a = in;
     a.status = device_status_ptr();
-    if (!a.status) return QG_ERR_CUDA;
-    const int64_t rows = static_cast<int64_t>(a.heads) * a.page_size;
-    const int64_t code = 32 * 16 * kCopyPieces;
-    const int code_items = static_cast<int>((rows * kv_row_bytes(a.fmt, a.dim) + code - 1) / code);
-    const int scale_items = static_cast<int>((rows * kv_scale_bytes(a.fmt, a.dim) + kScaleChunk - 1) / kScaleChunk);
-    // The list's length is device data: by its capacity. Below it, a few moves that have to be quick (8 part-filled pages:
-    // 2.4 us); above, 2,048 pages of 2 x 128 KB take COPYA us with the bulk copies, COPYB us without.
-    if (m.capacity * 2 * rows * kv_row_bytes(a.fmt, a.dim) > int64_t{64} << 20) {
-        static bool set[64] = {};
-        constexpr int kSmem = kBulkStages * kBulkChunk;
-        if (!allow_smem(reinterpret_cast<const void*>(pages_copy_bulk_kernel), set, kSmem)) return QG_ERR_CUDA;
-        const int code_chunks = a.heads * static_cast<int>((static_cast<int64_t>(a.page_size) * kv_row_bytes(a.fmt, a.dim) + kBulkChunk - 1) / kBulkChunk);
-        const cudaError_t e = launch_pdl(pages_copy_bulk_kernel, dim3(static_cast<unsigned>(kBulkBlocks * sm_count(-1))),
-                                         dim3(32 * kCopyWarps), kSmem, stream, a, m, code_chunks, scale_items);
-        return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;
-    }
-    const int64_t warps = static_cast<int64_t>(m.capacity) * 2 * (code_items + scale_items);
-    const int64_t blocks = min((warps + kCopyWarps - 1) / kCopyWarps, static_cast<int64_t>(sm_count(-1)) * 8);
-    const cudaError_t e = launch_pdl(pages_copy_kernel, dim3(static_cast<unsigned>(blocks)), dim3(32 * kCopyWarps), 0,
-                                     stream, a, m, code_items, scale_items);
+    if (!a.status || !allow_smem(reinterpret_cast<const void*>(pages_copy_kernel), set, kSmem)) return QG_ERR_CUDA;
+    const cudaError_t e = launch_pdl(pages_copy_kernel, dim3(static_cast<unsigned>(kBulkBlocks * sm_count(-1))),
+                                     dim3(32 * kCopyWarps), kSmem, stream, a, m);
     return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 
