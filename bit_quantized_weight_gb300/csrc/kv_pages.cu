@@ -16,7 +16,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kTableThreads = 256;
 constexpr int kHash = 2048;
 constexpr int kCopyWarps = 8, kCopyParts = 16;
-constexpr int kBulkChunk = 16 << 10, kBulkStages = 4, kBulkAhead = 2, kBulkBlocks = 2;
+constexpr int kBulkChunk = 16 << 10, kBulkStages = 4, kBulkAhead = 2, kBulkBlocks = 2, kBulkLeast = 4 << 10;
 constexpr uint64_t kBulkWaitNs = 1000000000ull;
 
 // ------------------------------------------------------------------ rows
@@ -679,14 +679,18 @@ __device__ __forceinline__ int4 move_at(const KvArgs& a, const MoveArgs& m, int 
     return e;
 }
 
-// Codes of whole pages, which lie next to each other: one warp of a block keeps
-// kBulkAhead chunks on their way into shared memory and stores them from
-// there, all with bulk copies. Codes of other moves, and scales: the other
-// warps, several to a side of a move where there are more warps than sides.
-// Bound by bytes: 2,048 pages of 2 x 128 KB in 165 us, 6.5 TB/s read and
-// written (with 16-byte loads and stores of all warps 192); 8 part-filled pages
-// in 2.3 us, 2,048 moves of 13 fp8 tokens of 8 heads in 18 (bulk copies of each
-// head's tokens: 68).
+// One warp of a block keeps kBulkAhead chunks on their way into shared memory
+// and stores them from there, all with bulk copies: codes of whole pages, which
+// lie next to each other, and of a head's tokens. The other warps take scales
+// and what is too short for that, several to a side of a move where there are
+// more warps than sides. Bound by bytes: 2,048 pages of 2 x 128 KB in 165 us,
+// 6.5 TB/s read and written (with 16-byte loads and stores of all warps 192); 8
+// moves of 37 fp8 tokens of 4 heads in 2.3 us. In bulk and by the warps: pages
+// of 4 KB (8,192 moves of nvfp4) 39.9 and 47.5 us, 1 KB (fp8) 32.4 and 19.2;
+// heads' tokens of 8 KB (1,000 moves of bf16) 27.7 and 36.8, 4.6 KB (1,000 of
+// fp8) 28.8 and 32.7, 1.6 KB (2,048 of fp8) 68 and 18. Where every warp has at
+// most one of the shares, tokens of 4.6 KB (8 moves of fp8) 2.8 and 2.3, 8 KB
+// (64 of bf16) 4.0 and 3.7, 16 KB (8 of bf16) 2.7 and 4.4.
 struct BulkChunk {
     const uint8_t* src;
     uint8_t* dst;
@@ -709,8 +713,10 @@ __global__ void __launch_bounds__(32 * kCopyWarps, kBulkBlocks) pages_copy_kerne
         return;
     }
     const int rb = kv_row_bytes(a.fmt, a.dim), sb = kv_scale_bytes(a.fmt, a.dim), sides = 2 * count;
+    const int64_t stride = static_cast<int64_t>(a.page_size) * rb, page = stride * a.heads;
+    const int warps = gridDim.x * (kCopyWarps - 1), least = (sides * kCopyParts > warps ? 1 : 3) * kBulkLeast;
     if (tid >= 32) {
-        const int warps = gridDim.x * (kCopyWarps - 1), kinds = sb ? 2 : 1;
+        const int kinds = sb ? 2 : 1;
         const int parts = max(1, min(kCopyParts, warps / max(1, sides * kinds)));
         const int64_t items = static_cast<int64_t>(sides) * kinds * parts;
         for (int64_t i = blockIdx.x * (kCopyWarps - 1) + (tid >> 5) - 1; i < items; i += warps) {
@@ -718,44 +724,54 @@ __global__ void __launch_bounds__(32 * kCopyWarps, kBulkBlocks) pages_copy_kerne
             const int4 e = move_at(a, m, side >> 1);
             if (x % kinds) {
                 if (e.z) copy_part(a, a.scales[side & 1], sb, e, part, parts);
-            } else if (e.z && e.z < a.page_size) {
+            } else if (e.z && !(e.z == a.page_size ? page >= kBulkLeast : e.z * rb >= least)) {
                 copy_part(a, a.codes[side & 1], rb, e, part, parts);
             }
         }
         return;
     }
-    const int64_t page = static_cast<int64_t>(a.page_size) * rb * a.heads;
-    const int chunks = static_cast<int>((page + kBulkChunk - 1) / kBulkChunk);
-    // Of the block's chunks, gridDim.x from each other, each lane looks at one: `whole` has those of whole pages that are
-    // still to be copied. Lane i also has the chunk on its way that is i-th of kBulkAhead.
-    const int64_t total = static_cast<int64_t>(sides) * chunks;
+    const int slots = static_cast<int>((page + kBulkChunk - 1) / kBulkChunk), heads = (a.heads + slots - 1) / slots;
+    // A slot is a chunk of a whole page, or some heads' tokens of another. Of the block's slots, gridDim.x from each other,
+    // each lane looks at one: `left` chunks of it are still to be copied, in runs of `run` bytes, `stride` from each other.
+    // Lane i also has the chunk on its way that is i-th of kBulkAhead.
+    const int64_t total = static_cast<int64_t>(sides) * slots;
     int64_t batch = blockIdx.x;
-    uint32_t whole = 0;
+    uint32_t some = 0;
     BulkChunk mine{}, waiting{};
+    int left = 0, run = 0, per_run = 1, sub = 0;
     int loaded = 0, stored = 0;
     uint32_t round = 0;
     for (int put = 0, got = 0;; ++stored) {
         while (loaded - stored < kBulkAhead) {
-            while (!whole && batch < total) {
+            while (!some && batch < total) {
                 const int64_t at = batch + static_cast<int64_t>(tid) * gridDim.x;
-                bool mine_is = false;
+                left = sub = 0;
                 if (at < total) {
-                    const int side = static_cast<int>(at / chunks), kv = side & 1;
+                    const int side = static_cast<int>(at / slots), kv = side & 1, slot = static_cast<int>(at - static_cast<int64_t>(side) * slots);
                     const int4 e = move_at(a, m, side >> 1);
-                    const int64_t from = (at - static_cast<int64_t>(side) * chunks) * kBulkChunk;
-                    mine_is = e.z == a.page_size;
-                    mine = BulkChunk{a.codes[kv] + e.x * page + from, a.codes[kv] + e.y * page + from,
-                                     static_cast<uint32_t>(min(page - from, static_cast<int64_t>(kBulkChunk)))};
+                    int64_t from = static_cast<int64_t>(slot) * kBulkChunk;
+                    if (e.z == a.page_size && page >= kBulkLeast) {
+                        left = per_run = 1;
+                        run = static_cast<int>(min(page - from, static_cast<int64_t>(kBulkChunk)));
+                    } else if (e.z < a.page_size && e.z * rb >= least) {
+                        run = e.z * rb;
+                        per_run = (run + kBulkChunk - 1) / kBulkChunk;
+                        left = max(0, min(heads, a.heads - slot * heads)) * per_run;
+                        from = slot * heads * stride;
+                    }
+                    mine = BulkChunk{a.codes[kv] + e.x * page + from, a.codes[kv] + e.y * page + from, 0};
                 }
-                whole = __ballot_sync(0xffffffffu, mine_is);
+                some = __ballot_sync(0xffffffffu, left > 0);
                 batch += 32 * static_cast<int64_t>(gridDim.x);
             }
-            if (!whole) break;
-            const int from_lane = __ffs(whole) - 1;
-            whole &= whole - 1;
-            const BulkChunk c{reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine.src), from_lane)),
-                              reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine.dst), from_lane)),
-                              __shfl_sync(0xffffffffu, mine.bytes, from_lane)};
+            if (!some) break;
+            const int of_lane = __ffs(some) - 1;
+            const int64_t off = sub / per_run * stride + sub % per_run * kBulkChunk;
+            const BulkChunk c{reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine.src + off), of_lane)),
+                              reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine.dst + off), of_lane)),
+                              static_cast<uint32_t>(__shfl_sync(0xffffffffu, min(run - sub % per_run * kBulkChunk, kBulkChunk), of_lane))};
+            if (tid == of_lane) ++sub;
+            if (__shfl_sync(0xffffffffu, left - sub, of_lane) == 0) some &= some - 1;
             if (tid == 0) {
                 // the stage's last store is at least kBulkStages - kBulkAhead + 1 stores back
                 if (loaded >= kBulkStages) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBulkStages - kBulkAhead) : "memory");
