@@ -231,8 +231,9 @@ __device__ __forceinline__ int cluster_word(const int* p, uint32_t rank)
     return v;
 }
 
-// Sum over the block of v, and what the threads before this one have: of two
-// numbers with one barrier. Each scan of a kernel has its own warp_sums.
+// Sums over a warp up to each lane, and of the warps before this one: a barrier
+// lies between the two, which several numbers share. Each scan of a kernel has
+// its own warp_sums.
 template <typename T>
 __device__ __forceinline__ T warp_scan(T v)
 {
@@ -255,6 +256,7 @@ __device__ __forceinline__ T before_warp(const T* warp_sums, T& total)
     return warp ? before : T(0);
 }
 
+// Sum over the block of v, and what the threads before this one have.
 __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total)
 {
     const int x = warp_scan(v);
@@ -263,13 +265,10 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total)
     return x - v + before_warp(warp_sums, total);
 }
 
-// A block's share of the pool, `words` words of 32 pages from word `word0` on:
-// bit i of a word is set for a page that is held (free_bits: that is free).
-// Pages behind the pool have bit 0.
+// The counts of four pages of a thread, 0 behind the pool.
 struct RefsLoad {
     int4 r;
 
-    // the counts of four pages of a thread, 0 behind the pool
     __device__ __forceinline__ RefsLoad(const PageArgs& a, int word0, int words, int base)
     {
         const int at = base + 4 * static_cast<int>(threadIdx.x);
@@ -286,7 +285,9 @@ struct RefsLoad {
     }
 };
 
-// `ahead`: the first ones, loaded before.
+// A block's share of the pool, `words` words of 32 pages from word `word0` on:
+// bit i of a word is set for a page that is held (free_bits: that is free).
+// Pages behind the pool have bit 0. `ahead`: the first counts, loaded before.
 __device__ __forceinline__ void scan_refs(const PageArgs& a, int word0, int words, bool free_bits, uint32_t* bits, RefsLoad ahead)
 {
     const int lane = threadIdx.x & 31;
