@@ -459,6 +459,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_reserve_kernel(const __
         if (b == 0) {
             *m.count = enough ? moves : 0;
             if (n_free) *n_free = static_cast<int>(max(free_pages - total, static_cast<int64_t>(-0x7FFFFFFF)));
+            else if (!enough) set_device_status(a.status, QG_ERR_INVALID_ARG);       // nobody would hear of it
         }
         if (enough && writes) a.held[b] = max(r.held, last);
         if (enough && replaced) atomicSub(&a.refs[tail], 1);

@@ -644,7 +644,8 @@ def kv_pages_fork(pages, parent, stream=None):
 def kv_pages_reserve(pages, n_new, moves, n_free=None, stream=None):
     """Pages of its own for each sequence's next n_new tokens (int32 [n]); the
     part-filled pages that are replaced join `moves`. n_free int32 [1]: the free
-    pages left, negative (and nothing changed) where they do not suffice."""
+    pages left, negative (and nothing changed: nothing may be appended) where
+    they do not suffice; without it, that is recorded in the status word."""
     n_new = _kv_int32("n_new", n_new, pages.index, pages.n_seqs)
     n_free = None if n_free is None else _kv_int32("n_free", n_free, pages.index, 1)
     if moves.index != pages.index:

@@ -571,11 +571,18 @@ QG_API qg_status kv_pages_fork(const qg_kv_pages* pages, const int32_t* parent, 
  * `moves` (kv_pages_copy in every layer before the append); where all who hold
  * it are sequences of this call that write, the lowest of them keeps it.
  * Either every sequence gets its pages or, where the free ones do not suffice,
- * the call changes nothing but moves->count = 0 and n_free.
+ * the call changes nothing but moves->count = 0 and n_free. What was to be
+ * written has no place then: entries behind those that a row holds are left
+ * over from earlier rows, and an append through them writes into pages of
+ * other sequences. So look at n_free before it, or ahead: a row with
+ * n_new = 1 takes one page at most, and while n_free is at least the number of
+ * such rows, the next call's will suffice.
  *   n_new   int32 [n_seqs], 0: the row is left as it is
  *   moves   capacity of at least n_seqs, entries in the order of the rows;
  *           entries behind count are not written
- *   n_free  int32 [1] or NULL: the free pages left, or minus the missing ones
+ *   n_free  int32 [1] or NULL: the free pages left, or minus the missing ones;
+ *           without it, missing ones record QG_ERR_INVALID_ARG in the device
+ *           status word
  * A row with a negative n_new, more positions than max_pages * page_size or
  * 2^30, or a page to be written that is outside the pool or, behind the last
  * token's page, shared (kv_pages_fork drops such pages) is left as it is and

@@ -1,0 +1,47 @@
+"""The page calls at their limits (GPU): pools that run out, waits that run
+out, and sizes on both sides of each rule that picks a kernel."""
+import numpy as np
+import pytest
+
+import pages_util as PU
+from test_gpu_pages import do_compact, do_fork, do_reserve, i32, parts_of, random_cache, status
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+q = pytest.importorskip("bit_quantized_weight_gb300")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.set_device(0)
+    yield
+    assert q.qg_last_device_status() == q.QG_OK
+
+
+# ------------------------------------------------------------------ pools that run out
+@pytest.mark.parametrize("pool", [3, 20000])
+def test_a_reserve_that_finds_too_few_pages_is_heard_of(pool):
+    """By n_free, or by the status word where there is none; in a replayed graph too."""
+    P = PU.Pages(4, 8, pool, 16)
+    P.refs[3:] = 1
+    rec, moves, left, new = P.device(torch, q), q.KVMoves.empty(4), i32([7]), i32(np.ones(4))
+    q.kv_pages_reserve(rec, new, moves)
+    status(True)
+    q.kv_pages_reserve(rec, new, moves, n_free=left)
+    status(False)
+    assert int(left) == -1 and int(moves.count) == 0
+    P.same(rec)
+    g, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=stream):
+        q.kv_pages_reserve(rec, new, moves)
+    g.replay()
+    status(True)
+    P.same(rec)
+    new[3] = 0                                               # three pages suffice
+    g.replay()
+    status(False)
+    P.reserve([1, 1, 1, 0])
+    P.same(rec)
