@@ -593,10 +593,12 @@ class KVPages:
 
     @classmethod
     def empty(cls, n_seqs, max_pages, num_pages, page_size, device="cuda"):
-        """Sequences without tokens over a pool of free pages."""
+        """Sequences without tokens over a pool of free pages. Table entries that
+        no row has held yet are -1, no page of any cache: what is appended
+        without a page is left out and recorded."""
         import torch
-        table, lens, held, refs = (torch.zeros(shape, dtype=torch.int32, device=device)
-                                   for shape in ((n_seqs, max_pages), (n_seqs,), (n_seqs,), (num_pages,)))
+        table = torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=device)
+        lens, held, refs = (torch.zeros(n, dtype=torch.int32, device=device) for n in (n_seqs, n_seqs, num_pages))
         return cls(table, lens, held, refs, page_size)
 
 

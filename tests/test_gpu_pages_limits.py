@@ -45,3 +45,30 @@ def test_a_reserve_that_finds_too_few_pages_is_heard_of(pool):
     status(False)
     P.reserve([1, 1, 1, 0])
     P.same(rec)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+def test_what_is_appended_without_a_page_is_left_out_and_recorded(fmt):
+    """Three of four rows write a token each; the fourth has no page, and then none has one for its next page."""
+    r = np.random.default_rng(41)
+    rec, moves, left = q.KVPages.empty(4, 3, 3, 16), q.KVMoves.empty(4), i32([7])
+    cache = random_cache(r, fmt, 3, 16, 2, 64)
+    batch = q.KVBatch(rec.page_table, rec.seq_lens, i32(np.arange(5)), 4)
+    x = torch.randn((4, 2, 64), device="cuda").bfloat16()
+    before = [t.clone() for t in parts_of(cache)]
+    q.kv_pages_reserve(rec, i32(np.ones(4)), moves, n_free=left)
+    assert int(left) == -1
+    q.kv_cache_append(cache, batch, x, x)                    # against the rule: no row has a page
+    status(True)
+    assert all(torch.equal(a, b) for a, b in zip(parts_of(cache), before))
+    q.kv_pages_reserve(rec, i32([16, 16, 16, 0]), moves, n_free=left)
+    assert int(left) == 0
+    q.kv_cache_append(cache, batch, x, x)                    # the fourth row has none
+    status(True)
+    rec.seq_lens.add_(torch.tensor([16, 16, 16, 0], dtype=torch.int32, device="cuda"))
+    before = [t.clone() for t in parts_of(cache)]
+    q.kv_pages_reserve(rec, i32([1, 1, 1, 0]), moves, n_free=left)
+    assert int(left) == -3
+    q.kv_cache_append(cache, batch, x, x)                    # nor have the others for their 17th token
+    status(True)
+    assert all(torch.equal(a, b) for a, b in zip(parts_of(cache), before))
