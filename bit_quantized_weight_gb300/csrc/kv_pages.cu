@@ -17,7 +17,6 @@ constexpr int kTableThreads = 256;
 constexpr int kHash = 2048;
 constexpr int kCopyWarps = 8, kCopyParts = 16;
 constexpr int kBulkChunk = 16 << 10, kBulkStages = 4, kBulkAhead = 2, kBulkBlocks = 2, kBulkLeast = 4 << 10;
-constexpr uint64_t kBulkWaitNs = 1000000000ull;
 
 // ------------------------------------------------------------------ rows
 // Row b of a page record: its tokens and entries, none if they do not fit.
@@ -699,7 +698,7 @@ struct BulkChunk {
     uint32_t bytes;
 };
 
-__global__ void __launch_bounds__(32 * kCopyWarps, kBulkBlocks) pages_copy_kernel(const __grid_constant__ KvArgs a, const MoveArgs m)
+__global__ void __launch_bounds__(32 * kCopyWarps, kBulkBlocks) pages_copy_kernel(const __grid_constant__ KvArgs a, const MoveArgs m, const DebugState dbg)
 {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[kBulkStages];
@@ -774,7 +773,7 @@ __global__ void __launch_bounds__(32 * kCopyWarps, kBulkBlocks) pages_copy_kerne
                               static_cast<uint32_t>(__shfl_sync(0xffffffffu, min(run - sub % per_run * kBulkChunk, kBulkChunk), of_lane))};
             if (tid == of_lane) ++sub;
             if (__shfl_sync(0xffffffffu, left - sub, of_lane) == 0) some &= some - 1;
-            if (tid == 0) {
+            if (tid == 0 && !dbg.starve) {
                 // the stage's last store is at least kBulkStages - kBulkAhead + 1 stores back
                 if (loaded >= kBulkStages) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBulkStages - kBulkAhead) : "memory");
                 mbar_arrive_expect_tx(&full[put], c.bytes);
@@ -788,10 +787,10 @@ __global__ void __launch_bounds__(32 * kCopyWarps, kBulkBlocks) pages_copy_kerne
         const int of = stored % kBulkAhead;
         const uint64_t dst = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(waiting.dst), of);
         const uint32_t bytes = __shfl_sync(0xffffffffu, waiting.bytes, of);
-        if (!__all_sync(0xffffffffu, tid || mbar_wait_bounded(&full[got], round, kBulkWaitNs, a.status))) {
-            // nothing is left on its way into a block that is gone
+        if (!__all_sync(0xffffffffu, tid || mbar_wait_bounded(&full[got], round, dbg.wait_ns, a.status))) {
+            // no more is asked for; what is on its way into this block is waited for as long once more
             for (; tid == 0 && stored < loaded; ++stored) {
-                mbar_wait_bounded(&full[got], round, kBulkWaitNs, a.status);
+                mbar_wait_bounded(&full[got], round, dbg.wait_ns, a.status);
                 got = got + 1 == kBulkStages ? 0 : got + 1;
                 round ^= got == 0;
             }
@@ -943,7 +942,7 @@ qg_status launch_pages_copy(const KvArgs& in, const MoveArgs& m, cudaStream_t st
     a.status = device_status_ptr();
     if (!a.status || !allow_smem(reinterpret_cast<const void*>(pages_copy_kernel), set, kSmem)) return QG_ERR_CUDA;
     const cudaError_t e = launch_pdl(pages_copy_kernel, dim3(static_cast<unsigned>(kBulkBlocks * sm_count(-1))),
-                                     dim3(32 * kCopyWarps), kSmem, stream, a, m);
+                                     dim3(32 * kCopyWarps), kSmem, stream, a, m, debug_state());
     return e == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 

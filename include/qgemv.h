@@ -673,9 +673,10 @@ QG_API const char* qg_status_string(qg_status status);
  * Fault-injection hook for testing the bounded-wait path. Sets the time
  * limit (ns) of every device-side wait for subsequent launches on this host
  * thread's process (0 restores the default of two seconds). With
- * starve != 0, the weight-streaming warps of the dense kernels issue no copies, so
- * the consumer waits run out and the kernels return early with
- * QG_ERR_DEVICE_TIMEOUT recorded. Not for production use.
+ * starve != 0, the weight-streaming warps of the dense kernels and the copying
+ * warps of kv_pages_copy issue no copies, so the consumer waits run out and the
+ * kernels return early with QG_ERR_DEVICE_TIMEOUT recorded. Not for production
+ * use.
  */
 QG_API qg_status qg_debug_set_wait(uint64_t limit_ns, int starve);
 

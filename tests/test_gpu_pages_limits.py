@@ -72,3 +72,26 @@ def test_what_is_appended_without_a_page_is_left_out_and_recorded(fmt):
     q.kv_cache_append(cache, batch, x, x)                    # nor have the others for their 17th token
     status(True)
     assert all(torch.equal(a, b) for a, b in zip(parts_of(cache), before))
+
+
+# ------------------------------------------------------------------ waits that run out
+@pytest.mark.parametrize("fmt,page,moves,tokens", [("bf16", 64, 5, 64), ("fp8", 256, 700, 256), ("fp8", 256, 40, 200), ("nvfp4", 64, 1, 64)])
+def test_a_copy_whose_wait_runs_out_reports_it_and_the_next_is_clean(fmt, page, moves, tokens):
+    """Whole pages and long runs of part-filled ones, a stage of the ring and many."""
+    r = np.random.default_rng(42)
+    c = random_cache(r, fmt, 2 * moves, page, 4, 128)
+    ids = r.permutation(2 * moves)
+    lst = q.KVMoves(i32(np.stack([ids[:moves], ids[moves:], np.full(moves, tokens), np.zeros(moves, int)], 1)), i32([moves]))
+    want = [t.clone() for t in parts_of(c)]
+    src, dst = (torch.from_numpy(x).cuda() for x in (ids[:moves], ids[moves:]))
+    for w in want:
+        w[dst, :, :tokens] = w[src, :, :tokens]
+    q.qg_debug_set_wait(20_000_000, True)
+    try:
+        q.kv_pages_copy(c, lst)
+        assert q.qg_last_device_status() == q.QG_ERR_DEVICE_TIMEOUT
+    finally:
+        q.qg_debug_set_wait(0, False)
+    q.kv_pages_copy(c, lst)
+    status(False)
+    assert all(torch.equal(a, b) for a, b in zip(parts_of(c), want))
