@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
     };
     bool closer = bound == -INFINITY && chosen * kPiece > kFew;
     for (;;) {
-        if (closer) {                                  // bounded by the tokens' groups
+        if (closer) {                                  // bounded by the tokens' groups too; either bound holds
             best = -INFINITY;
             each_chosen([&](int beam, int, const float (&v)[kEach]) {
                 float top = -INFINITY;
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
                 for (int k = 0; k < kEach; ++k) top = fmaxf(top, v[k]);
                 if (top > -INFINITY) best = fmaxf(best, lower(beam, top));
             });
-            bound = nth_best(best);
+            bound = fmaxf(bound, nth_best(best));
         }
         each_token([&](int beam, float x, int token) { return pick(make_key(x, token), beam); });
         if (finished && s.score[tid] >= bound) pick(0, -1 - tid);
