@@ -58,3 +58,19 @@ def test_the_second_bound_does_not_lose_the_first():
         us.append(graph_us(lambda: q.beam_select(d, s, *out, workspace=ws)))
         PU.check_selection(x, scores, None, -1, 0, [t.cpu().numpy() for t in out], N)
     assert us[0] <= 3 * us[1], us
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,vocab,step", [(4096, 4096, 1), (40, 300007, 7500)])
+def test_sums_of_equal_terms_are_exact_but_for_the_logarithm(dtype, rows, vocab, step):
+    """Row r has 1 + r step zeros, the rest -infinity: every exponential is 2^0
+    = 1 or 0 and every partial sum a whole number below 2^24, so that a score is
+    -ln(1 + r step) but for the logarithm (2^-23) and the rounding of the score."""
+    count = 1 + step * torch.arange(rows, device="cuda")
+    x = torch.where(torch.arange(vocab, device="cuda") < count[:, None], 0.0, -np.inf).to(dtype)
+    out = [torch.zeros((rows, 1), dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]
+    ws = torch.empty(q.beam_select_workspace_size(rows, 1, vocab, 1), dtype=torch.uint8, device="cuda")
+    q.beam_select(x, torch.zeros((rows, 1), device="cuda"), *out, workspace=ws)
+    want = -np.log(count.cpu().numpy().astype(np.float64))
+    assert (np.abs(out[0][:, 0].cpu().numpy() - want) <= 2.0 ** -23 + 2.0 ** -24 * np.abs(want)).all()
+    assert not out[1].any() and torch.equal(out[2][:, 0], torch.arange(rows, dtype=torch.int32, device="cuda"))

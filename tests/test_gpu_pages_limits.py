@@ -95,3 +95,68 @@ def test_a_copy_whose_wait_runs_out_reports_it_and_the_next_is_clean(fmt, page, 
     q.kv_pages_copy(c, lst)
     status(False)
     assert all(torch.equal(a, b) for a, b in zip(parts_of(c), want))
+
+
+# ------------------------------------------------------------------ the kernels' borders
+@pytest.mark.parametrize("rows,wide", [(1, 64), (1, 65), (1, 512), (1, 513), (8, 65), (8, 128), (8, 129), (8, 257), (15, 300), (16, 65), (16, 511), (16, 512),
+                                       (16, 513), (17, 65), (17, 512)])
+def test_fork_at_the_border_of_the_kernel_for_few_rows(rows, wide):
+    """Rows of every length up to the whole width that change places: a block
+    that read a length after it was replaced would keep, drop or count columns
+    of another row. Shared and lone pages; rows that end, and parents and
+    entries that do not exist."""
+    r = np.random.default_rng(rows * 1000 + wide)
+    P = PU.Pages(rows, wide, rows * wide + 9, 16)
+
+    def fill():
+        order = list(r.permutation(P.pool))
+        P.refs[:] = 0
+        for b in range(rows):
+            k = wide if b == rows - 1 else int(r.integers(0, wide + 1))
+            share = min(k, int(P.held[b - 1]), int(r.integers(0, wide + 1))) if b else 0
+            P.table[b] = -7
+            P.table[b, :share] = P.table[b - 1, :share]
+            P.table[b, share:k] = [order.pop() for _ in range(k - share)]
+            P.held[b] = k
+            P.lens[b] = max(0, k * 16 - int(r.integers(0, 40)))
+            for e in P.table[b, :k]:
+                P.refs[e] += 1
+        return P.device(torch, q)
+
+    for parent in (np.arange(rows)[::-1], np.roll(np.arange(rows), 1), r.permutation(rows), r.integers(0, rows, rows), r.integers(-1, rows, rows),
+                   np.full(rows, -1), np.full(rows, rows - 1), r.choice([-2, rows, 2 ** 31 - 1, 0], rows)):
+        rec = fill()
+        do_fork(P, rec, parent.astype(np.int32))
+        do_fork(P, rec, r.integers(0, rows, rows).astype(np.int32))
+        assert (P.counts() == P.refs).all()
+    fill()
+    for e in P.table[0, :P.held[0]]:
+        P.refs[e] -= 1
+    P.table[0, :P.held[0]] = r.choice([-1, P.pool, -2 ** 31], P.held[0])      # entries outside the pool
+    P.lens[rows // 2] = 2 ** 30 + 1                          # and a row that does not fit
+    rec = P.device(torch, q)
+    do_fork(P, rec, np.roll(np.arange(rows), 1).astype(np.int32))
+
+
+@pytest.mark.parametrize("pool", [16383, 16384, 16385])
+def test_pools_at_the_border_between_one_block_and_a_cluster(pool):
+    r = np.random.default_rng(pool)
+    P = PU.random_pages(r, 40, 300, pool, 16, fill=0.5)
+    P.refs[[0, pool - 1]] += 1
+    rec = P.device(torch, q)
+    do_reserve(P, rec, r.choice([0, 1, 17, 160], 40))
+    do_fork(P, rec, r.integers(-1, 40, 40).astype(np.int32))
+    do_reserve(P, rec, r.integers(0, 3, 40))
+    do_compact(P, rec, 100)
+    do_compact(P, rec, pool)
+    free = int((P.refs == 0).sum())
+    P.refs[P.refs == 0] = 1                                  # none is left, and then the last one
+    rec = P.device(torch, q)
+    do_reserve(P, rec, np.full(40, 40))
+    assert free > 1
+    P.refs[pool - 1] = 0
+    one = np.zeros(40, int)
+    one[int(np.argmin(P.held))] = int(P.held.min() * 16 - P.lens[np.argmin(P.held)]) + 1
+    rec = P.device(torch, q)
+    do_reserve(P, rec, one)
+    do_reserve(P, rec, one)
