@@ -718,7 +718,7 @@ qg_status kv_pages_copy(const qg_kv_cache* cache, const qg_kv_moves* moves, cuda
 qg_status beam_select_workspace_size(int lanes, int beams, int vocab, int n_out, size_t* bytes)
 {
     if (!bytes || !beam_sizes(lanes, beams, vocab, n_out)) return QG_ERR_INVALID_ARG;
-    *bytes = beam_select_workspace_bytes(lanes, beams, vocab, n_out);
+    *bytes = beam_select_workspace_bytes(lanes, beams, vocab);
     return QG_OK;
 }
 
@@ -737,7 +737,7 @@ qg_status beam_select(const void* logits, qg_out logits_dtype, int64_t row_strid
     const void* ptrs[] = {logits, scores, finished, out_scores, out_tokens, out_parents, out_finished};
     for (const void* p : ptrs)
         if (!aligned16(p)) return QG_ERR_MISALIGNED;
-    if (!workspace || workspace_bytes < beam_select_workspace_bytes(lanes, beams, vocab, n_out))
+    if (!workspace || workspace_bytes < beam_select_workspace_bytes(lanes, beams, vocab))
         return QG_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return QG_ERR_MISALIGNED;
     const BeamArgs a{logits, logits_dtype == QG_OUT_F32, row_stride, lanes, beams, vocab, scores, finished, eos, pad,

@@ -547,7 +547,7 @@ cudaError_t launch(const BeamArgs& a, ScaledSum* sums, cudaStream_t stream)
 
 }  // namespace
 
-size_t beam_select_workspace_bytes(int lanes, int beams, int vocab, int)
+size_t beam_select_workspace_bytes(int lanes, int beams, int vocab)
 {
     return static_cast<size_t>(lanes) * beams * ((vocab + kPiece - 1) / kPiece) * sizeof(ScaledSum) + 256;
 }

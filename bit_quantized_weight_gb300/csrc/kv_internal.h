@@ -81,7 +81,7 @@ struct BeamArgs {
     int* status;
 };
 
-size_t beam_select_workspace_bytes(int lanes, int beams, int vocab, int n_out);
+size_t beam_select_workspace_bytes(int lanes, int beams, int vocab);
 qg_status launch_beam_select(const BeamArgs& a, void* workspace, cudaStream_t stream);
 
 qg_status launch_kv_append(const KvArgs& a, const void* k, int64_t k_stride, const void* v, int64_t v_stride,

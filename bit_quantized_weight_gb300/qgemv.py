@@ -680,7 +680,7 @@ def kv_pages_copy(cache, moves, stream=None):
 
 
 def beam_select_workspace_size(lanes, beams, vocab, n_out) -> int:
-    """Bytes of beam_select's workspace on the current device."""
+    """Bytes of beam_select's workspace."""
     b = ctypes.c_size_t(0)
     _check("beam_select_workspace_size", lib().beam_select_workspace_size(int(lanes), int(beams), int(vocab), int(n_out),
                                                                           ctypes.byref(b)))

@@ -645,16 +645,17 @@ QG_API qg_status kv_pages_copy(const qg_kv_cache* cache, const qg_kv_moves* move
  *               the call, and may be shared by calls that do not overlap on
  *               the GPU
  * Sums of exponentials are held in fp32; scores are compared in 64 bits and
- * rounded once (one below fp32's range becomes -infinity). Rows with equal
- * logits get equal sums whatever their alignment, and the result does not
- * depend on the stream's other work (fixed order).
+ * rounded once (one below fp32's range becomes -infinity): the order is exact
+ * but for candidates of two rows that are closer than these sums are off. Rows
+ * with equal logits get equal sums whatever their alignment, and the result
+ * does not depend on the stream's other work (fixed order).
  */
 QG_API qg_status beam_select(const void* logits, qg_out logits_dtype, int64_t row_stride, int lanes, int beams,
                              int vocab, const float* scores, const uint8_t* finished, int eos, int pad, int n_out,
                              float* out_scores, int32_t* out_tokens, int32_t* out_parents, uint8_t* out_finished,
                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
-/* Bytes of beam_select's workspace on the current device for these sizes. */
+/* Bytes of beam_select's workspace for these sizes. */
 QG_API qg_status beam_select_workspace_size(int lanes, int beams, int vocab, int n_out, size_t* bytes);
 
 /*
