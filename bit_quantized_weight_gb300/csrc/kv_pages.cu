@@ -81,8 +81,9 @@ __device__ __forceinline__ void cluster_sync()
 // other: what it changes by is added up over a warp's four rows first, which
 // for beams that go on from each other is often nothing. Bound by chained
 // loads (lengths, then entries, 32 bytes of a row) and the second launch: 1,024
-// rows of 2,048 entries in 12.6 us (blocks of 32 columns with an atomic for
-// each entry: 50).
+// rows of 2,048 entries in 12.3 us where two of every four rows go on and in
+// 12.5 where the best few of 16 have most children (blocks of 32 columns with
+// an atomic for each entry: 50).
 __global__ void __launch_bounds__(kForkThreads, 2) pages_fork_kernel(const __grid_constant__ PageArgs a, const int32_t* parent)
 {
     extern __shared__ int smem[];
@@ -169,7 +170,9 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_rows_kernel(const __g
 
 // Few rows: one launch, of a cluster whose blocks have all read the lengths
 // before one of them writes any. 8 rows of 257 entries in 2.3 us, 16 in 2.8 (by
-// the two launches above 3.5 and 3.6); for 32 rows both take 3.7.
+// the two launches above 3.5 and 3.6); for 32 rows both take 3.7. Beyond 512
+// columns a block has several runs of them: 8 rows of 1,028 entries 3.0 us (by
+// the two launches 3.6), 16 rows 3.9 (3.7), 8 rows of 2,052 4.4 (3.6).
 __global__ void __launch_bounds__(kFewThreads) pages_fork_few_kernel(const __grid_constant__ PageArgs a, const int32_t* parent)
 {
     __shared__ int par[kFewRows], keep[kFewRows], held[kFewRows], kids[kFewRows], lens[kFewRows];
@@ -356,7 +359,12 @@ struct ReserveSmem {
 // number that each of its free pages has among all, and so the row and the
 // column that each is for. Nothing is written before every block has read.
 // Bound by chained loads and barriers (a row's length, last entry and count of
-// that page; two scans; the cluster's sum): 8 rows of a step in 4.5 us.
+// that page; two scans; the cluster's sum): 8 rows of a step in 5.3 us, 10.2 for
+// 64 rows and 21,000 pages of a pool of 100,000. Of some 18,000 cycles of the
+// latter the pool's bits and the rows take 4,800, the scans 2,200, the cluster's
+// barrier 1,400, its blocks' counts, read one after another, 3,100, and the
+// pages handed out 6,300. 32 pages held ahead by each row cost 1.9 us: a row's
+// thread looks at one after another.
 __global__ void __launch_bounds__(kPlanThreads, 1) pages_reserve_kernel(const __grid_constant__ PageArgs a, const int32_t* n_new,
                                                                      const MoveArgs m, int32_t* n_free)
 {
@@ -516,9 +524,12 @@ struct CompactSmem {
 // One cluster. Of L pages in use, those at L and above move into the free
 // places below L: as many of one as of the other. With S(p) pages in use below
 // page p, a free one below L is hole number p - S(p), and one in use from L on
-// is number L - 1 - S(p) of those that move, counted from the highest. Bound by
-// the cluster's few SMs: 46,000 pages in use of 92,000, half of them moved, in 14
-// us with the table.
+// is number L - 1 - S(p) of those that move, counted from the highest: 46,000
+// pages in use of 92,000, half of them moved, in 14.5 us with the table. Of some
+// 22,000 cycles before the table, bits and scan take 2,800, the first barrier
+// 1,700, the blocks' counts, read one after another, twice 3,100, the map and
+// the list with the barrier that waits for them 8,500, and the moves 1,100 to
+// 3,000.
 __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const __grid_constant__ PageArgs a, const MoveArgs m,
                                                                      int32_t* page_map, int32_t* n_live)
 {
