@@ -359,7 +359,7 @@ struct ReserveSmem {
 // number that each of its free pages has among all, and so the row and the
 // column that each is for. Nothing is written before every block has read.
 // Bound by chained loads and barriers (a row's length, last entry and count of
-// that page; two scans; the cluster's sum): 8 rows of a step in 5.3 us, 10.2 for
+// that page; two scans; the cluster's sum): 8 rows of a step in 5.0 us, 10.2 for
 // 64 rows and 21,000 pages of a pool of 100,000. Of some 18,000 cycles of the
 // latter the pool's bits and the rows take 4,800, the scans 2,200, the cluster's
 // barrier 1,400, its blocks' counts, read one after another, 3,100, and the

@@ -663,7 +663,8 @@ QG_API qg_status beam_select_workspace_size(int lanes, int beams, int vocab, int
  * QG_OK, QG_ERR_DEVICE_TIMEOUT when a bounded device-side wait gave up (the
  * kernel stopped early; its outputs are undefined), or QG_ERR_INVALID_ARG for
  * out-of-range device data (MoE expert ids, a cache batch's lengths, pages and
- * paths, page records and moves) or logits that have no sum.
+ * paths, page records and moves), a kv_pages_reserve without n_free that found
+ * too few pages, or logits that have no sum.
  */
 QG_API qg_status qg_last_device_status(cudaStream_t stream);
 
